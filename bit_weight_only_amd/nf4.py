@@ -22,9 +22,33 @@ EXPORTS = ("nf4_status_string", "nf4_codebook", "nf4_qweight_bytes", "nf4_absmax
            "nf4_gemv_argmax_workspace_bytes", "nf4_gemv_argmax", "nf4_gemv_argmax_noalloc",
            "nf4_gemv_prefetch",
            "nf4_awq_params_bytes", "nf4_awq_workspace_bytes", "nf4_awq_pack", "nf4_awq_repack",
-           "nf4_awq_unpack", "nf4_awq_dequant", "nf4_gather_columns", "nf4_awq_gemv_prefetch", "nf4_awq_gemv", "nf4_awq_gemm")
+           "nf4_awq_unpack", "nf4_awq_dequant", "nf4_gather_columns", "nf4_awq_gemv_prefetch", "nf4_awq_gemv", "nf4_awq_gemm",
+           "nf4_kv_code_bytes", "nf4_kv_scale_bytes", "nf4_kv_append",
+           "nf4_kv_attention_workspace_bytes", "nf4_kv_attention", "nf4_kv_copy_pages",
+           "nf4_kv_reserve", "nf4_kv_fork", "nf4_kv_release", "nf4_kv_compact_workspace_bytes",
+           "nf4_kv_compact")
+
+NF4_KV_BF16, NF4_KV_F32 = range(2)
 
 _lib = None
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale")] + \
+               [(f, ctypes.c_int64) for f in ("layers", "pages", "kv_heads", "page_tokens",
+                                              "head_dim")]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in ("seqs", "rows", "max_rows", "max_len")] + \
+               [(f, ctypes.c_void_p) for f in ("row_start", "kv_len", "table")] + \
+               [("table_stride", ctypes.c_int64)]
+
+
+class _KVPool(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("len", ctypes.c_void_p), ("missing", ctypes.c_void_p)]
 
 
 class NF4Error(RuntimeError):
@@ -91,6 +115,27 @@ def lib() -> ctypes.CDLL:
         for f in (L.nf4_awq_gemv, L.nf4_awq_gemm):
             f.restype = st
             f.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp, sz, vp]
+        cache, batch, pool = (ctypes.POINTER(t) for t in (_KVCache, _KVBatch, _KVPool))
+        for f in (L.nf4_kv_code_bytes, L.nf4_kv_scale_bytes, L.nf4_kv_compact_workspace_bytes):
+            f.restype = sz
+            f.argtypes = [cache]
+        L.nf4_kv_append.restype = st
+        L.nf4_kv_append.argtypes = [cache, i64, batch, vp, i64, vp, i64, st, vp]
+        L.nf4_kv_attention_workspace_bytes.restype = sz
+        L.nf4_kv_attention_workspace_bytes.argtypes = [cache, batch, i64, i64, i64]
+        L.nf4_kv_attention.restype = st
+        L.nf4_kv_attention.argtypes = [cache, i64, batch, vp, i64, i64, ctypes.c_float, i64, i64,
+                                       vp, vp, vp, sz, vp]
+        L.nf4_kv_copy_pages.restype = st
+        L.nf4_kv_copy_pages.argtypes = [cache, vp, vp, i64, vp]
+        L.nf4_kv_reserve.restype = st
+        L.nf4_kv_reserve.argtypes = [cache, pool, vp, vp]
+        L.nf4_kv_fork.restype = st
+        L.nf4_kv_fork.argtypes = [cache, pool, vp, vp, i64, vp]
+        L.nf4_kv_release.restype = st
+        L.nf4_kv_release.argtypes = [cache, pool, vp, i64, vp]
+        L.nf4_kv_compact.restype = st
+        L.nf4_kv_compact.argtypes = [cache, pool, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -262,6 +307,63 @@ def nf4_awq_gemm(x, M: int, qweight, params, N: int, K: int, y, workspace=None,
                               _ptr(workspace), ws_bytes, _stream(stream)), "nf4_awq_gemm")
 
 
+def nf4_kv_code_bytes(cache) -> int:
+    return lib().nf4_kv_code_bytes(cache.arg)
+
+
+def nf4_kv_scale_bytes(cache) -> int:
+    return lib().nf4_kv_scale_bytes(cache.arg)
+
+
+def nf4_kv_append(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, type: int,
+                  stream=None) -> None:
+    _check(lib().nf4_kv_append(cache.arg, layer, batch.arg, _ptr(k), k_stride, _ptr(v), v_stride,
+                               type, _stream(stream)), "nf4_kv_append")
+
+
+def nf4_kv_attention_workspace_bytes(cache, batch, heads: int, window: int = 0,
+                                     sinks: int = 0) -> int:
+    return lib().nf4_kv_attention_workspace_bytes(cache.arg, batch.arg, heads, window, sinks)
+
+
+def nf4_kv_attention(cache, layer: int, batch, q, q_stride: int, heads: int, scale: float,
+                     window: int, sinks: int, out, lse=None, workspace=None, ws_bytes: int = 0,
+                     stream=None) -> None:
+    _check(lib().nf4_kv_attention(cache.arg, layer, batch.arg, _ptr(q), q_stride, heads, scale,
+                                  window, sinks, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                                  _stream(stream)), "nf4_kv_attention")
+
+
+def nf4_kv_copy_pages(cache, src, dst, n: int, stream=None) -> None:
+    _check(lib().nf4_kv_copy_pages(cache.arg, _ptr(src), _ptr(dst), n, _stream(stream)),
+           "nf4_kv_copy_pages")
+
+
+def nf4_kv_reserve(cache, pool, add, stream=None) -> None:
+    _check(lib().nf4_kv_reserve(cache.arg, pool.arg, _ptr(add), _stream(stream)),
+           "nf4_kv_reserve")
+
+
+def nf4_kv_fork(cache, pool, src, dst, n: int, stream=None) -> None:
+    _check(lib().nf4_kv_fork(cache.arg, pool.arg, _ptr(src), _ptr(dst), n, _stream(stream)),
+           "nf4_kv_fork")
+
+
+def nf4_kv_release(cache, pool, rows, n: int, stream=None) -> None:
+    _check(lib().nf4_kv_release(cache.arg, pool.arg, _ptr(rows), n, _stream(stream)),
+           "nf4_kv_release")
+
+
+def nf4_kv_compact_workspace_bytes(cache) -> int:
+    return lib().nf4_kv_compact_workspace_bytes(cache.arg)
+
+
+def nf4_kv_compact(cache, pool, refs_out, table_out, workspace, ws_bytes: int,
+                   stream=None) -> None:
+    _check(lib().nf4_kv_compact(cache.arg, pool.arg, _ptr(refs_out), _ptr(table_out),
+                                _ptr(workspace), ws_bytes, _stream(stream)), "nf4_kv_compact")
+
+
 # ------------------------------------------------------------ conveniences
 class PackedWeight:
     """Device-layout codes and scales of one N x K weight (torch uint8/fp32)."""
@@ -328,3 +430,74 @@ def awq_pack_weight(W, stream=None) -> AwqWeight:
     aw = AwqWeight(N, K, device=W.device)
     nf4_awq_pack(W, N, K, aw.qweight, aw.params, stream)
     return aw
+
+
+class KVCache:
+    """A key-value cache's tensors (allocated zero-filled here, or given) and
+    the structure that names them to the library."""
+
+    def __init__(self, layers: int, pages: int, kv_heads: int, page_tokens: int, head_dim: int,
+                 device="cuda", k=None, v=None, k_scale=None, v_scale=None):
+        self.struct = _KVCache(None, None, None, None, layers, pages, kv_heads, page_tokens,
+                               head_dim)
+        self.arg = ctypes.pointer(self.struct)
+        codes, scales = nf4_kv_code_bytes(self), nf4_kv_scale_bytes(self)
+        if codes == 0:
+            raise NF4Error(NF4_ERR_SHAPE, "KVCache")
+        for name, size, given, width in (("k", codes, k, 1), ("v", codes, v, 1),
+                                         ("k_scale", scales, k_scale, 4),
+                                         ("v_scale", scales, v_scale, 4)):
+            if given is None:
+                import torch
+                lead = (layers, pages, kv_heads)
+                if width == 4:
+                    given = torch.zeros(lead + (page_tokens // 16,), dtype=torch.float32,
+                                        device=device)
+                else:
+                    shape = (page_tokens, head_dim) if name == "k" else \
+                        (page_tokens // 4, head_dim, 4)
+                    given = torch.zeros(lead + shape, dtype=torch.uint8, device=device)
+            elif given.numel() * given.element_size() != size or not given.is_contiguous():
+                raise NF4Error(NF4_ERR_SHAPE, "KVCache")
+            setattr(self, name, given)
+            setattr(self.struct, name, given.data_ptr())
+
+
+class KVBatch:
+    """The new rows of a step: int32 device tensors kv_len [seqs] and table
+    [seqs][entries], row_start [seqs + 1] where sequences have other than one
+    row each, and the host's bounds on rows and lengths."""
+
+    def __init__(self, kv_len, table, row_start=None, rows=None, max_rows: int = 1, max_len=None):
+        seqs = kv_len.numel()
+        if table.dim() != 2 or table.stride(1) != 1 or table.shape[0] < seqs or \
+                (row_start is not None and row_start.numel() != seqs + 1):
+            raise NF4Error(NF4_ERR_SHAPE, "KVBatch")
+        self.kv_len, self.table, self.row_start = _int32(kv_len), table, row_start
+        _int32(table[:1])
+        self.struct = _KVBatch(seqs, seqs if rows is None else rows, max_rows,
+                               (1 << 30) if max_len is None else max_len,
+                               None if row_start is None else _int32(row_start).data_ptr(),
+                               kv_len.data_ptr(), table.data_ptr(), table.stride(0))
+        self.arg = ctypes.pointer(self.struct)
+
+
+class KVPool:
+    """Who owns which page: int32 device tensors refs [pages], table
+    [rows][entries], length [rows] and, if wanted, missing [1]."""
+
+    def __init__(self, refs, table, length, missing=None):
+        if table.dim() != 2 or length.numel() != table.shape[0]:
+            raise NF4Error(NF4_ERR_SHAPE, "KVPool")
+        self.refs, self.table, self.length, self.missing = refs, table, length, missing
+        self.struct = _KVPool(_int32(refs).data_ptr(), _int32(table).data_ptr(), *table.shape,
+                              _int32(length).data_ptr(),
+                              None if missing is None else _int32(missing).data_ptr())
+        self.arg = ctypes.pointer(self.struct)
+
+
+def _int32(t):
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise NF4Error(NF4_ERR_SHAPE, "int32 tensor")
+    return t

@@ -354,6 +354,176 @@ nf4_status nf4_awq_gemm(const hip_bfloat16 *x, int64_t M, const uint8_t *qweight
                         const uint32_t *params, int64_t N, int64_t K, float *y, void *workspace,
                         size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Key-value cache in 8 bits, the attention that reads it, and the pool its
+ * pages come from: what stands between the q|k|v projection and the output
+ * projection of a decoder layer (vibevoice.c README: the KV cache bounds how
+ * long a recording fits, so it can be kept in FP8 and in pages shared by the
+ * slots).
+ *
+ * A page holds page_tokens consecutive tokens of one sequence, for every
+ * layer and kv head.  A block is 16 consecutive tokens of one head in a page,
+ * aligned to 16, keys or values: its codes are e4m3 values (4 exponent bits,
+ * bias 7, 3 mantissa bits, largest 448, code 0x7F or 0xFF is NaN) under one
+ * fp32 scale, a power of two 2^e with -40 <= e <= 100.  An element reads back
+ * as code * scale, exactly.
+ *
+ *   k       [layers][pages][kv_heads][page_tokens][head_dim]           bytes
+ *   v       [layers][pages][kv_heads][page_tokens / 4][head_dim][4]    bytes
+ *   scales  [layers][pages][kv_heads][page_tokens / 16]  floats, one array each
+ *
+ * The keys lie as rows and the values as quads of tokens, so that 16 or 32
+ * consecutive bytes of either are one lane's operand of the matrix
+ * instruction that reads them.
+ *
+ * Sequences name their pages in a table, int32 [..][table_stride]: token t of
+ * sequence s lies in page table[s][t / page_tokens].  An entry outside
+ * [0, pages) is a hole: tokens there are not written and never seen.
+ *
+ * Every array named in the three structures below is device memory; the
+ * structures are host memory, read during the call.  int32 arrays need
+ * 4-byte alignment, all else 16.
+ * ------------------------------------------------------------------------ */
+
+typedef struct nf4_kv_cache {
+  uint8_t *k, *v;          /* codes, nf4_kv_code_bytes() each */
+  float *k_scale, *v_scale; /* nf4_kv_scale_bytes() each */
+  int64_t layers, pages;   /* >= 1; pages <= 2^24 */
+  int64_t kv_heads;        /* 1 .. 1024 */
+  int64_t page_tokens;     /* 16, 32, 64, 128 or 256 */
+  int64_t head_dim;        /* 64 or 128 */
+} nf4_kv_cache;
+
+/* The new rows of a step.  Rows row_start[s] .. row_start[s + 1] - 1 are the
+ * last tokens of sequence s, so row row_start[s] + i stands at position
+ * kv_len[s] - (row_start[s + 1] - row_start[s]) + i.  A sequence may have no
+ * rows, and rows whose position would be negative are no tokens.  max_rows
+ * and max_len bound what any sequence has, as the host knows it: rows past
+ * max_rows are not processed, lengths past max_len (or past the table) count
+ * as that. */
+typedef struct nf4_kv_batch {
+  int64_t seqs, rows;        /* >= 1; rows of all sequences together */
+  int64_t max_rows, max_len; /* 1 .. rows; 0 .. 2^30 */
+  const int32_t *row_start;  /* [seqs + 1]; NULL: one row each (rows == seqs) */
+  const int32_t *kv_len;     /* [seqs] tokens, the new ones included */
+  const int32_t *table;      /* [seqs][table_stride] */
+  int64_t table_stride;      /* >= 1 */
+} nf4_kv_batch;
+
+/* Who owns which page.  refs[p] counts the table entries that name page p; 0
+ * is free. */
+typedef struct nf4_kv_pool {
+  int32_t *refs;   /* [pages], 16-byte aligned */
+  int32_t *table;  /* [table_rows][table_stride] */
+  int64_t table_rows, table_stride;
+  int32_t *len;    /* [table_rows] tokens of each row */
+  int32_t *missing; /* [1], or NULL: see nf4_kv_fork and nf4_kv_reserve */
+} nf4_kv_pool;
+
+typedef enum nf4_kv_type { NF4_KV_BF16 = 0, NF4_KV_F32 = 1 } nf4_kv_type;
+
+/* Bytes of the k (and of the v) codes, and of each scale array; 0 for a cache
+ * that the library rejects.  The pointers are not looked at. */
+size_t nf4_kv_code_bytes(const nf4_kv_cache *cache);
+size_t nf4_kv_scale_bytes(const nf4_kv_cache *cache);
+
+/* Quantize the new rows of k and v into their pages of one layer.  k, v: rows
+ * of kv_heads * head_dim values, k_stride and v_stride elements apart (at
+ * least kv_heads * head_dim; a multiple of 16 bytes), bfloat16 or fp32, so
+ * that slices of a fused q|k|v projection's rows are taken as they are.
+ *
+ * Per block the scale is 2^e with the least e for which the largest finite
+ * magnitude of its new tokens is at most 448 * 2^e, no less than the
+ * exponent the block had if it already holds earlier tokens of the sequence,
+ * and at least -40 and at most 100.  A new token's codes are x / 2^e to the
+ * nearest e4m3 value, ties to even, infinities and what lies past
+ * 448 * 2^100 as +-448, NaN as NaN.  Where e grew, the block's earlier codes
+ * are rounded to the new scale in the same way (exact unless they become
+ * subnormal).  Codes past the sequence's last token are left as they are.
+ *
+ * Pages that two sequences share must not be written: see nf4_kv_fork.
+ * Errors: NF4_ERR_NULL, NF4_ERR_SHAPE (also for a layer outside the cache and
+ * an unknown type), NF4_ERR_ALIGN. */
+nf4_status nf4_kv_append(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch,
+                         const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         nf4_kv_type type, hipStream_t stream);
+
+/* Bytes of workspace nf4_kv_attention needs for a call with these arguments
+ * on the current device (the arrays of the structures are not looked at); 0
+ * when it needs none or rejects the call. */
+size_t nf4_kv_attention_workspace_bytes(const nf4_kv_cache *cache, const nf4_kv_batch *batch,
+                                        int64_t heads, int64_t window, int64_t sinks);
+
+/* Causal attention of the batch's rows over one layer of the cache, prompts
+ * and single tokens alike.  q: bfloat16 rows of heads * head_dim values,
+ * q_stride elements apart (a multiple of 8); heads is a multiple of
+ * kv_heads, and query head h reads kv head h / (heads / kv_heads).  A row at
+ * position p sees the tokens j <= p with window == 0, or j > p - window, or
+ * j < sinks (a sliding window and the first tokens that stay visible).  With
+ * s_j = scale * q . k_j over those: out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ * lse = log sum_j exp(s_j); a row that sees nothing gets zeros and -inf.
+ * What a row does not see never reaches it, NaN and infinities included.
+ *
+ * out: bfloat16 [rows][heads * head_dim].  lse: fp32 [rows][heads], or NULL.
+ * Rows that are no tokens (a negative position) see nothing.  Products are
+ * bf16 x bf16 (a code is exact in bf16) with fp32 sums; the weights exp(s -
+ * max) are rounded to bf16 for the second product, like q for the first, and
+ * the sum they are divided by is of the unrounded ones.  Bitwise reproducible
+ * run to run for a given device.
+ *
+ * workspace: nf4_kv_attention_workspace_bytes bytes, any contents (NULL when
+ * that is 0); calls sharing one must be ordered.  scale must be finite and
+ * positive, window and sinks >= 0 (else NF4_ERR_SHAPE).  Other errors:
+ * NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_WORKSPACE. */
+nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch,
+                            const hip_bfloat16 *q, int64_t q_stride, int64_t heads, float scale,
+                            int64_t window, int64_t sinks, hip_bfloat16 *out, float *lse,
+                            void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Copy page src[i] to page dst[i], every layer, codes and scales, for i < n
+ * (device int32[n] each).  Pairs with a page outside the cache are skipped; no
+ * dst may be another pair's src or dst. */
+nf4_status nf4_kv_copy_pages(const nf4_kv_cache *cache, const int32_t *src, const int32_t *dst,
+                             int64_t n, hipStream_t stream);
+
+/* Give every table row r room for add[r] more tokens (device
+ * int32[table_rows]; less than 1 leaves the row alone): len[r] += add[r], and
+ * the entries from ceil(len / page_tokens) up to the new one get free pages,
+ * the lowest page ids first, in order of rows and tokens.  Pages that the
+ * pool or the table has no room for are counted in *missing (0 if there was
+ * room for all) and leave holes.  Only pages, page_tokens and the like of
+ * the cache are used. */
+nf4_status nf4_kv_reserve(const nf4_kv_cache *cache, const nf4_kv_pool *pool, const int32_t *add,
+                          hipStream_t stream);
+
+/* Row dst[i] continues as row src[i] (device int32[n] each), for i < n: it
+ * gets its length, shares its whole pages, and gets a copy of a page that is
+ * full in part (the lowest free pages, in order of i), every layer, so that
+ * both rows can then be appended to.  dst rows must be empty before
+ * (released), differ from each other and be no pair's src.  *missing counts
+ * the copies for which no page was free; they leave holes.  Pairs with a row
+ * outside the table are skipped. */
+nf4_status nf4_kv_fork(const nf4_kv_cache *cache, const nf4_kv_pool *pool, const int32_t *src,
+                       const int32_t *dst, int64_t n, hipStream_t stream);
+
+/* Rows rows[i] (device int32[n]) give up their pages: entries -1, len 0, a
+ * page is free when no row names it any more. */
+nf4_status nf4_kv_release(const nf4_kv_cache *cache, const nf4_kv_pool *pool, const int32_t *rows,
+                          int64_t n, hipStream_t stream);
+
+/* Bytes of workspace nf4_kv_compact needs. */
+size_t nf4_kv_compact_workspace_bytes(const nf4_kv_cache *cache);
+
+/* Move the live pages to the front of the pool: with n pages in use, the j-th
+ * page in use at or past n is copied (every layer) to the j-th free page
+ * before n.  refs_out (int32[pages]) and table_out (as the pool's table) get
+ * the counts and entries after that, holes as -1; each may be the pool's own
+ * array.  The moved pages' old places keep their contents until they are
+ * used again.  workspace: any contents. */
+nf4_status nf4_kv_compact(const nf4_kv_cache *cache, const nf4_kv_pool *pool, int32_t *refs_out,
+                          int32_t *table_out, void *workspace, size_t ws_bytes,
+                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
