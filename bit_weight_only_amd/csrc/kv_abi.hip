@@ -50,19 +50,21 @@ bool batch_shape_ok(const nf4_kv_batch &b) {
   return b.table_stride >= 1 && b.table_stride <= kMaxLen;
 }
 
-nf4::KvBatch as_batch(const nf4_kv_batch &b) {
-  return nf4::KvBatch{b.seqs,      b.rows,   (int)b.max_rows, (int)b.max_len,
-                      b.row_start, b.kv_len, b.table,         b.table_stride};
+// No sequence is longer than the table: a large max_len costs no launch size.
+nf4::KvBatch as_batch(const nf4_kv_batch &b, const nf4::KvCache &c) {
+  const int64_t room = b.table_stride << c.page_shift;
+  return nf4::KvBatch{b.seqs, b.rows, (int)b.max_rows, (int)(b.max_len < room ? b.max_len : room),
+                      b.row_start, b.kv_len, b.table, b.table_stride};
 }
 
-nf4_status check_batch(const nf4_kv_batch *b, nf4::KvBatch &out) {
+nf4_status check_batch(const nf4_kv_batch *b, const nf4::KvCache &c, nf4::KvBatch &out) {
   if (!b || !b->kv_len || !b->table) return NF4_ERR_NULL;
   if (!batch_shape_ok(*b)) return NF4_ERR_SHAPE;
   // without row_start every sequence has one row
   if (!b->row_start && (b->rows != b->seqs || b->max_rows != 1)) return NF4_ERR_NULL;
   if (!aligned(b->row_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->table, 4))
     return NF4_ERR_ALIGN;
-  out = as_batch(*b);
+  out = as_batch(*b, c);
   return NF4_OK;
 }
 
@@ -114,7 +116,7 @@ nf4_status nf4_kv_append(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_
   if (!k || !v) return NF4_ERR_NULL;
   nf4_status st = check_cache(cache, c);
   if (st != NF4_OK) return st;
-  if ((st = check_batch(batch, b)) != NF4_OK) return st;
+  if ((st = check_batch(batch, c, b)) != NF4_OK) return st;
   if (layer < 0 || layer >= c.layers) return NF4_ERR_SHAPE;
   if (type != NF4_KV_BF16 && type != NF4_KV_F32) return NF4_ERR_SHAPE;
   const int64_t width = (int64_t)c.kv_heads * c.head_dim, unit = type == NF4_KV_F32 ? 4 : 8;
@@ -131,7 +133,7 @@ size_t nf4_kv_attention_workspace_bytes(const nf4_kv_cache *cache, const nf4_kv_
   nf4::KvCache c;
   if (!cache || !batch || !shape_ok(*cache, c) || !batch_shape_ok(*batch)) return 0;
   if (!attention_shape_ok(c, batch->rows, heads, window, sinks)) return 0;
-  return nf4::kv_attention_workspace_bytes(c, as_batch(*batch), (int)heads, held(window),
+  return nf4::kv_attention_workspace_bytes(c, as_batch(*batch, c), (int)heads, held(window),
                                            held(sinks));
 }
 
@@ -144,7 +146,7 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_
   if (!q || !out) return NF4_ERR_NULL;
   nf4_status st = check_cache(cache, c);
   if (st != NF4_OK) return st;
-  if ((st = check_batch(batch, b)) != NF4_OK) return st;
+  if ((st = check_batch(batch, c, b)) != NF4_OK) return st;
   if (layer < 0 || layer >= c.layers) return NF4_ERR_SHAPE;
   if (!attention_shape_ok(c, b.rows, heads, window, sinks)) return NF4_ERR_SHAPE;
   if (!isfinite(scale) || !(scale > 0.0f)) return NF4_ERR_SHAPE;

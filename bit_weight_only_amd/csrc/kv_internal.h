@@ -61,6 +61,9 @@ struct KvPool {
   int32_t *len, *missing;
 };
 
+// Compute units of the current device (queried once per device).
+int device_cu_count();
+
 hipError_t launch_kv_append(const KvCache &c, int64_t layer, const KvBatch &b, const void *k,
                             int64_t k_stride, const void *v, int64_t v_stride, bool f32,
                             hipStream_t s);

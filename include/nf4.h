@@ -471,8 +471,8 @@ size_t nf4_kv_attention_workspace_bytes(const nf4_kv_cache *cache, const nf4_kv_
  * the sum they are divided by is of the unrounded ones.  Bitwise reproducible
  * run to run for a given device.
  *
- * workspace: nf4_kv_attention_workspace_bytes bytes, any contents (NULL when
- * that is 0); calls sharing one must be ordered.  scale must be finite and
+ * workspace: at least nf4_kv_attention_workspace_bytes bytes, any contents
+ * (NULL when that is 0); calls sharing one must be ordered.  scale must be finite and
  * positive, window and sinks >= 0 (else NF4_ERR_SHAPE).  Other errors:
  * NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_WORKSPACE. */
 nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch,
