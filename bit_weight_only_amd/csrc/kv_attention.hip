@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "kv_internal.h"
+#include "nf4_internal.h"
 
 namespace nf4 {
 namespace {
@@ -26,6 +27,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -52,8 +54,19 @@ __device__ inline uint32_t nan_bytes(uint32_t w) {
 __device__ inline uint32_t nan_ones(uint32_t w) { return (nan_bytes(w) >> 7) * 0x38u; }
 __device__ inline uint32_t without_nan(uint32_t w) { return w & ~((nan_bytes(w) >> 7) * 0xFFu); }
 
-__device__ inline f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The largest of three, NaN left out.  (fmaxf first quiets its arguments, an
+// instruction each.)
+__device__ inline float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
 }
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -64,12 +77,26 @@ __device__ inline int kv_scale_exponent(float s) {
   return e < kKvExpMin ? kKvExpMin : e > kKvExpMax ? kKvExpMax : e;
 }
 
+// A lane's value as a scalar.
+__device__ inline float lane_float(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
 // The keys of one row: up to its position, inside the window or among the
 // first tokens.
 struct Visible {
   int window, sinks;
   __device__ bool operator()(int key, int pos) const {
     return (key <= pos) & ((window == 0) | (key > pos - window) | (key < sinks));
+  }
+  // Bit x: whether the row sees key + x, x = 0 .. 63.
+  __device__ uint64_t bits(int key, int pos) const {
+    auto upto = [](int t) {  // bits 0 .. t
+      return t < 0 ? 0ull : t >= 63 ? ~0ull : ~0ull >> (63 - t);
+    };
+    uint64_t b = upto(pos - key);
+    if (window > 0) b &= ~upto(pos - window - key) | upto(sinks - 1 - key);
+    return b;
   }
   // Whether every row at p_lo .. p_hi sees all of key .. key + n - 1.
   __device__ bool all(int key, int n, int p_lo, int p_hi) const {
@@ -159,14 +186,17 @@ __device__ inline void store_row(const KvCache &c, const KvAttention &a, const T
   if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// NaN codes in places that some row does not see would reach it as 0 * NaN.
-// They become 0 here, and a product of their places with the visible ones
-// makes the sums NaN where that is due.
-template <int DT>
-__device__ inline void hide_nan(uint32_t (&vw)[2][DT], uint32_t see, f32x4 (&o)[DT]) {
+// NaN codes in places that some row does not see would reach it as 0 * NaN, so
+// steps that some row does not see whole take them as 0 (without_nan), and a
+// product of their places with the visible ones (bits of `see`, keys as in the
+// weights) makes the sums NaN where that is due.
+template <int DT, class Sums>
+__device__ inline void spread_nan(const uint32_t (&va)[DT], const uint32_t (&vc)[DT], uint32_t see,
+                                  Sums (&o)[DT]) {
+  constexpr int N = sizeof(Sums) / sizeof(float);
   uint32_t nan = 0;
 #pragma unroll
-  for (int t = 0; t < DT; ++t) nan |= nan_bytes(vw[0][t]) | nan_bytes(vw[1][t]);
+  for (int t = 0; t < DT; ++t) nan |= nan_bytes(va[t]) | nan_bytes(vc[t]);
   if (!__any(nan != 0)) return;
   union {
     bf16x8 v;
@@ -176,13 +206,11 @@ __device__ inline void hide_nan(uint32_t (&vw)[2][DT], uint32_t see, f32x4 (&o)[
   for (int e = 0; e < 8; ++e) ones.e[e] = (__bf16)(see >> e & 1 ? 1.0f : 0.0f);
 #pragma unroll
   for (int t = 0; t < DT; ++t) {
-    const f32x4 hit =
-        mfma16(widen(nan_ones(vw[0][t]), nan_ones(vw[1][t])), ones.v, f32x4{0, 0, 0, 0});
+    const Sums hit = mfma(widen(nan_ones(va[t]), nan_ones(vc[t])), ones.v, Sums{});
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < N; ++e)
       if (hit[e] > 0.0f) o[t][e] = NAN;
-    vw[0][t] = without_nan(vw[0][t]);
-    vw[1][t] = without_nan(vw[1][t]);
+    __builtin_amdgcn_sched_barrier(0);  // one at a time: registers
   }
 }
 
@@ -201,13 +229,10 @@ struct Step {
   uint4 k[2][D / 64], v[2][D / 64];
 };
 
-__device__ inline float lane_float(float v, int lane) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-
 template <int D, int W>
 __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer, KvBatch b,
-                                                        KvAttention a, int tiles, int max_splits,
+                                                        KvAttention a, uint32_t tiles,
+                                                        int max_splits,
                                                         int split_steps) {
   constexpr int KS = D / 32;   // k-steps of the first product
   constexpr int DT = D / 16;   // tiles of 16 values of the second
@@ -224,9 +249,9 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   w /= (uint32_t)c.kv_heads;
   const int split = w % (uint32_t)max_splits;
   w /= (uint32_t)max_splits;
-  const int64_t seq = w / (uint32_t)tiles;
+  const int64_t seq = w / tiles;
   const uint32_t item = w * (uint32_t)c.kv_heads + head;
-  const Tile tl(c, b, a, seq, w % (uint32_t)tiles, 16);
+  const Tile tl(c, b, a, seq, w % tiles, 16);
   if (tl.empty()) return;
   const Steps<32> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
   const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
@@ -309,7 +334,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     for (int h = 0; h < 2; ++h) {
       s[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < KS; ++j) s[h] = mfma16(widen(kw[h][2 * j], kw[h][2 * j + 1]), q[j], s[h]);
+      for (int j = 0; j < KS; ++j) s[h] = mfma(widen(kw[h][2 * j], kw[h][2 * j + 1]), q[j], s[h]);
       const float kc = lane_float(kc_l, 2 * sl + h);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[h][e] *= kc;
@@ -362,9 +387,16 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
       }
       l += sum * lane_float(vi_l, 2 * sl + h);
     }
-    if (masked) hide_nan<DT>(vw, see, o);  // the same for every lane
+    if (masked) {  // the same for every lane
+      spread_nan<DT>(vw[0], vw[1], see, o);
 #pragma unroll
-    for (int t = 0; t < DT; ++t) o[t] = mfma16(widen(vw[0][t], vw[1][t]), p.v, o[t]);
+      for (int t = 0; t < DT; ++t) {
+        vw[0][t] = without_nan(vw[0][t]);
+        vw[1][t] = without_nan(vw[1][t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[t] = mfma(widen(vw[0][t], vw[1][t]), p.v, o[t]);
   };
 
   // the loads of a step go out before the work on the step before it
@@ -434,65 +466,389 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   }
 }
 
-// Joins the parts of a row, one workgroup per (item, row): 256 threads take
-// four neighbouring values each and turns over the parts, in a fixed order.
+// ---------------------------------------------------------------------------
+// Many rows: one workgroup of 4 waves per (128 rows of a kv head, part of the
+// keys), 32 rows a wave.  64 keys and values at a time are copied to LDS as
+// they lie in memory, two steps ahead, each wave one block of 16; every wave
+// widens what it reads.  Lane l owns row l % 32; with h = l / 32 it holds keys
+// 8a + 4h + e of each 32 (a, e = 0 .. 3), element 4a + e of a product.
+//
+// Bound by the vector unit: per 32 rows and 64 keys (D = 128) the products
+// take 32 matrix instructions of 32 cycles, and widening the codes 128 vector
+// instructions, the softmax some 130 and 32 exponentials, 4 and 8 cycles each.
+constexpr int kTileKeys = 64;
+constexpr int kTileWaves = 4;
+constexpr int kTileRows = 32 * kTileWaves;
+constexpr int kStages = 3;
+
+template <int D>
+struct TileLds {
+  static constexpr int kV = kTileKeys * D;              // values, after the keys
+  static constexpr int kS = 2 * kTileKeys * D;          // scales: 4 of keys, 4 of values
+  static constexpr int kStage = kS + 64;
+  static constexpr int kClean = kStages * kStage;       // values of a step without their NaN
+  static constexpr int kBytes = kClean + kTileKeys * D;
+  static constexpr int kCopies = 2 * (D / 64) + 2;      // per wave and stage
+};
+
+template <int D>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int64_t layer,
+                                                                  KvBatch b, KvAttention a,
+                                                                  uint32_t tiles, int max_splits,
+                                                                  int split_steps) {
+  using L = TileLds<D>;
+  constexpr int DT = D / 32;   // tiles of 32 values
+  constexpr int CH = D / 16;   // 16-byte pieces of a key
+  __shared__ __align__(16) uint8_t lds[L::kBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, h = lane >> 5;
+  // heads first: a kv head's workgroups run on the same dies and find its keys
+  // in their cache; the last rows, which see most, start first
+  uint32_t w = blockIdx.x;
+  const int head = w % (uint32_t)c.kv_heads;
+  w /= (uint32_t)c.kv_heads;
+  const int split = w % (uint32_t)max_splits;
+  w /= (uint32_t)max_splits;
+  const uint32_t seq = w % (uint32_t)b.seqs;
+  const uint32_t tile = tiles - 1 - w / (uint32_t)b.seqs;
+  const Tile tl(c, b, a, seq, tile, kTileRows);
+  if (tl.empty()) return;
+  const Steps<kTileKeys> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
+  const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
+  if (split >= splits) return;
+  const int begin = split * split_steps, n = min(steps.count - begin, split_steps);
+
+  const uint32_t r0 = tl.r0 + 32 * wave;
+  const bool mine = r0 + col < tl.rows, idle = r0 >= tl.rows;
+  const uint32_t r = mine ? r0 + col : tl.rows - 1;
+  const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
+  const int pos = mine ? tl.len - tl.n + tok : -1;
+  const int w_lo = idle ? 0 : tl.len - tl.n + (int)(r0 / tl.group);
+  const int w_hi = idle ? -1 : tl.len - tl.n + (int)(min(r0 + 31, tl.rows - 1) / tl.group);
+
+  // copies of one step: the wave's block of 16 keys and values, and its scales
+  const int32_t *table = b.table + (int64_t)seq * b.table_stride;
+  uint32_t koff[D / 64];  // where in the block the lane's 16 bytes of each copy lie
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    // piece p of key row lies in LDS at piece p ^ (row / 2 % CH): 16 lanes of
+    // a read then hit every bank once
+    const int at = i * 64 + lane, row = at / CH, piece = (at % CH) ^ ((row >> 1) & (CH - 1));
+    koff[i] = row * D + piece * 16;
+  }
+  // lane 4s + i: page of block i of step s of a group of 16, -1 for none
+  auto pages_of = [&](int s0) {
+    const int s = begin + s0 + (lane >> 2);
+    const int t0 = steps.key(s) + 16 * (lane & 3);
+    int page = -1;
+    if (s0 + (lane >> 2) < n && t0 < tl.len) page = table[t0 >> c.page_shift];
+    return page;
+  };
+  int page_l = -1, page_next = pages_of(0);
+  uint64_t hole_mask = 0;
+  uint32_t holes = 0;  // four bits each for the steps that are in LDS or on their way
+  const uint32_t page_bytes = (uint32_t)c.page_bytes();  // at most 2^25
+  const int64_t first = (layer * c.pages * c.kv_heads + head) * ((int64_t)D << c.page_shift);
+  const uint8_t *const k0 = c.k + first, *const v0 = c.v + first;
+  const uint8_t *const ks0 = reinterpret_cast<const uint8_t *>(c.ks) + first / (4 * D);
+  const uint8_t *const vs0 = reinterpret_cast<const uint8_t *>(c.vs) + first / (4 * D);
+  const uint8_t *kb = k0, *vb = v0;
+  uint64_t sb = 0;
+  const uint32_t lds0 = lds_addr(lds);
+  uint32_t to = lds0;  // the stage of the step that is issued
+  auto issue = [&](int s) {
+    if (s < n) {
+      if ((s & 15) == 0) {
+        page_l = page_next >= c.pages ? -1 : page_next;
+        hole_mask = __ballot(page_l < 0);
+        if (s + 16 < n) page_next = pages_of(s + 16);
+      }
+      const int at = 4 * (s & 15);
+      holes |= ((uint32_t)(hole_mask >> at) & 15u) << 8;
+      const int page = __builtin_amdgcn_readlane(page_l, at + wave);
+      const int t0 = steps.key(begin + s) + 16 * wave;
+      const uint64_t off = (uint64_t)(uint32_t)(page < 0 ? 0 : page) * page_bytes +
+                           (uint32_t)((t0 & (c.page_tokens() - 1)) * D);
+      kb = k0 + off;
+      vb = v0 + off;
+      sb = off / (4 * D);
+    }
+    // past the last step: the last again, so that every step has as many
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      copy16_to_lds(to + wave * 16 * D + i * 1024, kb, koff[i]);
+      copy16_to_lds(to + L::kV + wave * 16 * D + i * 1024, vb + i * 1024, lane * 16);
+    }
+    if (lane == 0) {
+      copy4_to_lds(to + L::kS + wave * 4, ks0 + sb, 0);
+      copy4_to_lds(to + L::kS + 16 + wave * 4, vs0 + sb, 0);
+    }
+    to = to == lds0 + (kStages - 1) * L::kStage ? lds0 : to + L::kStage;
+  };
+
+  // the element of key piece 2m + h that step 2m + e of the first product takes
+  // is value 32m + 16h + 8e
+  bf16x8 q[D / 16];
+  const uint16_t *qp = a.q + (tl.row0 + tok) * a.q_stride + (int64_t)qh * D + h * 16;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j)
+    q[j] = *reinterpret_cast<const bf16x8 *>(qp + 32 * (j / 2) + 8 * (j % 2));
+  // waited for here: a wait inside the loop would be for the copies too
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
+
+  const Visible visible{a.window, a.sinks};
+  const float cscale = a.scale * kLog2e;
+  float m = -INFINITY, l[2] = {0.0f, 0.0f};
+  f32x16 o[DT] = {};
+
+  // values 8a + 4h .. of block k: quads h and 2 + h
+  auto values = [&](const uint8_t *vt, int k, uint32_t (&va)[DT], uint32_t (&vc)[DT]) {
+    const uint8_t *vr = vt + k * 16 * D + h * 4 * D + col * (D / 8);
+    __builtin_memcpy(va, __builtin_assume_aligned(vr, D / 8), D / 8);
+    __builtin_memcpy(vc, __builtin_assume_aligned(vr + 8 * D, D / 8), D / 8);
+  };
+  auto compute = [&](const uint8_t *st, int key0, uint32_t hole) {
+    // scales: lane 4k + i holds block i's of keys (k = 0) or values (k = 1)
+    const float sc = reinterpret_cast<const float *>(st + L::kS)[lane & 7];
+    const int ve_l = kv_scale_exponent(sc);
+    const float kc_l = sc * cscale, vi_l = __uint_as_float((uint32_t)(127 - ve_l) << 23);
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u] = f32x16{};
+      const uint8_t *kr = st + (32 * u + col) * D;
+#pragma unroll
+      for (int j = 0; j < CH / 2; ++j) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(
+            kr + (((2 * j + h) ^ ((col >> 1) & (CH - 1))) * 16));
+        s[u] = mfma(widen(k.x, k.y), q[2 * j], s[u]);
+        s[u] = mfma(widen(k.z, k.w), q[2 * j + 1], s[u]);
+      }
+    }
+    const uint8_t *vt = st + L::kV;
+    if (hole != 0 || !visible.all(key0, kTileKeys, w_lo, w_hi)) {
+      uint64_t bits = visible.bits(key0, pos);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (hole >> k & 1) bits &= ~(0xFFFFull << (16 * k));
+      bits >>= 4 * h;
+      // bit 8a + e for element 4a + e of s[u]
+      const uint32_t see[2] = {(uint32_t)bits, (uint32_t)(bits >> 32)};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[u][i] = see[u] >> (8 * (i >> 2) + (i & 3)) & 1 ? s[u][i] : -INFINITY;
+      uint32_t any = 0;
+#pragma unroll 1
+      for (int i = 0; i < kTileKeys * D; i += 1024) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(vt + i + lane * 16);
+        any |= nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w);
+      }
+      if (__any(any != 0)) {
+        // waves that come here in one step write the same bytes; the next
+        // step's barrier is between their last read and the next write
+        uint8_t *clean = lds + L::kClean;
+#pragma unroll 1
+        for (int i = 0; i < kTileKeys * D; i += 1024) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(vt + i + lane * 16);
+          *reinterpret_cast<uint4 *>(clean + i + lane * 16) =
+              make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
+        }
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t va[DT], vc[DT];
+          values(vt, k, va, vc);
+          const uint32_t w = (k >> 1 ? see[1] : see[0]) >> (16 * (k & 1));
+          spread_nan<DT>(va, vc, (w & 15u) | (w >> 4 & 0xF0u), o);
+        }
+        vt = clean;
+      }
+    }
+    float kc[4];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      kc[k] = lane_float(kc_l, k);
+      const auto at = [&](int i) { return s[k >> 1][8 * (k & 1) + i]; };
+      float t = max3(at(0), at(1), at(2));
+      t = max3(t, at(3), at(4));
+      t = max3(t, at(5), at(6));
+      t = max3(t, at(7), at(7));
+      mx = fmaxf(mx, t * kc[k]);  // scales are positive
+    }
+    if (__any(mx > m + 8.0f)) {
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float m_new = fmaxf(m, mx);
+      const float alpha = m_new == -INFINITY ? 1.0f : exp2_fast(m - m_new);
+      m = m_new;
+      l[0] *= alpha;
+      l[1] *= alpha;
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[t] *= alpha;
+    }
+    // (a row that has seen nothing yet has only -inf here, which stays 0)
+    const float base = m == -INFINITY ? 0.0f : m;
+    union {
+      bf16x8 v[4];
+      bf16x2 e[16];
+    } p;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float mk = (float)__builtin_amdgcn_readlane(ve_l, 4 + k) - base;
+      const float inv = lane_float(vi_l, 4 + k);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float x = exp2_fast(fmaf(s[k >> 1][8 * (k & 1) + i], kc[k], mk));
+        const float y = exp2_fast(fmaf(s[k >> 1][8 * (k & 1) + i + 1], kc[k], mk));
+        p.e[4 * k + i / 2][0] = (__bf16)x;
+        p.e[4 * k + i / 2][1] = (__bf16)y;
+        l[0] = fmaf(x, inv, l[0]);
+        l[1] = fmaf(y, inv, l[1]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t va[DT], vc[DT];
+      values(vt, k, va, vc);
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[t] = mfma(widen(va[t], vc[t]), p.v[k], o[t]);
+    }
+  };
+
+  issue(0);
+  holes >>= 4;
+  issue(1);
+  holes >>= 4;  // steps 0 and 1 now have the two low places
+  const uint8_t *st = lds;
+  for (int s = 0; s < n; ++s) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(L::kCopies) : "memory");
+    issue(s + 2);
+    const int key0 = steps.key(begin + s);
+    // rows of this wave that see nothing here leave it out
+    const bool none = key0 > w_hi || (a.window > 0 && key0 + kTileKeys - 1 <= w_lo - a.window &&
+                                      key0 >= a.sinks);
+    if (!none) compute(st, key0, holes & 15u);
+    st = st == lds + (kStages - 1) * L::kStage ? lds : st + L::kStage;
+    holes >>= 4;
+  }
+  // copies into LDS land before the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  float sum = l[0] + l[1];
+  sum += __shfl_xor(sum, 32);
+  // worked out again rather than kept in registers through the loop
+  const int lane2 = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  const int my_col = lane2 & 31, my_h = lane2 >> 5;
+  if (r0 + my_col >= tl.rows) return;
+  // element 4a + e of tile t is value DT (8a + 4h + e) + t
+  if (splits == 1) {
+    const bool none = sum == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / sum;
+    const uint32_t row = r0 + my_col;
+    const int64_t at = (tl.row0 + row / tl.group) * a.heads + head * tl.group + row % tl.group;
+    uint16_t *to = a.out + at * D + my_h * (4 * DT);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t y[2 * DT];
+#pragma unroll
+      for (int x = 0; x < 4 * DT; x += 2) {
+        const float u = o[x % DT][4 * i + x / DT] * inv, v = o[(x + 1) % DT][4 * i + (x + 1) / DT] * inv;
+        y[x / 2] = none ? 0u : bf16_pair(u, v);
+      }
+#pragma unroll
+      for (int x = 0; x < DT / 2; ++x)
+        *reinterpret_cast<uint4 *>(to + i * 8 * DT + 8 * x) =
+            make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
+    }
+    if (a.lse && my_h == 0) a.lse[at] = none ? -INFINITY : (m + __log2f(sum)) * kLn2;
+    return;
+  }
+  const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
+  float *part = static_cast<float *>(a.ws) + (item * max_splits + split) * part_floats(kTileRows, D);
+  const int row = 32 * wave + my_col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int x = 0; x < DT; ++x) {
+      f32x4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = o[(4 * x + e) % DT][4 * i + (4 * x + e) / DT];
+      *reinterpret_cast<f32x4 *>(part + row * D + i * 8 * DT + my_h * 4 * DT + 4 * x) = y;
+    }
+  if (my_h == 0) *reinterpret_cast<float2 *>(part + kTileRows * D + 2 * row) = make_float2(m, sum);
+}
+
+// Joins the parts of rows: 256 threads take four neighbouring values each of
+// 256 / (D / 4) / turns rows, and turns over the parts, in a fixed order.
 // A second launch rather than the last workgroup to arrive: between eight
 // dies, the stores, the count and the loads of that are each a trip to memory
 // one after the other (two sequences of 14449 tokens, 28 heads over 4: 16.3 us
 // that way, 13.6 us with the launch, 9.4 us without either).
 template <int D, int N>
 __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAttention a,
-                                                   uint32_t tiles, int width, int cols,
+                                                   uint32_t tiles, int width, int groups, int turns,
                                                    int max_splits, int split_steps) {
-  constexpr int QUADS = D / 4, TURNS = 256 / QUADS;
+  constexpr int QUADS = D / 4;
   __shared__ f32x4 xs[256];
-  __shared__ float ms[TURNS], ls[TURNS];
-  const int d = (threadIdx.x % QUADS) * 4, turn = threadIdx.x / QUADS;
+  __shared__ float2 mls[256];
+  const int d = (threadIdx.x % QUADS) * 4, t = threadIdx.x / QUADS, turn = t % turns;
+  const int rows = 256 / QUADS / turns;
   uint32_t w = blockIdx.x;
-  const int cc = w % (uint32_t)cols;
-  w /= (uint32_t)cols;
+  const int cc = (w % (uint32_t)groups) * rows + t / turns;
+  w /= (uint32_t)groups;
   const uint32_t item = w;
   const int head = w % (uint32_t)c.kv_heads;
   w /= (uint32_t)c.kv_heads;
   const Tile tl(c, b, a, w / tiles, w % tiles, width);
-  if (tl.r0 + cc >= tl.rows) return;
+  if (tl.empty()) return;
   const Steps<N> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
   if (steps.count <= split_steps) return;  // written already
   const int splits = (steps.count + split_steps - 1) / split_steps;
+  const bool on = cc < width && tl.r0 + cc < tl.rows;
   const float *part = static_cast<const float *>(a.ws) +
                       (int64_t)item * max_splits * part_floats(width, D);
   float mm = -INFINITY, ll = 0.0f;
   f32x4 x = {0, 0, 0, 0};
-  for (int s0 = turn; s0 < splits; s0 += 8 * TURNS) {
+  for (int s0 = turn; on && s0 < splits; s0 += 8 * turns) {
     float2 ml[8];
     f32x4 y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float *from = part + min(s0 + j * TURNS, splits - 1) * part_floats(width, D);
+      const float *from = part + min(s0 + j * turns, splits - 1) * part_floats(width, D);
       ml[j] = *reinterpret_cast<const float2 *>(from + width * D + 2 * cc);
       y[j] = *reinterpret_cast<const f32x4 *>(from + cc * D + d);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (s0 + j * TURNS < splits) join(mm, ll, x, ml[j].x, ml[j].y, y[j]);
+      if (s0 + j * turns < splits) join(mm, ll, x, ml[j].x, ml[j].y, y[j]);
   }
-  xs[threadIdx.x] = x;
-  if (d == 0) ms[turn] = mm, ls[turn] = ll;
-  __syncthreads();
-  if (turn != 0) return;
-  for (int t = 1; t < TURNS; ++t) join(mm, ll, x, ms[t], ls[t], xs[threadIdx.x + t * QUADS]);
-  store_row(c, a, tl, head, cc, d, x, mm, ll);
+  if (turns > 1) {
+    xs[threadIdx.x] = x;
+    mls[threadIdx.x] = make_float2(mm, ll);
+    __syncthreads();
+    if (turn == 0)
+      for (int j = 1; j < turns; ++j) {
+        const float2 other = mls[threadIdx.x + j * QUADS];
+        join(mm, ll, x, other.x, other.y, xs[threadIdx.x + j * QUADS]);
+      }
+  }
+  if (on && turn == 0) store_row(c, a, tl, head, cc, d, x, mm, ll);
 }
 
-// How the keys of a call are split: a workgroup takes split_steps steps.
+// How a call is launched: in tiles of `width` rows, a workgroup taking
+// split_steps steps of `keys` keys.
 struct Plan {
+  bool few;
+  int width, keys;
   int64_t tiles, items, splits;
   int split_steps;
 };
 
-// A workgroup takes 64 steps (2048 keys), so that sequences of very different
-// lengths fill the card evenly (64 sequences of up to 16384 tokens: 221 us,
-// one workgroup each 238 us), and fewer, down to 16, where that leaves
+// Few rows: a workgroup takes 64 steps (2048 keys), so that sequences of very
+// different lengths fill the card evenly (64 sequences of up to 16384 tokens:
+// 221 us, one workgroup each 238 us), and fewer, down to 16, where that leaves
 // compute units without one (two sequences of 14449 tokens: 13.7 us with 16,
 // 15.2 with 8).  Splitting costs the second launch, so a call whose rows all
 // see at most that many steps is not split (48 sequences with a window of
@@ -500,56 +856,87 @@ struct Plan {
 constexpr int kWaves = 4;
 constexpr int64_t kMinSteps = 16, kMostSteps = 64, kMaxSplits = 256;
 
-Plan decode_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
+// Many rows: as many parts as give every compute unit two workgroups, of 8
+// steps at least (113 rows over 14449 tokens, 28 heads over 4: 28 tiles in 18
+// parts 55 us, in 10 parts 66 us), and none where there are about as many
+// tiles as units (1024 rows of 28 heads over 4, 224 tiles: 29 us, in two
+// parts 41 us).
+constexpr int64_t kMinTileSteps = 8;
+
+Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
   Plan p;
-  const int group = heads / c.kv_heads;
-  p.tiles = ((int64_t)b.max_rows * group + 15) / 16;
+  const int64_t group = heads / c.kv_heads, rows = b.max_rows * group, cus = device_cu_count();
+  p.few = rows <= 32;
+  p.width = p.few ? 16 : kTileRows;
+  p.keys = p.few ? 32 : kTileKeys;
+  p.tiles = (rows + p.width - 1) / p.width;
   p.items = b.seqs * p.tiles * c.kv_heads;
-  const int64_t steps = most_steps(32, b, (15 + group) / group + 1, window, sinks);
-  const int64_t even = (p.items * steps + device_cu_count() - 1) / device_cu_count();
-  int64_t per = even < kMinSteps ? kMinSteps : even > kMostSteps ? kMostSteps : even;
-  // sixteen tiles for every compute unit fill the card evenly by themselves
-  if (p.items >= 16 * device_cu_count()) per = steps;
+  const int64_t span = (p.width - 1 + group) / group + 1;  // positions of a tile's rows
+  const int64_t steps = most_steps(p.keys, b, (int)span, window, sinks);
+  const int64_t even = (p.items * steps + cus - 1) / cus;
+  int64_t per;
+  if (p.few) {
+    per = even < kMinSteps ? kMinSteps : even > kMostSteps ? kMostSteps : even;
+    per = (per + kWaves - 1) / kWaves * kWaves;
+    // sixteen tiles for every compute unit fill the card evenly by themselves
+    if (p.items >= 16 * cus) per = steps;
+  } else {
+    per = std::max(kMinTileSteps, (even + 1) / 2);
+    if (p.items * 8 >= cus * 7) per = steps;
+  }
+  if (per > steps) per = steps;
   if (per * kMaxSplits < steps) per = (steps + kMaxSplits - 1) / kMaxSplits;
-  per = (per + kWaves - 1) / kWaves * kWaves;
   p.split_steps = (int)per;
   p.splits = (steps + per - 1) / per;
   return p;
-}
-
-size_t plan_bytes(const KvCache &c, const Plan &p) {
-  if (p.splits == 1) return 0;
-  return (size_t)(p.items * p.splits * part_floats(16, c.head_dim)) * sizeof(float);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(const KvCache &c, const KvBatch &b, int heads, int window,
                                     int sinks) {
-  return plan_bytes(c, decode_plan(c, b, heads, window, sinks));
+  const Plan p = make_plan(c, b, heads, window, sinks);
+  if (p.splits == 1) return 0;
+  return (size_t)(p.items * p.splits * part_floats(p.width, c.head_dim)) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b,
                                const KvAttention &a, hipStream_t s) {
-  const Plan p = decode_plan(c, b, a.heads, a.window, a.sinks);
+  const Plan p = make_plan(c, b, a.heads, a.window, a.sinks);
   const int64_t grid = p.items * p.splits;
-  if (grid > 0x7FFFFFFF / (64 * kWaves)) return hipErrorInvalidConfiguration;
+  const int64_t cols = std::min<int64_t>(p.width, (int64_t)b.max_rows * (a.heads / c.kv_heads));
+  if (grid > 0x7FFFFFFF / 256 || p.items * cols > 0x7FFFFFFF / 256)
+    return hipErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * kWaves), 0, s, c, layer, b, a,
-                       (int)p.tiles, (int)p.splits, p.split_steps);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, c, layer, b, a,
+                       (uint32_t)p.tiles, (int)p.splits, p.split_steps);
   };
-  if (c.head_dim == 128) go(decode_kernel<128, kWaves>);
-  else go(decode_kernel<64, kWaves>);
-  if (p.splits > 1) {
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    auto join = [&](auto kernel) {
-      const int cols = (int)std::min<int64_t>(16, (int64_t)b.max_rows * (a.heads / c.kv_heads));
-      hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * cols)), dim3(256), 0, s, c, b, a,
-                         (uint32_t)p.tiles, 16, cols, (int)p.splits, p.split_steps);
-    };
+  if (p.few) {
+    if (c.head_dim == 128) go(decode_kernel<128, kWaves>);
+    else go(decode_kernel<64, kWaves>);
+  } else {
+    if (c.head_dim == 128) go(tile_kernel<128>);
+    else go(tile_kernel<64>);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  // as many turns as there are four parts for each, the rest of the threads on
+  // other rows
+  int turns = 256 / (c.head_dim / 4);
+  while (turns > 1 && p.splits <= 2 * turns) turns /= 2;
+  const int at_once = 256 / (c.head_dim / 4) / turns;
+  const int64_t groups = (cols + at_once - 1) / at_once;
+  auto join = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * groups)), dim3(256), 0, s, c, b, a,
+                       (uint32_t)p.tiles, p.width, (int)groups, turns, (int)p.splits,
+                       p.split_steps);
+  };
+  if (p.few) {
     if (c.head_dim == 128) join(join_kernel<128, 32>);
     else join(join_kernel<64, 32>);
+  } else {
+    if (c.head_dim == 128) join(join_kernel<128, kTileKeys>);
+    else join(join_kernel<64, kTileKeys>);
   }
   return hipGetLastError();
 }

@@ -137,6 +137,11 @@ __device__ inline void copy16_to_lds(uint32_t m0, const void *base, uint32_t vof
   asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(m0) : "memory");
 }
 
+// The same with 4 bytes per active lane, which land at m0 + 4 * lane.
+__device__ inline void copy4_to_lds(uint32_t m0, const void *base, uint32_t voff) {
+  asm volatile("global_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(m0) : "memory");
+}
+
 // Sum of the 8 bf16 values of a 16-byte chunk, in k order.
 __device__ inline float chunk_sum8(uint4 c) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
