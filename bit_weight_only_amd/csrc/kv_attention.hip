@@ -251,6 +251,14 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   w /= (uint32_t)max_splits;
   const int64_t seq = w / tiles;
   const uint32_t item = w * (uint32_t)c.kv_heads + head;
+  const int32_t *table = b.table + seq * b.table_stride;
+  // without a window, where the first page ids stand does not depend on the
+  // lengths: they are read beside them
+  int page_ahead = -1;
+  if (a.window == 0) {
+    const int64_t t0 = (int64_t)(split * split_steps + wave + (lane >> 1) * W) * 32 + 16 * (lane & 1);
+    page_ahead = table[min(t0 >> c.page_shift, b.table_stride - 1)];
+  }
   const Tile tl(c, b, a, seq, w % tiles, 16);
   if (tl.empty()) return;
   const Steps<32> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
@@ -263,7 +271,6 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
   const int pos = mine ? tl.len - tl.n + tok : -1;
 
-  const int32_t *table = b.table + seq * b.table_stride;
   const int64_t layer_pages = layer * c.pages;
   const int page_blocks = 1 << (c.page_shift - 4);
   // What the wave's next 32 steps need to know of their blocks, lane 2s + h
@@ -271,6 +278,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   // the values' scale 2^e e and 2^-e.  Read ahead of the steps as vectors: a
   // scalar read per step would cost the step its whole latency, since scalar
   // reads return out of order and any use waits for all of them.
+  const int first = split * split_steps + wave;
   int page_l = -1;
   float kc_l = 0.0f, ve_l = 0.0f, vi_l = 1.0f;
   auto block_of = [&](int page, int t0) {
@@ -280,7 +288,9 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   auto look = [&](int i0) {
     const int i = i0 + (lane >> 1) * W;
     const int t0 = steps.key(i) + 16 * (lane & 1);
-    page_l = i < end && t0 < tl.len ? table[t0 >> c.page_shift] : -1;
+    page_l = -1;
+    if (i < end && t0 < tl.len)
+      page_l = a.window == 0 && i0 == first ? page_ahead : table[t0 >> c.page_shift];
     if (page_l >= c.pages) page_l = -1;
     const int64_t block = block_of(page_l < 0 ? 0 : page_l, t0);
     kc_l = c.ks[block];
@@ -310,7 +320,6 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     }
   };
 
-  const int first = split * split_steps + wave;
   look(first);
 
   bf16x8 q[KS];
@@ -801,25 +810,30 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
   const uint32_t item = w;
   const int head = w % (uint32_t)c.kv_heads;
   w /= (uint32_t)c.kv_heads;
+  const float *part = static_cast<const float *>(a.ws) +
+                      (int64_t)item * max_splits * part_floats(width, D);
+  // the first parts are on their way before the lengths say how many there are
+  float2 ml[8];
+  f32x4 y[8];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float *from = part + min(s0 + j * turns, max_splits - 1) * part_floats(width, D);
+      ml[j] = *reinterpret_cast<const float2 *>(from + width * D + 2 * min(cc, width - 1));
+      y[j] = *reinterpret_cast<const f32x4 *>(from + min(cc, width - 1) * D + d);
+    }
+  };
+  load(turn);
   const Tile tl(c, b, a, w / tiles, w % tiles, width);
   if (tl.empty()) return;
   const Steps<N> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
   if (steps.count <= split_steps) return;  // written already
   const int splits = (steps.count + split_steps - 1) / split_steps;
   const bool on = cc < width && tl.r0 + cc < tl.rows;
-  const float *part = static_cast<const float *>(a.ws) +
-                      (int64_t)item * max_splits * part_floats(width, D);
   float mm = -INFINITY, ll = 0.0f;
   f32x4 x = {0, 0, 0, 0};
-  for (int s0 = turn; on && s0 < splits; s0 += 8 * turns) {
-    float2 ml[8];
-    f32x4 y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float *from = part + min(s0 + j * turns, splits - 1) * part_floats(width, D);
-      ml[j] = *reinterpret_cast<const float2 *>(from + width * D + 2 * cc);
-      y[j] = *reinterpret_cast<const f32x4 *>(from + cc * D + d);
-    }
+  for (int s0 = turn; s0 < splits; s0 += 8 * turns) {
+    if (s0 != turn) load(s0);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (s0 + j * turns < splits) join(mm, ll, x, ml[j].x, ml[j].y, y[j]);

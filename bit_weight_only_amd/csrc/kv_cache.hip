@@ -88,12 +88,6 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
   const int t0 = (int)(blk * kKvBlock);
   if (blk * kKvBlock >= last) return;
   const int page = b.table[seq * b.table_stride + (t0 >> c.page_shift)];
-  if (page < 0 || page >= c.pages) return;
-  const int64_t block = ((layer * c.pages + page) * c.kv_heads + head) *
-                            (int64_t)(1 << (c.page_shift - 4)) +
-                        ((t0 & (c.page_tokens() - 1)) >> 4);
-  uint8_t *codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
-  float *scale = (kv ? c.vs : c.ks) + block;
   const uint8_t *src = static_cast<const uint8_t *>(kv ? x.v : x.k);
   const int64_t stride = (kv ? x.v_stride : x.k_stride) * (F32 ? 4 : 2);
 
@@ -120,6 +114,13 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
       }
     }
   }
+  // the rows are on their way before the page is known
+  if (page < 0 || page >= c.pages) return;
+  const int64_t block = ((layer * c.pages + page) * c.kv_heads + head) *
+                            (int64_t)(1 << (c.page_shift - 4)) +
+                        ((t0 & (c.page_tokens() - 1)) >> 4);
+  uint8_t *codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
+  float *scale = (kv ? c.vs : c.ks) + block;
   int e = block_exponent(wave_max(top));
   const bool has_old = first > t0;
   int e_old = e;
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
 
 // ------------------------------------------------------------------ the pool
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 
 // Exclusive prefix sum of v over the workgroup's threads in thread order;
 // `total` gets the sum.  `part`: one int per wave in LDS.
@@ -253,40 +254,87 @@ struct ReserveRequests {
   }
 };
 
-// One workgroup: items 1024 at a time, their requests numbered by a prefix
+// The counts of 2048 pages: a wave takes 512 consecutive ones, 64 at a time, a
+// page per lane, so that pages are numbered by counting bits of ballots.
+constexpr int kRunGroups = 8;
+constexpr int kRunPages = kPlanThreads * kRunGroups;
+
+__device__ inline int64_t run_page(int64_t page0, int g) {
+  return page0 + ((threadIdx.x >> 6) * kRunGroups + g) * 64 + (threadIdx.x & 63);
+}
+__device__ inline void read_run(const KvCache &c, const int32_t *refs, int64_t page0,
+                                int32_t (&r)[kRunGroups]) {
+#pragma unroll
+  for (int g = 0; g < kRunGroups; ++g) {
+    const int64_t page = run_page(page0, g);
+    r[g] = page < c.pages ? refs[page] : -1;
+  }
+}
+// Number of ones below the lane.
+__device__ inline int ones_below(uint64_t bits) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(bits >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)bits, 0u));
+}
+// `before`: ones of the waves before this one, out of each wave's own number;
+// `total`: of all waves.  `part`: one int per wave in LDS.
+__device__ inline void wave_prefix(int mine, int *part, int &before, int &total) {
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();  // the previous call's reads of part are over
+  if ((threadIdx.x & 63) == 0) part[wave] = mine;
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    const int p = part[w];
+    before += w < wave ? p : 0;
+    total += p;
+  }
+}
+
+// One workgroup: items 256 at a time, their requests numbered by a prefix
 // sum, then the free pages numbered the same way from page 0 on until every
-// request has its page.  Latency bound (a few dependent reads per 8192 pages
-// looked at); one workgroup, so that the order needs no second launch.
+// request has its page.  Latency bound, a few dependent reads and barriers;
+// one workgroup, so that the order needs no second launch.
 template <class Requests>
 __global__ __launch_bounds__(kPlanThreads) void assign_pages_kernel(KvCache c, KvPool p,
                                                                     Requests rq) {
   __shared__ int part[kPlanThreads / 64];
   __shared__ int first[kPlanThreads];        // number of an item's first request
   __shared__ int64_t where[kPlanThreads];    // table place of its first page
+  __shared__ int all_lost;
   const int tid = threadIdx.x;
+  int32_t refs[kRunGroups];
+  read_run(c, p.refs, 0, refs);  // the first pages, beside the requests
+  if (tid == 0) all_lost = 0;
   const int64_t items = rq.count() < 0 ? p.rows : rq.count();
   int64_t missing = 0;
   for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
     const int64_t i = i0 + tid;
     int64_t row = 0, entry = 0;
-    int lost = 0, want = 0, total, all_lost;
+    int lost = 0, want = 0, total;
     if (i < items) want = rq.ask(c, p, i, row, entry, lost);
     const int mine = block_prefix(want, part, total);
-    block_prefix(lost, part, all_lost);
+    if (lost) atomicAdd(&all_lost, lost);
     first[tid] = mine;
     where[tid] = row * p.stride + entry;
-    __syncthreads();
     int found = 0;
-    for (int64_t page0 = 0; page0 < c.pages && found < total; page0 += 8 * kPlanThreads) {
-      const int64_t at = page0 + 8 * tid;
-      uint32_t free_mask = 0;
+    for (int64_t page0 = 0; page0 < c.pages && found < total; page0 += kRunPages) {
+      if (i0 + page0 > 0) read_run(c, p.refs, page0, refs);
+      uint64_t free[kRunGroups];
+      int count = 0, before, here;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (at + j < c.pages && p.refs[at + j] == 0) free_mask |= 1u << j;
-      int here;
-      int rank = found + block_prefix(__popc(free_mask), part, here);
-      for (; free_mask && rank < total; free_mask &= free_mask - 1, ++rank) {
-        const int64_t page = at + __ffs(free_mask) - 1;
+      for (int g = 0; g < kRunGroups; ++g) {
+        free[g] = __ballot(refs[g] == 0);
+        count += __popcll(free[g]);
+      }
+      wave_prefix(count, part, before, here);  // its barriers are first's and where's too
+      int rank0 = found + before;
+#pragma unroll
+      for (int g = 0; g < kRunGroups; ++g) {
+        const int rank = rank0 + ones_below(free[g]);
+        rank0 += __popcll(free[g]);
+        if (refs[g] != 0 || rank >= total) continue;
+        const int64_t page = run_page(page0, g);
         int lo = 0, hi = kPlanThreads;  // the last item whose first request is <= rank
         while (hi - lo > 1) {
           const int mid = (lo + hi) / 2;
@@ -300,16 +348,20 @@ __global__ __launch_bounds__(kPlanThreads) void assign_pages_kernel(KvCache c, K
     found = found < total ? found : total;
     for (int r = mine + (found > mine ? found - mine : 0); r < mine + want; ++r)
       p.table[where[tid] + (r - mine)] = -1;
-    missing += total - found + all_lost;
+    missing += total - found;
     if (i < items) rq.done(p, i);
     __syncthreads();
   }
-  if (tid == 0 && p.missing) *p.missing = (int32_t)(missing > 0x7FFFFFFF ? 0x7FFFFFFF : missing);
+  if (tid == 0 && p.missing) {
+    missing += all_lost;
+    *p.missing = (int32_t)(missing > 0x7FFFFFFF ? 0x7FFFFFFF : missing);
+  }
 }
 
-// Page copies are cut into pieces of 16 KB of codes per workgroup (256 lanes,
-// four 16-byte loads in flight each).
-constexpr int kPieceBytes = 16384;
+// Page copies are cut into pieces of 16 KB of codes per workgroup, four 16-byte
+// loads in flight for each of 256 lanes (eight: a third slower).
+constexpr int kPieceLoads = 4;
+constexpr int kPieceBytes = kPieceLoads * 256 * 16;
 
 __host__ __device__ inline int64_t page_pieces(const KvCache &c) {
   return (c.page_bytes() + kPieceBytes - 1) / kPieceBytes;
@@ -327,12 +379,12 @@ __device__ inline void copy_piece(const KvCache &c, int64_t layer, int64_t from,
   const uint4 *s = reinterpret_cast<const uint4 *>(base + (layer * c.pages + from) * bytes + at);
   uint4 *d = reinterpret_cast<uint4 *>(base + (layer * c.pages + to) * bytes + at);
   const int left = (int)((bytes - at < kPieceBytes ? bytes - at : kPieceBytes) / 16);
-  uint4 r[4];
+  uint4 r[kPieceLoads];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kPieceLoads; ++i)
     if ((int)threadIdx.x + i * 256 < left) r[i] = s[threadIdx.x + i * 256];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kPieceLoads; ++i)
     if ((int)threadIdx.x + i * 256 < left) d[threadIdx.x + i * 256] = r[i];
   if (at == 0) {
     float *sc = kv ? c.vs : c.ks;
@@ -420,26 +472,46 @@ __global__ __launch_bounds__(kPlanThreads) void compact_plan_kernel(KvCache c, K
   __shared__ int part[kPlanThreads / 64];
   int32_t *src = ws + kMoveWords, *dst = src + c.pages, *to = dst + c.pages;
   const int tid = threadIdx.x;
-  int count = 0, live;
-  for (int64_t i = tid; i < c.pages; i += kPlanThreads) count += p.refs[i] > 0;
-  block_prefix(count, part, live);
+  int32_t refs[kRunGroups];
+  int count = 0, before, live;
+  for (int64_t page0 = 0; page0 < c.pages; page0 += kRunPages) {
+    read_run(c, p.refs, page0, refs);
+#pragma unroll
+    for (int g = 0; g < kRunGroups; ++g) count += __popcll(__ballot(refs[g] > 0));
+  }
+  wave_prefix(count, part, before, live);
   int moves = 0, holes = 0;
-  for (int64_t page0 = 0; page0 < c.pages; page0 += kPlanThreads) {
-    const int64_t i = page0 + tid;
-    const int refs = i < c.pages ? p.refs[i] : 0;
-    const bool high = i < c.pages && i >= live && refs > 0;
-    const bool hole = i < live && refs <= 0;
-    int h, f;
-    const int hr = moves + block_prefix(high, part, h);
-    const int fr = holes + block_prefix(hole, part, f);
-    if (high) src[hr] = (int32_t)i;
-    if (hole) dst[fr] = (int32_t)i;
-    if (i < c.pages) {
-      to[i] = refs > 0 ? (int32_t)i : -1;
-      refs_out[i] = refs > 0 ? refs : 0;
+  for (int64_t page0 = 0; page0 < c.pages; page0 += kRunPages) {
+    if (c.pages > kRunPages) read_run(c, p.refs, page0, refs);  // else they are there
+    uint64_t high[kRunGroups], hole[kRunGroups];
+    int highs = 0, free = 0, h0, f0, all_high, all_free;
+#pragma unroll
+    for (int g = 0; g < kRunGroups; ++g) {
+      const int64_t page = run_page(page0, g);
+      high[g] = __ballot(page >= live && refs[g] > 0);
+      hole[g] = __ballot(page < live && refs[g] <= 0);
+      highs += __popcll(high[g]);
+      free += __popcll(hole[g]);
     }
-    moves += h;
-    holes += f;
+    wave_prefix(highs, part, h0, all_high);
+    wave_prefix(free, part, f0, all_free);
+    h0 += moves;
+    f0 += holes;
+#pragma unroll
+    for (int g = 0; g < kRunGroups; ++g) {
+      const int64_t page = run_page(page0, g);
+      if (page < c.pages) {
+        const bool used = refs[g] > 0;
+        if (used && page >= live) src[h0 + ones_below(high[g])] = (int32_t)page;
+        if (!used && page < live) dst[f0 + ones_below(hole[g])] = (int32_t)page;
+        to[page] = used ? (int32_t)page : -1;
+        refs_out[page] = used ? refs[g] : 0;
+      }
+      h0 += __popcll(high[g]);
+      f0 += __popcll(hole[g]);
+    }
+    moves += all_high;
+    holes += all_free;
   }
   __syncthreads();
   // refs_out holds the old counts of the moved pages (it may be refs itself)

@@ -151,6 +151,9 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():
+            # the raw handle: a Stream object first costs 2.9 us of a 6.5 us call
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
