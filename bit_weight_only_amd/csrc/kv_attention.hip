@@ -379,10 +379,12 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] *= alpha;
     }
+    // two bf16 terms: memory bound, this kernel has the time (rel-L2 of the
+    // result 0.0023 with one, 0.0017 with two, which is its own rounding)
     union {
       bf16x8 v;
       __bf16 e[8];
-    } p;
+    } p, rest;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float sum = 0.0f;
@@ -393,6 +395,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
         if (!(see >> (4 * h + e) & 1)) x = 0.0f;  // also where m is still -inf
         sum += x;
         p.e[4 * h + e] = (__bf16)x;
+        rest.e[4 * h + e] = (__bf16)(x - (float)p.e[4 * h + e]);
       }
       l += sum * lane_float(vi_l, 2 * sl + h);
     }
@@ -405,7 +408,11 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
       }
     }
 #pragma unroll
-    for (int t = 0; t < DT; ++t) o[t] = mfma(widen(vw[0][t], vw[1][t]), p.v, o[t]);
+    for (int t = 0; t < DT; ++t) {
+      const bf16x8 v = widen(vw[0][t], vw[1][t]);
+      o[t] = mfma(v, p.v, o[t]);
+      o[t] = mfma(v, rest.v, o[t]);
+    }
   };
 
   // the loads of a step go out before the work on the step before it

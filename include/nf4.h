@@ -465,11 +465,11 @@ size_t nf4_kv_attention_workspace_bytes(const nf4_kv_cache *cache, const nf4_kv_
  * What a row does not see never reaches it, NaN and infinities included.
  *
  * out: bfloat16 [rows][heads * head_dim].  lse: fp32 [rows][heads], or NULL.
- * Rows that are no tokens (a negative position) see nothing.  Products are
- * bf16 x bf16 (a code is exact in bf16) with fp32 sums; the weights exp(s -
- * max) are rounded to bf16 for the second product, like q for the first, and
- * the sum they are divided by is of the unrounded ones.  Bitwise reproducible
- * run to run for a given device.
+ * Rows that are no tokens (a negative position) see nothing.  The codes enter
+ * the products exactly, q as the bf16 values it holds, the weights exp(s -
+ * max) rounded to bf16 (up to 32 rows of a kv head: to two bf16 terms); sums
+ * are fp32, and the one that the result is divided by is of the unrounded
+ * weights.  Bitwise reproducible run to run for a given device.
  *
  * workspace: at least nf4_kv_attention_workspace_bytes bytes, any contents
  * (NULL when that is 0); calls sharing one must be ordered.  scale must be finite and
