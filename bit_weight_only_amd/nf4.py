@@ -481,7 +481,8 @@ class KVBatch:
         self.struct = _KVBatch(seqs, seqs if rows is None else rows, max_rows,
                                (1 << 30) if max_len is None else max_len,
                                None if row_start is None else _int32(row_start).data_ptr(),
-                               kv_len.data_ptr(), table.data_ptr(), table.stride(0))
+                               kv_len.data_ptr(), table.data_ptr(),
+                               max(table.stride(0), table.shape[1]))  # one row: any stride
         self.arg = ctypes.pointer(self.struct)
 
 

@@ -164,3 +164,6 @@ def test_python_structures_refuse_wrong_tensors():
         nf4.KVBatch(i(3), i(3, 4), row_start=i(3))
     with pytest.raises(nf4.NF4Error):
         nf4.KVPool(i(4), i(3, 4), i(2))
+    # a table of one row may carry any stride, a slice of a wider one its own
+    assert nf4.KVBatch(i(1), i(5).as_strided((1, 5), (0, 1))).struct.table_stride == 5
+    assert nf4.KVBatch(i(2), i(3, 9)[:, :4]).struct.table_stride == 9
