@@ -507,16 +507,21 @@ struct TileLds {
   static constexpr int kCopies = 2 * (D / 64) + 2;      // per wave and stage
 };
 
-template <int D>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int64_t layer,
-                                                                  KvBatch b, KvAttention a,
-                                                                  uint32_t tiles, int max_splits,
-                                                                  int split_steps) {
+template <int D, int G>
+__global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c, int64_t layer,
+                                                                      KvBatch b, KvAttention a,
+                                                                      uint32_t tiles,
+                                                                      int max_splits,
+                                                                      int split_steps) {
   using L = TileLds<D>;
   constexpr int DT = D / 32;   // tiles of 32 values
   constexpr int CH = D / 16;   // 16-byte pieces of a key
-  __shared__ __align__(16) uint8_t lds[L::kBytes];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __align__(16) uint8_t all_lds[G * L::kBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & (kTileWaves - 1);
+  // the team of four waves: team g takes steps g, g + G, .. with its own LDS
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kTileWaves));
+  uint8_t *const lds = all_lds + team * L::kBytes;
   const int col = lane & 31, h = lane >> 5;
   // heads first: a kv head's workgroups run on the same dies and find its keys
   // in their cache; the last rows, which see most, start first
@@ -532,7 +537,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int
   const Steps<kTileKeys> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
   const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
   if (split >= splits) return;
-  const int begin = split * split_steps, n = min(steps.count - begin, split_steps);
+  const int begin = split * split_steps + team;
+  const int turns = (min(steps.count - split * split_steps, split_steps) + G - 1) / G;
+  const int n = (min(steps.count - split * split_steps, split_steps) - team + G - 1) / G;
 
   const uint32_t r0 = tl.r0 + 32 * wave;
   const bool mine = r0 + col < tl.rows, idle = r0 >= tl.rows;
@@ -554,7 +561,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int
   }
   // lane 4s + i: page of block i of step s of a group of 16, -1 for none
   auto pages_of = [&](int s0) {
-    const int s = begin + s0 + (lane >> 2);
+    const int s = begin + (s0 + (lane >> 2)) * G;
     const int t0 = steps.key(s) + 16 * (lane & 3);
     int page = -1;
     if (s0 + (lane >> 2) < n && t0 < tl.len) page = table[t0 >> c.page_shift];
@@ -582,7 +589,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int
       const int at = 4 * (s & 15);
       holes |= ((uint32_t)(hole_mask >> at) & 15u) << 8;
       const int page = __builtin_amdgcn_readlane(page_l, at + wave);
-      const int t0 = steps.key(begin + s) + 16 * wave;
+      const int t0 = steps.key(begin + s * G) + 16 * wave;
       const uint64_t off = (uint64_t)(uint32_t)(page < 0 ? 0 : page) * page_bytes +
                            (uint32_t)((t0 & (c.page_tokens() - 1)) * D);
       kb = k0 + off;
@@ -738,12 +745,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int
   issue(1);
   holes >>= 4;  // steps 0 and 1 now have the two low places
   const uint8_t *st = lds;
-  for (int s = 0; s < n; ++s) {
+  for (int s = 0; s < turns; ++s) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(L::kCopies) : "memory");
     issue(s + 2);
-    const int key0 = steps.key(begin + s);
+    const int key0 = steps.key(begin + s * G);
     // rows of this wave that see nothing here leave it out
-    const bool none = key0 > w_hi || (a.window > 0 && key0 + kTileKeys - 1 <= w_lo - a.window &&
+    const bool none = s >= n || key0 > w_hi || (a.window > 0 && key0 + kTileKeys - 1 <= w_lo - a.window &&
                                       key0 >= a.sinks);
     if (!none) compute(st, key0, holes & 15u);
     st = st == lds + (kStages - 1) * L::kStage ? lds : st + L::kStage;
@@ -754,6 +761,30 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void tile_kernel(KvCache c, int
 
   float sum = l[0] + l[1];
   sum += __shfl_xor(sum, 32);
+  if (G > 1) {  // the teams' sums, through LDS that nobody copies into any more
+    __syncthreads();
+    float *of = reinterpret_cast<float *>(all_lds) + wave * (64 * (16 * DT + 2)) + lane;
+    if (team == 1) {
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) of[64 * (16 * t + e)] = o[t][e];
+      of[64 * 16 * DT] = m;
+      of[64 * (16 * DT + 1)] = sum;
+    }
+    __syncthreads();
+    if (team == 1) return;
+    const float m1 = of[64 * 16 * DT], sum1 = of[64 * (16 * DT + 1)];
+    const float top = fmaxf(m, m1);
+    const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+    const float f1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
+    m = top;
+    sum = sum * f0 + sum1 * f1;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[t][e] = o[t][e] * f0 + of[64 * (16 * t + e)] * f1;
+  }
   // worked out again rather than kept in registers through the loop
   const int lane2 = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
   const int my_col = lane2 & 31, my_h = lane2 >> 5;
@@ -862,7 +893,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
 // split_steps steps of `keys` keys.
 struct Plan {
   bool few;
-  int width, keys;
+  int width, keys, teams;
   int64_t tiles, items, splits;
   int split_steps;
 };
@@ -877,16 +908,19 @@ struct Plan {
 constexpr int kWaves = 4;
 constexpr int64_t kMinSteps = 16, kMostSteps = 64, kMaxSplits = 256;
 
-// Many rows: as many parts as give every compute unit two workgroups, of 8
-// steps at least (113 rows over 14449 tokens, 28 heads over 4: 28 tiles in 18
-// parts 55 us, in 10 parts 66 us), and none where there are about as many
-// tiles as units (1024 rows of 28 heads over 4, 224 tiles: 29 us, in two
-// parts 41 us).
+// Many rows: no more tiles than compute units leave a unit one workgroup, and a
+// SIMD one wave, which waits for its own products half of the time: then two
+// teams of waves share a tile (1024 rows of 28 heads over 4, 224 tiles: 27.2 us
+// against 29.3), and the keys are split as far as one workgroup per unit goes,
+// in parts of 8 steps at least (113 rows over 14449 tokens, 28 tiles: 9 parts
+// of two teams 53 us, 18 parts of one 56 us, 10 parts, past one workgroup per
+// unit, 75 us).
 constexpr int64_t kMinTileSteps = 8;
 
 Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
   Plan p;
   const int64_t group = heads / c.kv_heads, rows = b.max_rows * group, cus = device_cu_count();
+  p.teams = 1;
   p.few = rows <= 32;
   p.width = p.few ? 16 : kTileRows;
   p.keys = p.few ? 32 : kTileKeys;
@@ -902,8 +936,12 @@ Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int si
     // sixteen tiles for every compute unit fill the card evenly by themselves
     if (p.items >= 16 * cus) per = steps;
   } else {
-    per = std::max(kMinTileSteps, (even + 1) / 2);
-    if (p.items * 8 >= cus * 7) per = steps;
+    per = steps;
+    p.teams = p.items <= cus ? 2 : 1;
+    if (p.teams == 2) {
+      const int64_t parts = cus / p.items;
+      per = std::max(kMinTileSteps, (steps + parts - 1) / parts);
+    }
   }
   if (per > steps) per = steps;
   if (per * kMaxSplits < steps) per = (steps + kMaxSplits - 1) / kMaxSplits;
@@ -926,18 +964,23 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
   const Plan p = make_plan(c, b, a.heads, a.window, a.sinks);
   const int64_t grid = p.items * p.splits;
   const int64_t cols = std::min<int64_t>(p.width, (int64_t)b.max_rows * (a.heads / c.kv_heads));
-  if (grid > 0x7FFFFFFF / 256 || p.items * cols > 0x7FFFFFFF / 256)
+  if (grid > 0x7FFFFFFF / 512 || p.items * cols > 0x7FFFFFFF / 256)
     return hipErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, c, layer, b, a,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256 * p.teams), 0, s, c, layer, b, a,
                        (uint32_t)p.tiles, (int)p.splits, p.split_steps);
   };
   if (p.few) {
     if (c.head_dim == 128) go(decode_kernel<128, kWaves>);
     else go(decode_kernel<64, kWaves>);
   } else {
-    if (c.head_dim == 128) go(tile_kernel<128>);
-    else go(tile_kernel<64>);
+    if (p.teams == 1) {
+      if (c.head_dim == 128) go(tile_kernel<128, 1>);
+      else go(tile_kernel<64, 1>);
+    } else {
+      if (c.head_dim == 128) go(tile_kernel<128, 2>);
+      else go(tile_kernel<64, 2>);
+    }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
