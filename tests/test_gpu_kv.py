@@ -374,6 +374,28 @@ def test_long_sequence_and_split(side):
     Case(side, 16, 128, 16, 4, 1, [3001, 700, 1500], [33, 64, 1]).run()
 
 
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+def test_more_tiles_than_compute_units(side, dim, page):
+    """320 tiles of rows: one team of waves each, the keys unsplit; with a
+    window, holes and NaN in unseen places."""
+    kv_len = [1 + (37 * i) % 90 for i in range(40)]
+    count = [min(n, 1 + (23 * i) % 50) for i, n in enumerate(kv_len)]
+    c = Case(side, 21, dim, page, 8, 8, kv_len, count)
+    c.run()
+    c.run(20, 3)
+    c.tokens(4, [1, kv_len[4] - 1], 1, 0x7F)
+    c.table[7, 0] = -1
+    c.run(20, 1)
+    Case(side, 22, dim, page, 6, 3, [300] * 90, [17] * 90).run()
+
+
+def test_many_short_sequences(side):
+    """4800 (sequence, head) pairs of single tokens, some without a token."""
+    kv_len = [(7 * i) % 45 for i in range(600)]
+    c = Case(side, 23, 64, 16, 8, 8, kv_len, [1 if n else 0 for n in kv_len])
+    c.run()
+
+
 def test_offsets_past_32_bits(side):
     """A cache whose codes pass 4 GiB: pages at its end are read and written."""
     t = side.torch
