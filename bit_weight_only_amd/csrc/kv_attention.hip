@@ -534,14 +534,26 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   const uint32_t tile = tiles - 1 - w / (uint32_t)b.seqs;
   const Tile tl(c, b, a, seq, tile, kTileRows);
   if (tl.empty()) return;
-  const Steps<kTileKeys> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
+  // the wave's rows: with two teams, waves w and w + 4 share a SIMD and hold
+  // different halves of the tile
+  const int sub = team == 0 ? wave : wave ^ 2;
+  uint32_t r0 = tl.r0 + 32 * sub;
+  int p_hi = tl.p_hi;
+  if (G > 1 && a.window == 0 && max_splits == 1) {
+    // the halves are the sequence's 64 rows number `tile` from its end (sub 0
+    // and 1) and from its start, so that every tile has as much to do
+    const uint32_t high = (2 * ((tl.rows + kTileRows - 1) / kTileRows) - 1 - tile) * 64;
+    r0 = (sub < 2 ? high : 64 * tile) + 32 * (sub & 1);
+    const uint32_t end = high < tl.rows ? high + 64 : 64 * tile + 64;
+    p_hi = tl.len - tl.n + (int)((min(end, tl.rows) - 1) / tl.group);
+  }
+  const Steps<kTileKeys> steps(tl.p_lo, p_hi, a.window, a.sinks);
   const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
   if (split >= splits) return;
   const int begin = split * split_steps + team;
   const int turns = (min(steps.count - split * split_steps, split_steps) + G - 1) / G;
   const int n = (min(steps.count - split * split_steps, split_steps) - team + G - 1) / G;
 
-  const uint32_t r0 = tl.r0 + 32 * wave;
   const bool mine = r0 + col < tl.rows, idle = r0 >= tl.rows;
   const uint32_t r = mine ? r0 + col : tl.rows - 1;
   const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
@@ -616,10 +628,6 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
   for (int j = 0; j < D / 16; ++j)
     q[j] = *reinterpret_cast<const bf16x8 *>(qp + 32 * (j / 2) + 8 * (j % 2));
-  // waited for here: a wait inside the loop would be for the copies too
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
-
   const Visible visible{a.window, a.sinks};
   const float cscale = a.scale * kLog2e;
   float m = -INFINITY, l[2] = {0.0f, 0.0f};
@@ -744,6 +752,9 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   holes >>= 4;
   issue(1);
   holes >>= 4;  // steps 0 and 1 now have the two low places
+  // q is waited for here: a wait inside the loop would be for the copies too
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
   const uint8_t *st = lds;
   for (int s = 0; s < turns; ++s) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(L::kCopies) : "memory");
@@ -763,7 +774,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   sum += __shfl_xor(sum, 32);
   if (G > 1) {  // the teams' sums, through LDS that nobody copies into any more
     __syncthreads();
-    float *of = reinterpret_cast<float *>(all_lds) + wave * (64 * (16 * DT + 2)) + lane;
+    float *of = reinterpret_cast<float *>(all_lds) + sub * (64 * (16 * DT + 2)) + lane;
     if (team == 1) {
 #pragma unroll
       for (int t = 0; t < DT; ++t)
@@ -814,7 +825,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   }
   const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
   float *part = static_cast<float *>(a.ws) + (item * max_splits + split) * part_floats(kTileRows, D);
-  const int row = 32 * wave + my_col;
+  const int row = 32 * sub + my_col;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -910,11 +921,12 @@ constexpr int64_t kMinSteps = 16, kMostSteps = 64, kMaxSplits = 256;
 
 // Many rows: no more tiles than compute units leave a unit one workgroup, and a
 // SIMD one wave, which waits for its own products half of the time: then two
-// teams of waves share a tile (1024 rows of 28 heads over 4, 224 tiles: 27.2 us
-// against 29.3), and the keys are split as far as one workgroup per unit goes,
-// in parts of 8 steps at least (113 rows over 14449 tokens, 28 tiles: 9 parts
-// of two teams 53 us, 18 parts of one 56 us, 10 parts, past one workgroup per
-// unit, 75 us).
+// teams of waves share a tile (1024 rows of 28 heads over 4, 224 tiles: 27.0 us
+// against 29.3; and 23.7 with a late and an early half in every tile, so that
+// none has more keys to go through), and the keys are split as far as one
+// workgroup per unit goes, in parts of 8 steps at least (113 rows over 14449
+// tokens, 28 tiles: 9 parts of two teams 49 us, 18 parts of one 55 us, 10
+// parts, past one workgroup per unit, 75 us).
 constexpr int64_t kMinTileSteps = 8;
 
 Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
