@@ -218,11 +218,18 @@ __device__ inline void spread_nan(const uint32_t (&va)[DT], const uint32_t (&vc)
 // Few rows: one workgroup of W waves per (16 rows of a kv head, part of the
 // keys), each wave every W-th step of 32 keys straight from memory to its
 // registers, a step ahead.  Lane l owns query row l % 16; with g = l / 16 it
-// holds keys 4g .. 4g + 3 of both blocks of a step.  Memory bound: a step
-// reads 8 KB (D = 128) for some 400 cycles of vector work.
+// holds keys 4g .. 4g + 3 of both blocks of a step.
 //
-// The waves meet in LDS, the parts in the workspace: each writes its sums and
-// counts its arrival, the last one adds them in order.
+// Memory bound: a step reads 8 KB (D = 128) for some 400 cycles of vector work.
+// 64 sequences of up to 16384 tokens (1.11 GB): 217 us = 5.1 TB/s, the rate of
+// a large copy; a bare read of the same pieces takes 185 us.  Six waves
+// took 252 us, eight 247, loads marked as not to be kept some 20 more.  Small
+// calls are bound by dependent trips to memory (lengths, page ids, keys, the
+// waves' meeting): one sequence of 113 tokens 6.3 us, of which 1.6 an empty
+// launch.
+//
+// The waves meet in LDS; the parts of split keys in the workspace, where each
+// leaves its sums for the second launch.
 
 template <int D>
 struct Step {
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   const int col = lane & 15, g = lane >> 4;
   // neighbouring workgroups take the heads of one page, so that what is read
   // at a time lies side by side (64 sequences of up to 16384 tokens: 256 us
-  // with the parts of a head side by side instead, 221 us this way)
+  // with the parts of a head side by side instead, 217 us this way)
   uint32_t w = blockIdx.x;
   const int head = w % (uint32_t)c.kv_heads;
   w /= (uint32_t)c.kv_heads;
@@ -492,6 +499,11 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 // Bound by the vector unit: per 32 rows and 64 keys (D = 128) the products
 // take 32 matrix instructions of 32 cycles, and widening the codes 128 vector
 // instructions, the softmax some 130 and 32 exponentials, 4 and 8 cycles each.
+// 14449 rows of 28 heads over 4: 1420 to 1460 us = 1025 to 1055 TFLOP/s, the
+// vector unit busy 0.72 of the time and the matrix cores 0.49; a product of
+// large bf16 matrices reaches 1222 TFLOP/s.  Keys and values widened once per
+// workgroup, bf16 in LDS, took 1538 us (LDS is then full), the scores of the
+// next 32 keys beside the weights of these 1486 us.
 constexpr int kTileKeys = 64;
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = 32 * kTileWaves;
@@ -911,11 +923,11 @@ struct Plan {
 
 // Few rows: a workgroup takes 64 steps (2048 keys), so that sequences of very
 // different lengths fill the card evenly (64 sequences of up to 16384 tokens:
-// 221 us, one workgroup each 238 us), and fewer, down to 16, where that leaves
-// compute units without one (two sequences of 14449 tokens: 13.7 us with 16,
+// 217 us, one workgroup each 238 us), and fewer, down to 16, where that leaves
+// compute units without one (two sequences of 14449 tokens: 13.9 us with 16,
 // 15.2 with 8).  Splitting costs the second launch, so a call whose rows all
 // see at most that many steps is not split (48 sequences with a window of
-// 1500: 19.0 us, split in two 25.5 us).
+// 1500: 20.4 us, split in two 25.5 us).
 constexpr int kWaves = 4;
 constexpr int64_t kMinSteps = 16, kMostSteps = 64, kMaxSplits = 256;
 
