@@ -500,7 +500,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 // take 32 matrix instructions of 32 cycles, and widening the codes 128 vector
 // instructions, the softmax some 130 and 32 exponentials, 4 and 8 cycles each.
 // 14449 rows of 28 heads over 4: 1420 to 1460 us = 1025 to 1055 TFLOP/s, the
-// vector unit busy 0.72 of the time and the matrix cores 0.49; a product of
+// vector unit busy 0.70 of the time and the matrix cores 0.47; a product of
 // large bf16 matrices reaches 1222 TFLOP/s.  Keys and values widened once per
 // workgroup, bf16 in LDS, took 1538 us (LDS is then full), the scores of the
 // next 32 keys beside the weights of these 1486 us.

@@ -389,6 +389,18 @@ def test_more_tiles_than_compute_units(side, dim, page):
     Case(side, 22, dim, page, 6, 3, [300] * 90, [17] * 90).run()
 
 
+@pytest.mark.parametrize("dim,page,heads,kv_heads", [(128, 32, 2, 2), (64, 16, 7, 1)])
+def test_rows_that_end_inside_tiles(side, dim, page, heads, kv_heads):
+    """Sequences of one to several tiles that end in any part of the last one."""
+    count = [64, 65, 128, 129, 192, 193, 300, 1, 0, 33]
+    c = Case(side, 24, dim, page, heads, kv_heads,
+             [n + (41 * i) % 130 for i, n in enumerate(count)], count)
+    c.run()
+    c.run(70, 2)
+    c.table[5, 1] = c.table[6, 7] = -1
+    c.run()
+
+
 def test_many_short_sequences(side):
     """4800 (sequence, head) pairs of single tokens, some without a token."""
     kv_len = [(7 * i) % 45 for i in range(600)]
