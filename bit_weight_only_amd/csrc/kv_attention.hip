@@ -681,10 +681,12 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[u][i] = see[u] >> (8 * (i >> 2) + (i & 3)) & 1 ? s[u][i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t on = (uint32_t)__builtin_amdgcn_sbfe((int)see[u], 8 * (i >> 2) + (i & 3), 1);
+          s[u][i] = __uint_as_float((on & __float_as_uint(s[u][i])) | (~on & 0xFF800000u));  // or -inf
+        }
       uint32_t any = 0;
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < kTileKeys * D; i += 1024) {
         const uint4 v = *reinterpret_cast<const uint4 *>(vt + i + lane * 16);
         any |= nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w);
@@ -816,6 +818,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   if (splits == 1) {
     const bool none = sum == 0.0f;
     const float inv = none ? 0.0f : 1.0f / sum;
+    const uint32_t keep = none ? 0u : ~0u;
     const uint32_t row = r0 + my_col;
     const int64_t at = (tl.row0 + row / tl.group) * a.heads + head * tl.group + row % tl.group;
     uint16_t *to = a.out + at * D + my_h * (4 * DT);
@@ -825,7 +828,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
       for (int x = 0; x < 4 * DT; x += 2) {
         const float u = o[x % DT][4 * i + x / DT] * inv, v = o[(x + 1) % DT][4 * i + (x + 1) / DT] * inv;
-        y[x / 2] = none ? 0u : bf16_pair(u, v);
+        y[x / 2] = bf16_pair(u, v) & keep;
       }
 #pragma unroll
       for (int x = 0; x < DT / 2; ++x)
