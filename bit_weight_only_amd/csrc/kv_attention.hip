@@ -499,8 +499,8 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 // Bound by the vector unit: per 32 rows and 64 keys (D = 128) the products
 // take 32 matrix instructions of 32 cycles, and widening the codes 128 vector
 // instructions, the softmax some 130 and 32 exponentials, 4 and 8 cycles each.
-// 14449 rows of 28 heads over 4: 1420 to 1460 us = 1025 to 1055 TFLOP/s, the
-// vector unit busy 0.70 of the time and the matrix cores 0.47; a product of
+// 14449 rows of 28 heads over 4: 1385 to 1430 us = 1045 to 1080 TFLOP/s, the
+// vector unit busy 0.73 of the time and the matrix cores 0.50; a product of
 // large bf16 matrices reaches 1222 TFLOP/s.  Keys and values widened once per
 // workgroup, bf16 in LDS, took 1538 us (LDS is then full), the scores of the
 // next 32 keys beside the weights of these 1486 us.
@@ -937,8 +937,8 @@ constexpr int64_t kMinSteps = 16, kMostSteps = 64, kMaxSplits = 256;
 // Many rows: no more tiles than compute units leave a unit one workgroup, and a
 // SIMD one wave, which waits for its own products half of the time: then two
 // teams of waves share a tile (1024 rows of 28 heads over 4, 224 tiles: 27.0 us
-// against 29.3; and 23.7 with a late and an early half in every tile, so that
-// none has more keys to go through), and the keys are split as far as one
+// against 29.3; and 23.7, by now 22.4, with a late and an early half in every
+// tile, so that none has more keys to go through), and the keys are split as far as one
 // workgroup per unit goes, in parts of 8 steps at least (113 rows over 14449
 // tokens, 28 tiles: 9 parts of two teams 49 us, 18 parts of one 55 us, 10
 // parts, past one workgroup per unit, 75 us).
