@@ -652,10 +652,12 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     __builtin_memcpy(vc, __builtin_assume_aligned(vr + 8 * D, D / 8), D / 8);
   };
   auto compute = [&](const uint8_t *st, int key0, uint32_t hole) {
-    // scales: lane 4k + i holds block i's of keys (k = 0) or values (k = 1)
-    const float sc = reinterpret_cast<const float *>(st + L::kS)[lane & 7];
-    const int ve_l = kv_scale_exponent(sc);
-    const float kc_l = sc * cscale, vi_l = __uint_as_float((uint32_t)(127 - ve_l) << 23);
+    // scales: lane 4k + i holds block i's of keys (k = 0) or values (k = 1),
+    // held to what a cache can have: a masked block's may never have been
+    // written, and the -inf of its scores times 0, NaN or less would not stay -inf
+    const int ve_l = kv_scale_exponent(reinterpret_cast<const float *>(st + L::kS)[lane & 7]);
+    const float kc_l = __uint_as_float((uint32_t)(127 + ve_l) << 23) * cscale;
+    const float vi_l = __uint_as_float((uint32_t)(127 - ve_l) << 23);
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -721,7 +723,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       t = max3(t, at(3), at(4));
       t = max3(t, at(5), at(6));
       t = max3(t, at(7), at(7));
-      mx = fmaxf(mx, t * kc[k]);  // scales are positive
+      mx = fmaxf(mx, t * kc[k]);  // kc is positive and finite
     }
     if (__any(mx > m + 8.0f)) {
       mx = fmaxf(mx, __shfl_xor(mx, 32));
