@@ -162,9 +162,12 @@ __device__ inline uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Adds sums (m, l, x) of other keys to (mm, ll, xx).
+// Adds sums (m, l, x) of other keys to (mm, ll, xx).  l is 0 where no key was
+// seen, and only there: the key at m has a weight.  m says less, since it leaves
+// NaN scores out and is -inf still if there were no others; l and x are NaN then
+// and make the result NaN.
 __device__ inline void join(float &mm, float &ll, f32x4 &xx, float m, float l, f32x4 x) {
-  if (m == -INFINITY) return;  // no key of these was seen
+  if (l == 0.0f) return;  // no key of these was seen
   const float top = fmaxf(mm, m);
   const float f = exp2_fast(mm - top), g = exp2_fast(m - top);
   ll = ll * f + l * g;
@@ -477,7 +480,8 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 #pragma unroll
     for (int v = 0; v < W; ++v) {
       const float mv = ml[0][v][cc];
-      ll += mv == -INFINITY ? 0.0f : ml[1][v][cc] * exp2_fast(mv - mm);
+      const float lv = ml[1][v][cc];
+      ll += lv == 0.0f ? 0.0f : lv * exp2_fast(mv - mm);  // (0: no key was seen)
       x += *reinterpret_cast<const f32x4 *>(sums + (v * 16 + cc) * PITCH + d);
     }
     if (splits == 1) {
@@ -672,11 +676,13 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       }
     }
     const uint8_t *vt = st + L::kV;
+    bool sees = true;  // whether the row sees any of these keys
     if (hole != 0 || !visible.all(key0, kTileKeys, w_lo, w_hi)) {
       uint64_t bits = visible.bits(key0, pos);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (hole >> k & 1) bits &= ~(0xFFFFull << (16 * k));
+      sees = bits != 0;
       bits >>= 4 * h;
       // bit 8a + e for element 4a + e of s[u]
       const uint32_t see[2] = {(uint32_t)bits, (uint32_t)(bits >> 32)};
@@ -735,8 +741,9 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] *= alpha;
     }
-    // (a row that has seen nothing yet has only -inf here, which stays 0)
-    const float base = m == -INFINITY ? 0.0f : m;
+    // (a row that has seen nothing yet has only -inf here, which stays 0; if
+    // what it sees is NaN or -inf by itself, its weights become NaN)
+    const float base = m == -INFINITY && !sees ? 0.0f : m;
     union {
       bf16x8 v[4];
       bf16x2 e[16];

@@ -76,3 +76,67 @@ def test_a_prompt_on_a_new_cache(side):
     case = Case(side, 32, dim, page, heads, kv_heads, [n], [n])
     case.c, case.table = c, table
     case.run(d=d)
+
+
+# -------------------------------------------------- NaN in all that a row sees
+def run_nan(c, *a, **kw):
+    """The case's check, and lse NaN just where the plain one is."""
+    out, z = c.run(*a, **kw)
+    q = c.q.reshape(-1, c.heads, c.dim).astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        lse = kv.attention(c.c, 0, c.table, c.start, c.kv_len, q, float(np.float32(0.09)), *(a or (0, 0)))[1]
+    assert np.array_equal(np.isnan(z), np.isnan(lse))
+    return out, z
+
+
+# one wave, single tokens, single tokens over split keys, two teams, split, one team
+NAN_FORMS = [(4, 2, [20], [1]), (4, 2, [200, 64], [1, 1]), (4, 1, [5001], [2]), (8, 2, [200, 70], [50, 70]),
+             (4, 1, [1500], [40]), (8, 8, [40] * 40, [33] * 40)]
+
+
+@pytest.mark.filterwarnings("ignore:invalid value")
+@pytest.mark.parametrize("form", range(len(NAN_FORMS)))
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_whose_scores_are_all_nan(side, form, dim):
+    """A query with NaN in it, and one whose scores are all -infinity, come out
+    as NaN, lse too, however the call is split."""
+    heads, kv_heads, kv_len, count = NAN_FORMS[form]
+    c = Case(side, 33, dim, 64, heads, kv_heads, kv_len, count)
+    c.q.reshape(-1, heads, dim)[-1, 1, 3] = np.nan
+    out, z = run_nan(c)
+    assert np.isnan(out[-1, 1]).all() and np.isnan(z[-1, 1]) and not np.isnan(z[-1, 0])
+    run_nan(c, 25, 2)
+    c = Case(side, 34, dim, 64, heads, kv_heads, kv_len, count)
+    c.c.k[..., 5] = c.c.k[..., 5] & 0x7F | 0x08  # positive and not 0
+    c.c.k[c.c.k == 127] = 0x38
+    row = c.q.reshape(-1, heads, dim)[-1, 1]
+    row[:] = 0.0
+    row[5] = -np.inf
+    out, z = run_nan(c)
+    assert np.isnan(out[-1, 1]).all() and np.isnan(z[-1, 1]) and not np.isnan(z[-1, 0])
+
+
+@pytest.mark.filterwarnings("ignore:invalid value")
+@pytest.mark.parametrize("form", range(len(NAN_FORMS)))
+def test_keys_that_are_all_nan_in_a_part(side, form):
+    """NaN keys wherever one wave, one team or one part of split keys looks:
+    the rows that see them are NaN, lse too."""
+    heads, kv_heads, kv_len, count = NAN_FORMS[form]
+    c = Case(side, 35, 64, 64, heads, kv_heads, kv_len, count)
+    n = kv_len[0]
+    for lo, hi in ((0, 1), (0, 32), (32, 64), (64, 128), (0, 2048), (2048, 5001), (0, n)):
+        if lo >= n:
+            continue
+        was = c.c.k.copy()
+        c.tokens(0, range(lo, min(hi, n)), 0, 0x7F, heads=[0])
+        out, z = run_nan(c)
+        assert np.isnan(z[count[0] - 1, 0])
+        run_nan(c, 16, 1)
+        c.c.k[:] = was
+
+
+def test_one_token_whose_key_is_nan(side):
+    c = Case(side, 36, 64, 16, 4, 2, [1], [1])
+    c.tokens(0, [0], 0, 0xFF)
+    out, z = run_nan(c)
+    assert np.isnan(out).all() and np.isnan(z).all()
