@@ -50,10 +50,12 @@ bool batch_shape_ok(const nf4_kv_batch &b) {
   return b.table_stride >= 1 && b.table_stride <= kMaxLen;
 }
 
-// No sequence is longer than the table: a large max_len costs no launch size.
+// No key lies past the table: a large max_len costs no launch size.
 nf4::KvBatch as_batch(const nf4_kv_batch &b, const nf4::KvCache &c) {
   const int64_t room = b.table_stride << c.page_shift;
-  return nf4::KvBatch{b.seqs, b.rows, (int)b.max_rows, (int)(b.max_len < room ? b.max_len : room),
+  const bool held = b.max_len < room;
+  return nf4::KvBatch{b.seqs, b.rows, (int)b.max_rows, (int)(held ? b.max_len : room),
+                      held ? (int)b.max_len : INT32_MAX,
                       b.row_start, b.kv_len, b.table, b.table_stride};
 }
 

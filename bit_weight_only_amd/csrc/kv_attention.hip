@@ -104,19 +104,20 @@ struct Visible {
   }
 };
 
-// The steps of N keys that rows p_lo .. p_hi can see, as a list: those with
-// first tokens, then from the start of the lowest row's window on.
+// The steps of N keys that rows from p_lo on can see, as a list: those with
+// first tokens, then from the start of the lowest row's window to the key `last`.
 template <int N>
 struct Steps {
   int sink_steps, from, count;
-  __device__ Steps(int p_lo, int p_hi, int window, int sinks) {
+  __device__ Steps(int p_lo, int last, int window, int sinks) {
     sink_steps = from = 0;
+    const int steps = last < 0 ? 0 : last / N + 1;
     if (window > 0 && p_lo - window + 1 > 0) {
       from = (p_lo - window + 1) / N;
-      sink_steps = (int)(((int64_t)sinks + N - 1) / N);
+      sink_steps = min((int)(((int64_t)sinks + N - 1) / N), steps);
       if (sink_steps >= from) from = sink_steps = 0;
     }
-    count = p_hi < 0 ? 0 : sink_steps + p_hi / N + 1 - from;
+    count = sink_steps + max(steps - from, 0);
   }
   __device__ int key(int i) const { return (i < sink_steps ? i : i - sink_steps + from) * N; }
 };
@@ -135,11 +136,11 @@ int64_t most_steps(int N, const KvBatch &b, int tile_rows, int window, int sinks
 struct Tile {
   int64_t row0;
   uint32_t rows, r0, group;  // rows of a kv head of one sequence stay under 2^31
-  int n, len, p_lo, p_hi;
+  int n, len, end, p_lo, p_hi;
   __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, int64_t seq,
                   uint32_t tile, uint32_t width) {
     group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
-    b.sequence(seq, c.page_shift, row0, n, len);
+    b.sequence(seq, row0, n, len, end);
     rows = (uint32_t)(n < b.max_rows ? n : b.max_rows) * group;
     r0 = tile * width;
     const uint32_t last = r0 + width < rows ? r0 + width - 1 : rows - 1;
@@ -147,6 +148,8 @@ struct Tile {
     p_hi = len - n + (int)(last / group);
   }
   __device__ bool empty() const { return r0 >= rows; }
+  // The last key that a row at p may see: not past the table.
+  __device__ int last_key(int p) const { return min(p, end - 1); }
 };
 
 // Workspace of a call whose keys are split: for every (item, split), an item
@@ -271,7 +274,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   }
   const Tile tl(c, b, a, seq, w % tiles, 16);
   if (tl.empty()) return;
-  const Steps<32> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
+  const Steps<32> steps(tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
   const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
   if (split >= splits) return;
   const int end = min(steps.count, (split + 1) * split_steps);
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     const int i = i0 + (lane >> 1) * W;
     const int t0 = steps.key(i) + 16 * (lane & 1);
     page_l = -1;
-    if (i < end && t0 < tl.len)
+    if (i < end && t0 < tl.end)
       page_l = a.window == 0 && i0 == first ? page_ahead : table[t0 >> c.page_shift];
     if (page_l >= c.pages) page_l = -1;
     const int64_t block = block_of(page_l < 0 ? 0 : page_l, t0);
@@ -563,7 +566,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     const uint32_t end = high < tl.rows ? high + 64 : 64 * tile + 64;
     p_hi = tl.len - tl.n + (int)((min(end, tl.rows) - 1) / tl.group);
   }
-  const Steps<kTileKeys> steps(tl.p_lo, p_hi, a.window, a.sinks);
+  const Steps<kTileKeys> steps(tl.p_lo, tl.last_key(p_hi), a.window, a.sinks);
   const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
   if (split >= splits) return;
   const int begin = split * split_steps + team;
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     const int s = begin + (s0 + (lane >> 2)) * G;
     const int t0 = steps.key(s) + 16 * (lane & 3);
     int page = -1;
-    if (s0 + (lane >> 2) < n && t0 < tl.len) page = table[t0 >> c.page_shift];
+    if (s0 + (lane >> 2) < n && t0 < tl.end) page = table[t0 >> c.page_shift];
     return page;
   };
   int page_l = -1, page_next = pages_of(0);
@@ -899,7 +902,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
   load(turn);
   const Tile tl(c, b, a, w / tiles, w % tiles, width);
   if (tl.empty()) return;
-  const Steps<N> steps(tl.p_lo, tl.p_hi, a.window, a.sinks);
+  const Steps<N> steps(tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
   if (steps.count <= split_steps) return;  // written already
   const int splits = (steps.count + split_steps - 1) / split_steps;
   const bool on = cc < width && tl.r0 + cc < tl.rows;

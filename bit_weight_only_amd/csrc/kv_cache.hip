@@ -82,11 +82,12 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
   const int64_t seq = w / blocks_per_seq;
   if (seq >= b.seqs) return;
   int64_t row0;
-  int n, len;
-  b.sequence(seq, c.page_shift, row0, n, len);
+  int n, len, end;
+  b.sequence(seq, row0, n, len, end);
   const int begin = len - n;                    // position of row 0, may be negative
   const int first = begin < 0 ? 0 : begin;      // first new token
   int last = begin + (n < b.max_rows ? n : b.max_rows);  // past the last one
+  last = last < end ? last : end;
   const int64_t blk = first / kKvBlock + w % blocks_per_seq;
   const int t0 = (int)(blk * kKvBlock);
   if (blk * kKvBlock >= last) return;

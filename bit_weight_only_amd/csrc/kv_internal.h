@@ -31,13 +31,17 @@ struct KvCache {
 
 struct KvBatch {
   int64_t seqs, rows;
-  int max_rows, max_len;
+  int max_rows;
+  int max_len;   // no more than the table has room for
+  int held_len;  // what the host holds lengths to, 2^31 - 1 where only the table does
   const int32_t *row_start, *kv_len, *table;
   int64_t table_stride;
 
-  // Rows of sequence s: the first one's index, their number and the tokens of
-  // the sequence, held to what the host was told.
-  __device__ void sequence(int64_t s, int page_shift, int64_t &row0, int &n, int &len) const {
+  // Rows of sequence s: the first one's index and their number; the tokens of
+  // the sequence, and how many of them have a place in the table.  Only the
+  // rows' positions come from the former: a sequence that has outgrown its
+  // table must not find its new tokens on the places of older ones.
+  __device__ void sequence(int64_t s, int64_t &row0, int &n, int &len, int &end) const {
     int64_t r0 = s, r1 = s + 1;
     if (row_start) {
       r0 = row_start[s];
@@ -47,11 +51,9 @@ struct KvBatch {
     r1 = r1 < r0 ? r0 : r1 > rows ? rows : r1;
     row0 = r0;
     n = (int)(r1 - r0);
-    const int64_t room = table_stride << page_shift;
-    int64_t l = kv_len[s];
-    l = l < 0 ? 0 : l;
-    l = l > max_len ? max_len : l;
-    len = (int)(l > room ? room : l);
+    const int l = kv_len[s];
+    len = l < 0 ? 0 : l > held_len ? held_len : l;
+    end = len > max_len ? max_len : len;
   }
 };
 

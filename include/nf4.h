@@ -399,8 +399,12 @@ typedef struct nf4_kv_cache {
  * kv_len[s] - (row_start[s + 1] - row_start[s]) + i.  A sequence may have no
  * rows, and rows whose position would be negative are no tokens.  max_rows
  * and max_len bound what any sequence has, as the host knows it: rows past
- * max_rows are not processed, lengths past max_len (or past the table) count
- * as that. */
+ * max_rows are not processed, lengths past max_len count as max_len (the rows'
+ * positions follow, so that max_len must cover what is appended).  Where
+ * max_len is no less than the tokens the table has room for, it bounds
+ * nothing: a sequence that is longer than its table (nf4_kv_reserve lets it
+ * become that) keeps its rows' positions, and its tokens past the table are
+ * those of a hole, not written and never seen. */
 typedef struct nf4_kv_batch {
   int64_t seqs, rows;        /* >= 1; rows of all sequences together */
   int64_t max_rows, max_len; /* 1 .. rows; 0 .. 2^30 */

@@ -5,7 +5,7 @@ import pytest
 from oracle import kv
 
 from gpu_helpers import say
-from test_gpu_kv import Case, bf16, device_batch, same_cache, side  # noqa: F401
+from test_gpu_kv import Case, PoolCase, bf16, device_batch, device_cache, same_cache, side  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,77 @@ def test_one_token_whose_key_is_nan(side):
     c.tokens(0, [0], 0, 0xFF)
     out, z = run_nan(c)
     assert np.isnan(out).all() and np.isnan(z).all()
+
+
+# ------------------------------------------- sequences longer than their tables
+def with_holes(table, entries):
+    """The table with entries that name no page after its own."""
+    return np.concatenate([table, np.full((len(table), entries), -1, np.int32)], 1)
+
+
+@pytest.mark.parametrize("kv_len,count", [([49, 40], [1, 1]), ([60, 48], [20, 7]), ([48, 200], [48, 40]),
+                                          ([100, 49], [100, 49])])
+@pytest.mark.parametrize("max_len", [None, 48, 1000])
+def test_sequences_longer_than_their_tables(side, kv_len, count, max_len):
+    """Tokens past the table are dropped as in a hole, and every row keeps its
+    position."""
+    rng = np.random.default_rng(40)
+    dim, heads, page = 64, 2, 16
+    table = np.array([[4, 1, 6], [0, 5, 2]], np.int32)
+    c = kv.Cache(1, 8, heads, page, dim, rng)
+    start = np.concatenate([[0], np.cumsum(count)])
+    x = bf16(rng.normal(size=(start[-1], heads * dim)))
+    d = device_cache(side, c)
+    b = device_batch(side, table, kv_len, start, max_len=max_len)
+    r = side.to_dev(x)
+    side.stream.wait_stream(side.torch.cuda.current_stream())
+    side.nf4.nf4_kv_append(d, 0, b, r, heads * dim, r, heads * dim, 1, stream=side.stream)
+    side.sync()
+    y = x.reshape(-1, heads, dim).astype(np.float64)
+    kv.append(c, 0, with_holes(table, 20), start, kv_len, y, y)
+    same_cache(c, d)
+    for a in (c.k, c.v):
+        a[a & 127 == 127] = 0x30
+    for group in (1, 8, 24):
+        case = Case(side, 41, dim, page, heads * group, heads, kv_len, count)
+        case.c, case.pages = c, 8
+        for window, sinks in ((0, 0), (5, 0), (9, 40), (30, 3)):
+            case.table = table
+            out, z = case.run(window, sinks, check=False, max_len=max_len)
+            case.table = with_holes(table, 20)
+            case.check(out, z, window, sinks, 0.09)
+
+
+def test_a_long_sequence_past_its_table(side):
+    """Keys in parts, the window past what the table holds."""
+    for count in (1, 40):
+        for length in (4097, 9000):
+            c = Case(side, 42, 64, 64, 4, 1, [4096], [1], stride_more=0)
+            c.kv_len, c.count, c.start = [length], [count], np.array([0, count])
+            c.q = bf16(c.rng.normal(size=(count, 4 * 64)) * 4)
+            table = c.table
+            for window, sinks in ((0, 0), (300, 5), (4950, 0), (100, 1 << 40)):
+                c.table = table
+                out, z = c.run(window, sinks, check=False, max_len=None)
+                c.table = with_holes(table, 80)
+                c.check(out, z, window, sinks, 0.09)
+
+
+def test_fork_and_go_on_past_a_full_table(side):
+    """Both rows of a fork whose pages are all shared outgrow the table: no code
+    of the shared pages changes."""
+    c = PoolCase(side, 12, 3, 3, page=16, layers=1, seed=6)
+    c.do("reserve", [48, 20, 0])
+    c.do("fork", [0], [2])
+    c.do("reserve", [1, 1, 1])
+    assert c.p.missing == 2 and c.p.len.tolist() == [49, 21, 49]
+    t = side.torch
+    for max_len in (1 << 30, 48):
+        b = side.nf4.KVBatch(c.pool.length, c.pool.table, max_len=max_len)
+        x = t.randn(3, 64, device="cuda")
+        side.stream.wait_stream(t.cuda.current_stream())
+        side.nf4.nf4_kv_append(c.d, 0, b, x, 64, x, 64, side.nf4.NF4_KV_F32, stream=side.stream)
+        side.sync()
+        y = x.double().cpu().numpy().reshape(3, 1, 64)
+        kv.append(c.c, 0, with_holes(c.p.table, 2), [0, 1, 2, 3], c.p.len, y, y)
+        same_cache(c.c, c.d)
