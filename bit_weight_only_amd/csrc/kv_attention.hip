@@ -77,6 +77,15 @@ __device__ inline int kv_scale_exponent(float s) {
   return e < kKvExpMin ? kKvExpMin : e > kKvExpMax ? kKvExpMax : e;
 }
 
+// m only has to be near the maximum: it is raised, and the sums rescaled, when a
+// weight would pass 2^8 (as the first key's would).  The 2^30 keys that a
+// sequence may have then sum to less than 2^30 * 2^8 * 448 * 2^e, which fp32
+// holds up to e = 80.  In steps with a value scale over that, m is kept 27 over
+// the maximum: the weights are at most 2^-19, and 2^30 of them times 448 * 2^100
+// stay under 2^120.
+constexpr float kSlack = 8.0f, kLift = 27.0f;
+constexpr int kLiftExp = 80;
+
 // A lane's value as a scalar.
 __device__ inline float lane_float(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
@@ -294,6 +303,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   const int first = split * split_steps + wave;
   int page_l = -1;
   float kc_l = 0.0f, ve_l = 0.0f, vi_l = 1.0f;
+  uint64_t high_l = 0;  // bit 2s + h: that block's values need kLift
   auto block_of = [&](int page, int t0) {
     return ((layer_pages + page) * c.kv_heads + head) * page_blocks +
            ((t0 & (c.page_tokens() - 1)) >> 4);
@@ -314,6 +324,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     // (held to what a cache can have: a block that was never written may lie
     // past the last token, and 0 weight times its 2^-e has to be 0)
     const int ve = kv_scale_exponent(ve_l);
+    high_l = __ballot(ve > kLiftExp && page_l >= 0);
     ve_l = (float)ve;
     vi_l = __uint_as_float((uint32_t)(127 - ve) << 23);
   };
@@ -380,12 +391,11 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[h][e]);
-    // m only has to be near the maximum: it is raised, and the sums rescaled,
-    // when a weight would pass 2^8 (as the first key's would)
-    if (__any(mx > m + 8.0f)) {
+    const float lift = (high_l >> (2 * sl) & 3) != 0 ? kLift : 0.0f;
+    if (__any(mx > m + (kSlack - lift))) {
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float m_new = fmaxf(m, mx);
+      const float m_new = fmaxf(m, mx + lift);
       const float alpha = m_new == -INFINITY ? 1.0f : exp2_fast(m - m_new);
       m = m_new;
       l *= alpha;
@@ -679,13 +689,18 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       }
     }
     const uint8_t *vt = st + L::kV;
-    bool sees = true;  // whether the row sees any of these keys
+    float least = -INFINITY;  // of the m that weights are taken against
+    // blocks whose values need kLift (lanes 4 to 7 hold the values' exponents)
+    uint32_t high = (uint32_t)__ballot(ve_l > kLiftExp) & 0xF0u;
     if (hole != 0 || !visible.all(key0, kTileKeys, w_lo, w_hi)) {
       uint64_t bits = visible.bits(key0, pos);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (hole >> k & 1) bits &= ~(0xFFFFull << (16 * k));
-      sees = bits != 0;
+      // a row that has seen nothing yet has only -inf here, whose weights are to
+      // be 0; -inf or NaN that it does see makes them NaN
+      least = bits == 0 && m == -INFINITY ? 0.0f : -INFINITY;
+      high &= ~(hole << 4);  // a hole's exponent is another block's
       bits >>= 4 * h;
       // bit 8a + e for element 4a + e of s[u]
       const uint32_t see[2] = {(uint32_t)bits, (uint32_t)(bits >> 32)};
@@ -734,9 +749,10 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       t = max3(t, at(7), at(7));
       mx = fmaxf(mx, t * kc[k]);  // kc is positive and finite
     }
-    if (__any(mx > m + 8.0f)) {
+    const float lift = high != 0 ? kLift : 0.0f;
+    if (__any(mx > m + (kSlack - lift))) {
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float m_new = fmaxf(m, mx);
+      const float m_new = fmaxf(m, mx + lift);
       const float alpha = m_new == -INFINITY ? 1.0f : exp2_fast(m - m_new);
       m = m_new;
       l[0] *= alpha;
@@ -744,9 +760,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] *= alpha;
     }
-    // (a row that has seen nothing yet has only -inf here, which stays 0; if
-    // what it sees is NaN or -inf by itself, its weights become NaN)
-    const float base = m == -INFINITY && !sees ? 0.0f : m;
+    const float base = fmaxf(m, least);
     union {
       bf16x8 v[4];
       bf16x2 e[16];

@@ -10,6 +10,7 @@ namespace nf4 {
 constexpr int kKvBlock = 16;    // tokens under one scale
 constexpr int kKvExpMin = -40;  // exponents that a block's scale may have: the
 constexpr int kKvExpMax = 100;  // attention folds them into exponents of its weights
+                                // (kLift there keeps the sums in range)
 
 // The cache as a kernel sees it.  A page of one layer is kv_heads runs of
 // page_tokens * D bytes (k and v alike) and kv_heads * page_tokens / 16 scales.

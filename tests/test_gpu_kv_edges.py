@@ -214,3 +214,28 @@ def test_fork_and_go_on_past_a_full_table(side):
         y = x.double().cpu().numpy().reshape(3, 1, 64)
         kv.append(c.c, 0, with_holes(c.p.table, 2), [0, 1, 2, 3], c.p.len, y, y)
         same_cache(c.c, c.d)
+
+
+# ------------------------------------------------------------ the largest scale
+@pytest.mark.parametrize("heads,kv_heads,kv_len,count,low", [
+    (1, 1, [8192], [1], 512),                          # single token, the keys split
+    (1, 1, [9000], [40], 512),                         # two teams, split
+    (8, 8, [6000] + [9] * 19, [33] + [9] * 19, 10000),  # two teams, not split
+    (8, 8, [6000] + [9] * 39, [33] + [9] * 39, 10000)])  # one team
+def test_largest_values_over_many_keys(side, heads, kv_heads, kv_len, count, low):
+    """Values of 448 * 2^100 under thousands of equal weights, the first keys of
+    every `low` of them 2^-7.9 as heavy: the result is as large as the values,
+    and no sum on the way overflows."""
+    c = Case(side, 37, 64, 64, heads, kv_heads, kv_len, count)
+    c.q[:] = 0.0
+    c.q.reshape(-1, heads, 64)[..., 0] = 1.0
+    n = kv_len[0]
+    for page in c.table[0, :-(-n // 64)]:
+        c.c.k[0, page], c.c.v[0, page] = 0, 0x7E
+        c.c.ks[0, page], c.c.vs[0, page] = 1.0, 2.0 ** 100
+    for t in range(n):
+        if t % low >= 128:
+            for h in range(kv_heads):
+                c.c.codes(0, 0, c.table[0, t // 64], h, t % 64)[0] = 0x38
+    out, z = c.run(scale=7.9 * np.log(2))
+    assert np.isfinite(out).all() and np.isfinite(z).all()
