@@ -47,12 +47,13 @@ nf4_status check_cache(const nf4_kv_cache *c, nf4::KvCache &out) {
 bool batch_shape_ok(const nf4_kv_batch &b) {
   if (b.seqs < 1 || b.seqs > kMaxRows || b.rows < 1 || b.rows > kMaxRows) return false;
   if (b.max_rows < 1 || b.max_rows > b.rows || b.max_len < 0 || b.max_len > kMaxLen) return false;
-  return b.table_stride >= 1 && b.table_stride <= kMaxLen;
+  if (b.table_stride < 1 || b.table_stride > kMaxLen) return false;
+  return b.table_entries >= 0 && b.table_entries <= b.table_stride;
 }
 
 // No key lies past the table: a large max_len costs no launch size.
 nf4::KvBatch as_batch(const nf4_kv_batch &b, const nf4::KvCache &c) {
-  const int64_t room = b.table_stride << c.page_shift;
+  const int64_t room = (b.table_entries ? b.table_entries : b.table_stride) << c.page_shift;
   const bool held = b.max_len < room;
   return nf4::KvBatch{b.seqs, b.rows, (int)b.max_rows, (int)(held ? b.max_len : room),
                       held ? (int)b.max_len : INT32_MAX,

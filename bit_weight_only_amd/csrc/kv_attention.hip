@@ -275,11 +275,11 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   const uint32_t item = w * (uint32_t)c.kv_heads + head;
   const int32_t *table = b.table + seq * b.table_stride;
   // without a window, where the first page ids stand does not depend on the
-  // lengths: they are read beside them
+  // lengths: they are read beside them (as far as the longest one may reach)
   int page_ahead = -1;
   if (a.window == 0) {
     const int64_t t0 = (int64_t)(split * split_steps + wave + (lane >> 1) * W) * 32 + 16 * (lane & 1);
-    page_ahead = table[min(t0 >> c.page_shift, b.table_stride - 1)];
+    page_ahead = table[min(t0, (int64_t)max(b.max_len - 1, 0)) >> c.page_shift];
   }
   const Tile tl(c, b, a, seq, w % tiles, 16);
   if (tl.empty()) return;

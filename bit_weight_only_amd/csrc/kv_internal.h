@@ -33,7 +33,7 @@ struct KvCache {
 struct KvBatch {
   int64_t seqs, rows;
   int max_rows;
-  int max_len;   // no more than the table has room for
+  int max_len;   // no more than the table's entries have room for
   int held_len;  // what the host holds lengths to, 2^31 - 1 where only the table does
   const int32_t *row_start, *kv_len, *table;
   int64_t table_stride;

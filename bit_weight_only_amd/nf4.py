@@ -42,7 +42,7 @@ class _KVCache(ctypes.Structure):
 class _KVBatch(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in ("seqs", "rows", "max_rows", "max_len")] + \
                [(f, ctypes.c_void_p) for f in ("row_start", "kv_len", "table")] + \
-               [("table_stride", ctypes.c_int64)]
+               [("table_stride", ctypes.c_int64), ("table_entries", ctypes.c_int64)]
 
 
 class _KVPool(ctypes.Structure):
@@ -468,12 +468,14 @@ class KVCache:
 
 class KVBatch:
     """The new rows of a step: int32 device tensors kv_len [seqs] and table
-    [seqs][entries], row_start [seqs + 1] where sequences have other than one
-    row each, and the host's bounds on rows and lengths."""
+    [seqs][entries] (rows or columns of a wider one, too), row_start [seqs + 1]
+    where sequences have other than one row each, and the host's bounds on
+    rows and lengths."""
 
     def __init__(self, kv_len, table, row_start=None, rows=None, max_rows: int = 1, max_len=None):
         seqs = kv_len.numel()
-        if table.dim() != 2 or table.stride(1) != 1 or table.shape[0] < seqs or \
+        if table.dim() != 2 or table.shape[1] < 1 or table.stride(1) != 1 or \
+                table.shape[0] < seqs or (seqs > 1 and table.stride(0) < table.shape[1]) or \
                 (row_start is not None and row_start.numel() != seqs + 1):
             raise NF4Error(NF4_ERR_SHAPE, "KVBatch")
         self.kv_len, self.table, self.row_start = _int32(kv_len), table, row_start
@@ -482,7 +484,8 @@ class KVBatch:
                                (1 << 30) if max_len is None else max_len,
                                None if row_start is None else _int32(row_start).data_ptr(),
                                kv_len.data_ptr(), table.data_ptr(),
-                               max(table.stride(0), table.shape[1]))  # one row: any stride
+                               max(table.stride(0), table.shape[1]),  # one row: any stride
+                               table.shape[1])
         self.arg = ctypes.pointer(self.struct)
 
 

@@ -401,7 +401,7 @@ typedef struct nf4_kv_cache {
  * and max_len bound what any sequence has, as the host knows it: rows past
  * max_rows are not processed, lengths past max_len count as max_len (the rows'
  * positions follow, so that max_len must cover what is appended).  Where
- * max_len is no less than the tokens the table has room for, it bounds
+ * max_len is no less than the tokens the table's entries have room for, it bounds
  * nothing: a sequence that is longer than its table (nf4_kv_reserve lets it
  * become that) keeps its rows' positions, and its tokens past the table are
  * those of a hole, not written and never seen. */
@@ -412,6 +412,8 @@ typedef struct nf4_kv_batch {
   const int32_t *kv_len;     /* [seqs] tokens, the new ones included */
   const int32_t *table;      /* [seqs][table_stride] */
   int64_t table_stride;      /* >= 1 */
+  int64_t table_entries;     /* entries of a sequence, 1 .. table_stride, nothing past
+                                them is read; 0: table_stride */
 } nf4_kv_batch;
 
 /* Who owns which page.  refs[p] counts the table entries that name page p; 0

@@ -5,7 +5,7 @@ import pytest
 from oracle import kv
 
 from gpu_helpers import say
-from test_gpu_kv import Case, PoolCase, bf16, device_batch, device_cache, same_cache, side  # noqa: F401
+from test_gpu_kv import Case, PoolCase, bf16, device_batch, device_cache, i32, same_cache, side  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -239,3 +239,42 @@ def test_largest_values_over_many_keys(side, heads, kv_heads, kv_len, count, low
                 c.c.codes(0, 0, c.table[0, t // 64], h, t % 64)[0] = 0x38
     out, z = c.run(scale=7.9 * np.log(2))
     assert np.isfinite(out).all() and np.isfinite(z).all()
+
+
+@pytest.mark.parametrize("columns", [slice(0, 3), slice(2, 5), slice(6, 9)])
+def test_tables_that_are_columns_of_wider_ones(side, columns):
+    """Entries beside the view are other things' pages: sequences end with the view."""
+    rng = np.random.default_rng(60)
+    dim, heads, page = 64, 2, 16
+    wide = rng.permutation(27).reshape(3, 9).astype(np.int32)
+    kv_len, count = [48, 61, 200], [1, 20, 1]
+    c = kv.Cache(1, 27, heads, page, dim, rng)
+    d, t = device_cache(side, c), side.torch
+    start = np.concatenate([[0], np.cumsum(count)])
+    x = bf16(rng.normal(size=(start[-1], heads * dim)))
+    r, view = side.to_dev(x), i32(side, wide)[:, columns]
+    side.stream.wait_stream(t.cuda.current_stream())
+    b = side.nf4.KVBatch(i32(side, kv_len), view, row_start=i32(side, start), rows=int(start[-1]), max_rows=20)
+    side.stream.wait_stream(t.cuda.current_stream())
+    side.nf4.nf4_kv_append(d, 0, b, r, heads * dim, r, heads * dim, 1, stream=side.stream)
+    side.sync()
+    table = with_holes(wide[:, columns], 20)
+    y = x.reshape(-1, heads, dim).astype(np.float64)
+    kv.append(c, 0, table, start, kv_len, y, y)
+    same_cache(c, d)
+    for a in (c.k, c.v):
+        a[a & 127 == 127] = 0x30
+    d = device_cache(side, c)
+    for group in (1, 8):
+        h = heads * group
+        case = Case(side, 61, dim, page, h, heads, kv_len, count)
+        case.c, case.table, case.pages = c, table, 27
+        q = side.to_dev(case.q).bfloat16()
+        out, lse = t.empty_like(q), t.empty(len(q), h, dtype=t.float32, device="cuda")
+        n = side.nf4.nf4_kv_attention_workspace_bytes(d, b, h)
+        ws = t.empty(max(n, 16), dtype=t.uint8, device="cuda")
+        side.stream.wait_stream(t.cuda.current_stream())
+        say(f"[kv columns] {columns} group {group}")
+        side.nf4.nf4_kv_attention(d, 0, b, q, h * dim, h, 0.09, 0, 0, out, lse, ws, n, stream=side.stream)
+        side.sync()
+        case.check(out.float().cpu().numpy().reshape(-1, h, dim), lse.cpu().numpy(), 0, 0, 0.09)
