@@ -318,8 +318,27 @@ def nf4_kv_scale_bytes(cache) -> int:
     return lib().nf4_kv_scale_bytes(cache.arg)
 
 
+def _gpu(*tensors) -> int:
+    """The GPU that all the tensors lie on (None is left out), -1 if they do not."""
+    at = {t.device.index if t.is_cuda else -1 for t in tensors if t is not None}
+    return at.pop() if len(at) == 1 else -1
+
+
+def _on_gpu(where: str, *gpus: int) -> None:
+    """A kernel would take a host address as one of the GPU's."""
+    if gpus[0] < 0 or gpus[0] != gpus[-1]:
+        raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on one GPU")
+
+
+def _counted(where: str, cache, pool) -> None:
+    """The kernels go over the counts of all of the cache's pages."""
+    if pool.refs.numel() < cache.struct.pages:
+        raise NF4Error(NF4_ERR_SHAPE, f"{where}: fewer counts than pages")
+
+
 def nf4_kv_append(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, type: int,
                   stream=None) -> None:
+    _on_gpu("nf4_kv_append", cache.gpu, batch.gpu)
     _check(lib().nf4_kv_append(cache.arg, layer, batch.arg, _ptr(k), k_stride, _ptr(v), v_stride,
                                type, _stream(stream)), "nf4_kv_append")
 
@@ -332,27 +351,35 @@ def nf4_kv_attention_workspace_bytes(cache, batch, heads: int, window: int = 0,
 def nf4_kv_attention(cache, layer: int, batch, q, q_stride: int, heads: int, scale: float,
                      window: int, sinks: int, out, lse=None, workspace=None, ws_bytes: int = 0,
                      stream=None) -> None:
+    _on_gpu("nf4_kv_attention", cache.gpu, batch.gpu)
     _check(lib().nf4_kv_attention(cache.arg, layer, batch.arg, _ptr(q), q_stride, heads, scale,
                                   window, sinks, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
                                   _stream(stream)), "nf4_kv_attention")
 
 
 def nf4_kv_copy_pages(cache, src, dst, n: int, stream=None) -> None:
+    _on_gpu("nf4_kv_copy_pages", cache.gpu)
     _check(lib().nf4_kv_copy_pages(cache.arg, _ptr(src), _ptr(dst), n, _stream(stream)),
            "nf4_kv_copy_pages")
 
 
 def nf4_kv_reserve(cache, pool, add, stream=None) -> None:
+    _on_gpu("nf4_kv_reserve", pool.gpu)
+    _counted("nf4_kv_reserve", cache, pool)
     _check(lib().nf4_kv_reserve(cache.arg, pool.arg, _ptr(add), _stream(stream)),
            "nf4_kv_reserve")
 
 
 def nf4_kv_fork(cache, pool, src, dst, n: int, stream=None) -> None:
+    _on_gpu("nf4_kv_fork", cache.gpu, pool.gpu)
+    _counted("nf4_kv_fork", cache, pool)
     _check(lib().nf4_kv_fork(cache.arg, pool.arg, _ptr(src), _ptr(dst), n, _stream(stream)),
            "nf4_kv_fork")
 
 
 def nf4_kv_release(cache, pool, rows, n: int, stream=None) -> None:
+    _on_gpu("nf4_kv_release", pool.gpu)
+    _counted("nf4_kv_release", cache, pool)
     _check(lib().nf4_kv_release(cache.arg, pool.arg, _ptr(rows), n, _stream(stream)),
            "nf4_kv_release")
 
@@ -363,6 +390,8 @@ def nf4_kv_compact_workspace_bytes(cache) -> int:
 
 def nf4_kv_compact(cache, pool, refs_out, table_out, workspace, ws_bytes: int,
                    stream=None) -> None:
+    _on_gpu("nf4_kv_compact", cache.gpu, pool.gpu)
+    _counted("nf4_kv_compact", cache, pool)
     _check(lib().nf4_kv_compact(cache.arg, pool.arg, _ptr(refs_out), _ptr(table_out),
                                 _ptr(workspace), ws_bytes, _stream(stream)), "nf4_kv_compact")
 
@@ -436,8 +465,9 @@ def awq_pack_weight(W, stream=None) -> AwqWeight:
 
 
 class KVCache:
-    """A key-value cache's tensors (allocated zero-filled here, or given) and
-    the structure that names them to the library."""
+    """A key-value cache's tensors (allocated zero-filled here, or given, as the
+    codes' bytes and the float32 scales or as plain bytes) and the structure
+    that names them to the library."""
 
     def __init__(self, layers: int, pages: int, kv_heads: int, page_tokens: int, head_dim: int,
                  device="cuda", k=None, v=None, k_scale=None, v_scale=None):
@@ -460,10 +490,12 @@ class KVCache:
                     shape = (page_tokens, head_dim) if name == "k" else \
                         (page_tokens // 4, head_dim, 4)
                     given = torch.zeros(lead + shape, dtype=torch.uint8, device=device)
-            elif given.numel() * given.element_size() != size or not given.is_contiguous():
+            elif given.numel() * given.element_size() != size or not given.is_contiguous() or \
+                    (given.element_size() != 1 and (width == 1 or not _is_float32(given))):
                 raise NF4Error(NF4_ERR_SHAPE, "KVCache")
             setattr(self, name, given)
             setattr(self.struct, name, given.data_ptr())
+        self.gpu = _gpu(self.k, self.v, self.k_scale, self.v_scale)
 
 
 class KVBatch:
@@ -487,6 +519,7 @@ class KVBatch:
                                max(table.stride(0), table.shape[1]),  # one row: any stride
                                table.shape[1])
         self.arg = ctypes.pointer(self.struct)
+        self.gpu = _gpu(kv_len, table, row_start)
 
 
 class KVPool:
@@ -501,6 +534,12 @@ class KVPool:
                               _int32(length).data_ptr(),
                               None if missing is None else _int32(missing).data_ptr())
         self.arg = ctypes.pointer(self.struct)
+        self.gpu = _gpu(refs, table, length, missing)
+
+
+def _is_float32(t) -> bool:
+    import torch
+    return t.dtype == torch.float32
 
 
 def _int32(t):
