@@ -1016,9 +1016,16 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
                                const KvAttention &a, hipStream_t s) {
   const Plan p = make_plan(c, b, a.heads, a.window, a.sinks);
   const int64_t grid = p.items * p.splits;
+  // the join: as many turns as there are four parts for each, the rest of the
+  // threads on other rows
   const int64_t cols = std::min<int64_t>(p.width, (int64_t)b.max_rows * (a.heads / c.kv_heads));
-  if (grid > 0x7FFFFFFF / 512 || p.items * cols > 0x7FFFFFFF / 256)
-    return hipErrorInvalidConfiguration;
+  int turns = 256 / (c.head_dim / 4);
+  while (turns > 1 && p.splits <= 2 * turns) turns /= 2;
+  const int at_once = 256 / (c.head_dim / 4) / turns;
+  const int64_t groups = (cols + at_once - 1) / at_once;
+  // up to 2^31 threads a launch
+  if (grid > 0x7FFFFFFF / (256 * p.teams)) return hipErrorInvalidConfiguration;
+  if (p.splits > 1 && p.items * groups > 0x7FFFFFFF / 256) return hipErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256 * p.teams), 0, s, c, layer, b, a,
                        (uint32_t)p.tiles, (int)p.splits, p.split_steps);
@@ -1037,12 +1044,6 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  // as many turns as there are four parts for each, the rest of the threads on
-  // other rows
-  int turns = 256 / (c.head_dim / 4);
-  while (turns > 1 && p.splits <= 2 * turns) turns /= 2;
-  const int at_once = 256 / (c.head_dim / 4) / turns;
-  const int64_t groups = (cols + at_once - 1) / at_once;
   auto join = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * groups)), dim3(256), 0, s, c, b, a,
                        (uint32_t)p.tiles, p.width, (int)groups, turns, (int)p.splits,

@@ -382,7 +382,8 @@ nf4_status nf4_awq_gemm(const hip_bfloat16 *x, int64_t M, const uint8_t *qweight
  *
  * Every array named in the three structures below is device memory; the
  * structures are host memory, read during the call.  int32 arrays need
- * 4-byte alignment, all else 16.
+ * 4-byte alignment, all else 16.  A call that would launch 2^31 threads
+ * or more at a time returns NF4_ERR_SHAPE.
  * ------------------------------------------------------------------------ */
 
 typedef struct nf4_kv_cache {

@@ -278,3 +278,40 @@ def test_tables_that_are_columns_of_wider_ones(side, columns):
         side.nf4.nf4_kv_attention(d, 0, b, q, h * dim, h, 0.09, 0, 0, out, lse, ws, n, stream=side.stream)
         side.sync()
         case.check(out.float().cpu().numpy().reshape(-1, h, dim), lse.cpu().numpy(), 0, 0, 0.09)
+
+
+def test_one_long_prompt_among_many_short_sequences(side):
+    """A batch whose bound on rows makes many tiles, most of them empty."""
+    t, nf4 = side.torch, side.nf4
+    rng = np.random.default_rng(50)
+    heads, kv_heads, dim, page, n, others = 128, 8, 64, 64, 2000, 63
+    pages = -(-n // page) + others
+    c = kv.Cache(1, pages, kv_heads, page, dim, rng)
+    for a in (c.k, c.v):
+        a[a & 127 == 127] = 0x30
+    table = np.full((1 + others, -(-n // page)), -1, np.int32)
+    table[0] = np.arange(others, pages)
+    table[1:, 0] = np.arange(others)
+    d = device_cache(side, c)
+    q = side.to_dev(rng.normal(size=(n + others, heads * dim)).astype(np.float32)).bfloat16()
+
+    def run(rows, kv_len, start):
+        b = device_batch(side, table[rows], kv_len, start)
+        qs = q[:start[-1]]
+        out = t.empty_like(qs)
+        ws_bytes = nf4.nf4_kv_attention_workspace_bytes(d, b, heads)
+        ws = t.empty(max(ws_bytes, 16), dtype=t.uint8, device="cuda")
+        side.stream.wait_stream(t.cuda.current_stream())
+        say(f"[kv ragged] sequences={len(kv_len)} rows={start[-1]} ws={ws_bytes}")
+        nf4.nf4_kv_attention(d, 0, b, qs, qs.stride(0), heads, 0.1, 0, 0, out, None, ws, ws_bytes,
+                             stream=side.stream)
+        side.sync()
+        return out
+    short = [1 + i % page for i in range(others)]
+    both = run(slice(0, 1 + others), [n] + short, np.concatenate([[0], n + np.arange(1 + others)]))
+    alone = run(slice(0, 1), [n], np.array([0, n]))
+    assert t.equal(both[:n], alone)
+    case = Case(side, 51, dim, page, heads, kv_heads, short, [1] * others)
+    case.c, case.table, case.pages = c, table[1:], pages
+    case.q = q[n:].float().cpu().numpy()
+    case.check(both[n:].float().cpu().numpy().reshape(others, heads, dim), None, 0, 0, 0.1)
