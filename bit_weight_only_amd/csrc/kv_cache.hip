@@ -185,15 +185,18 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
 
 constexpr int kPlanThreads = 256;
 
-// Exclusive prefix sum of v over the workgroup's threads in thread order;
-// `total` gets the sum.  `part`: one int per wave in LDS.
+// Exclusive prefix sum of v (0 .. 2^28) over the workgroup's threads in thread
+// order; `total` gets the sum.  Both stop at kManyPages, more than a pool has:
+// 256 requests may pass 32 bits.  `part`: one int per wave in LDS.
+constexpr int kManyPages = 1 << 28;
+
 __device__ inline int block_prefix(int v, int *part, int &total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int x = v;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int y = __shfl_up(x, o);
-    if (lane >= o) x += y;
+    if (lane >= o) x = min(x + y, kManyPages);
   }
   __syncthreads();  // the previous call's reads of part are over
   if (lane == 63) part[wave] = x;
@@ -205,8 +208,9 @@ __device__ inline int block_prefix(int v, int *part, int &total) {
     before += w < wave ? p : 0;
     sum += p;
   }
-  total = sum;
-  return before + x - v;
+  total = min(sum, kManyPages);
+  const int below = __shfl_up(x, 1);
+  return min(before + (lane > 0 ? below : 0), kManyPages);
 }
 
 // Requests for pages, in an order that fixes which free page answers which:
@@ -254,7 +258,9 @@ struct ReserveRequests {
     return end > entry ? (int)(end - entry) : 0;
   }
   __device__ void done(const KvPool &p, int64_t i) const {
-    if (add[i] > 0) p.len[i] = (p.len[i] < 0 ? 0 : p.len[i]) + add[i];
+    if (add[i] <= 0) return;
+    const int64_t len = (int64_t)(p.len[i] < 0 ? 0 : p.len[i]) + add[i];
+    p.len[i] = (int)(len > 0x7FFFFFFF ? 0x7FFFFFFF : len);
   }
 };
 
@@ -306,20 +312,18 @@ __global__ __launch_bounds__(kPlanThreads) void assign_pages_kernel(KvCache c, K
   __shared__ int part[kPlanThreads / 64];
   __shared__ int first[kPlanThreads];        // number of an item's first request
   __shared__ int64_t where[kPlanThreads];    // table place of its first page
-  __shared__ int all_lost;
+  __shared__ unsigned long long missing;     // pages that requests did not get
   const int tid = threadIdx.x;
   int32_t refs[kRunGroups];
   read_run(c, p.refs, 0, refs);  // the first pages, beside the requests
-  if (tid == 0) all_lost = 0;
+  if (tid == 0) missing = 0;
   const int64_t items = rq.count() < 0 ? p.rows : rq.count();
-  int64_t missing = 0;
   for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
     const int64_t i = i0 + tid;
     int64_t row = 0, entry = 0;
     int lost = 0, want = 0, total;
     if (i < items) want = rq.ask(c, p, i, row, entry, lost);
     const int mine = block_prefix(want, part, total);
-    if (lost) atomicAdd(&all_lost, lost);
     first[tid] = mine;
     where[tid] = row * p.stride + entry;
     int found = 0;
@@ -351,16 +355,14 @@ __global__ __launch_bounds__(kPlanThreads) void assign_pages_kernel(KvCache c, K
       found += here;
     }
     found = found < total ? found : total;
-    for (int r = mine + (found > mine ? found - mine : 0); r < mine + want; ++r)
-      p.table[where[tid] + (r - mine)] = -1;
-    missing += total - found;
+    const int got = min(max(found - mine, 0), want);
+    for (int r = got; r < want; ++r) p.table[where[tid] + r] = -1;
+    if (lost + (want - got) > 0) atomicAdd(&missing, (unsigned long long)lost + (want - got));
     if (i < items) rq.done(p, i);
     __syncthreads();
   }
-  if (tid == 0 && p.missing) {
-    missing += all_lost;
+  if (tid == 0 && p.missing)
     *p.missing = (int32_t)(missing > 0x7FFFFFFF ? 0x7FFFFFFF : missing);
-  }
 }
 
 // Page copies are cut into pieces of 16 KB of codes per workgroup, four 16-byte

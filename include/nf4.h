@@ -498,8 +498,8 @@ nf4_status nf4_kv_copy_pages(const nf4_kv_cache *cache, const int32_t *src, cons
  * the entries from ceil(len / page_tokens) up to the new one get free pages,
  * the lowest page ids first, in order of rows and tokens.  Pages that the
  * pool or the table has no room for are counted in *missing (0 if there was
- * room for all) and leave holes.  Only pages, page_tokens and the like of
- * the cache are used. */
+ * room for all) and leave holes; lengths and counts stop at 2^31 - 1.  Only
+ * pages, page_tokens and the like of the cache are used. */
 nf4_status nf4_kv_reserve(const nf4_kv_cache *cache, const nf4_kv_pool *pool, const int32_t *add,
                           hipStream_t stream);
 

@@ -315,3 +315,23 @@ def test_one_long_prompt_among_many_short_sequences(side):
     case.c, case.table, case.pages = c, table[1:], pages
     case.q = q[n:].float().cpu().numpy()
     case.check(both[n:].float().cpu().numpy().reshape(others, heads, dim), None, 0, 0, 0.1)
+
+
+def test_reserve_counts_past_31_bits(side):
+    """Rows that ask for far more than there is: lengths and the count of
+    missing pages stop at 2^31 - 1."""
+    t, nf4 = side.torch, side.nf4
+    d = nf4.KVCache(1, 8, 1, 16, 64)
+    rows, top = 40, 2 ** 31 - 1
+    pool = nf4.KVPool(i32(side, np.zeros(8)), i32(side, np.full((rows, 2), -1)),
+                      i32(side, np.arange(rows)), i32(side, [5]))
+    add = i32(side, np.full(rows, top))
+    side.stream.wait_stream(t.cuda.current_stream())
+    for _ in range(2):
+        nf4.nf4_kv_reserve(d, pool, add, stream=side.stream)
+        side.sync()
+        assert pool.length.tolist() == [top] * rows
+        assert int(pool.missing) == top
+    assert pool.refs.tolist() == [1] * 8
+    # row 0 has no token yet, the others one page that this call did not have to give
+    assert pool.table.flatten().tolist()[:6] == [0, 1, -1, 2, -1, 3]
