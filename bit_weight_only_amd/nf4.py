@@ -151,9 +151,11 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        if torch.cuda.is_initialized():
-            # the raw handle: a Stream object first costs 2.9 us of a 6.5 us call
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the raw handle, where this torch gives it: a Stream object first costs
+        # 2.9 us of a 6.5 us call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -101,3 +101,15 @@ def test_a_pool_with_too_few_counts_is_refused():
         with pytest.raises(nf4.NF4Error, match="fewer counts than pages") as e:
             call()
         assert e.value.status == nf4.NF4_ERR_SHAPE
+
+
+@pytest.mark.parametrize("there", [True, False])
+def test_current_stream_with_and_without_the_raw_handle(monkeypatch, there):
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), {"cuda_stream": 0x40})())
+    if there:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0x30 + d, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert nf4._stream(None) == (0x33 if there else 0x40)
