@@ -56,7 +56,7 @@ nf4::KvBatch as_batch(const nf4_kv_batch &b, const nf4::KvCache &c) {
   const int64_t room = (b.table_entries ? b.table_entries : b.table_stride) << c.page_shift;
   const bool held = b.max_len < room;
   return nf4::KvBatch{b.seqs, b.rows, (int)b.max_rows, (int)(held ? b.max_len : room),
-                      held ? (int)b.max_len : INT32_MAX,
+                      held ? (int)b.max_len : nf4::kKvLongest,
                       b.row_start, b.kv_len, b.table, b.table_stride};
 }
 
@@ -92,8 +92,9 @@ bool attention_shape_ok(const nf4::KvCache &c, int64_t rows, int64_t heads, int6
   return window >= 0 && sinks >= 0;
 }
 
-// Windows and first tokens past any length are as good as the longest one.
-int held(int64_t v) { return (int)(v > kMaxLen ? kMaxLen : v); }
+// Windows and first tokens past any position are as good as the longest one.
+int held(int64_t v) { return (int)(v > nf4::kKvLongest ? nf4::kKvLongest : v); }
+static_assert(nf4::kKvLongest == kMaxLen + kMaxRows, "no row of the longest sequence is held");
 
 }  // namespace
 

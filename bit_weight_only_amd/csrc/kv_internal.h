@@ -12,6 +12,11 @@ constexpr int kKvExpMin = -40;  // exponents that a block's scale may have: the
 constexpr int kKvExpMax = 100;  // attention folds them into exponents of its weights
                                 // (kLift there keeps the sums in range)
 
+// Positions are held to this, and windows: the most tokens of a table that the
+// library reads and as many rows past them, so that a row there is past every
+// key, and positions less windows stay in 32 bits.
+constexpr int kKvLongest = (1 << 30) + (1 << 23);
+
 // The cache as a kernel sees it.  A page of one layer is kv_heads runs of
 // page_tokens * D bytes (k and v alike) and kv_heads * page_tokens / 16 scales.
 struct KvCache {
@@ -34,7 +39,7 @@ struct KvBatch {
   int64_t seqs, rows;
   int max_rows;
   int max_len;   // no more than the table's entries have room for
-  int held_len;  // what the host holds lengths to, 2^31 - 1 where only the table does
+  int held_len;  // what the host holds lengths to, kKvLongest where only the table does
   const int32_t *row_start, *kv_len, *table;
   int64_t table_stride;
 

@@ -405,7 +405,8 @@ typedef struct nf4_kv_cache {
  * max_len is no less than the tokens the table's entries have room for, it bounds
  * nothing: a sequence that is longer than its table (nf4_kv_reserve lets it
  * become that) keeps its rows' positions, and its tokens past the table are
- * those of a hole, not written and never seen. */
+ * those of a hole, not written and never seen.  (Lengths past 2^30 + 2^23, which
+ * max_len cannot be, count as that.) */
 typedef struct nf4_kv_batch {
   int64_t seqs, rows;        /* >= 1; rows of all sequences together */
   int64_t max_rows, max_len; /* 1 .. rows; 0 .. 2^30 */

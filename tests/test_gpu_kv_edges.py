@@ -335,3 +335,28 @@ def test_reserve_counts_past_31_bits(side):
     assert pool.refs.tolist() == [1] * 8
     # row 0 has no token yet, the others one page that this call did not have to give
     assert pool.table.flatten().tolist()[:6] == [0, 1, -1, 2, -1, 3]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1 << 40, 0), (1 << 31, 3), (1, 1 << 40)])
+def test_lengths_at_the_end_of_their_type(side, window, sinks):
+    """Rows at positions past 2^30 see what the table holds, and nothing is
+    written there."""
+    rng = np.random.default_rng(70)
+    dim, heads, page = 64, 2, 16
+    table = np.array([[4, 1, 6], [0, 5, 2]], np.int32)
+    for group, count in ((1, 1), (24, 2)):
+        case = Case(side, 71, dim, page, heads * group, heads, [48, 48], [count, count])
+        case.c, case.table, case.pages = kv.Cache(1, 8, heads, page, dim, rng), table, 8
+        for a in (case.c.k, case.c.v):
+            a[a & 127 == 127] = 0x30
+        case.kv_len = [2 ** 31 - 1, 2 ** 30 + 5]
+        out, z = case.run(window, sinks, check=False, max_len=None)
+        case.kv_len, case.table = [48 + count] * 2, with_holes(table, 3)
+        case.check(out, z, 0, 0, 0.09)  # as rows just past the table that see it all
+        d = device_cache(side, case.c)
+        x = side.to_dev(np.ones((2 * count, heads * dim), np.float32))
+        b = device_batch(side, table, [2 ** 31 - 1, 2 ** 30 + 5], case.start, max_len=None)
+        side.stream.wait_stream(side.torch.cuda.current_stream())
+        side.nf4.nf4_kv_append(d, 0, b, x, heads * dim, x, heads * dim, 1, stream=side.stream)
+        side.sync()
+        same_cache(case.c, d)
