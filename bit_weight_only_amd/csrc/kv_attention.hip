@@ -517,7 +517,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 // take 32 matrix instructions of 32 cycles, and widening the codes 128 vector
 // instructions, the softmax some 130 and 32 exponentials, 4 and 8 cycles each.
 // 14449 rows of 28 heads over 4: 1385 to 1430 us = 1045 to 1080 TFLOP/s, the
-// vector unit busy 0.73 of the time and the matrix cores 0.50; a product of
+// vector unit busy 0.74 of the time and the matrix cores 0.50; a product of
 // large bf16 matrices reaches 1222 TFLOP/s.  Keys and values widened once per
 // workgroup, bf16 in LDS, took 1538 us (LDS is then full), the scores of the
 // next 32 keys beside the weights of these 1486 us.
@@ -957,24 +957,33 @@ struct Plan {
 // 15.2 with 8).  Splitting costs the second launch, so a call whose rows all
 // see at most that many steps is not split (48 sequences with a window of
 // 1500: 20.4 us, split in two 25.5 us).
+// Up to 32 rows: 16 sequences of up to 8000 tokens, 32 heads over 4: 32 rows 30.4
+// us, as a tile of many rows 31.9; 40 rows 46.9 as three tiles of few, 32.9 as
+// one of many, and 64 sequences of up to 500 19.5 and 12.4.  (One sequence alone
+// favours tiles of few: 35 rows over 14449 tokens 15.5 us, 17.1 as one of many.)
+// At most 256 parts: one sequence of 10^6 tokens, one kv head, takes 48.9 us,
+// 99.7 in at most 64 parts, 52.9 in at most 1024.
 constexpr int kWaves = 4;
 constexpr int64_t kMinSteps = 16, kMostSteps = 64, kMaxSplits = 256;
+constexpr int64_t kFewRows = 32;
 
 // Many rows: no more tiles than compute units leave a unit one workgroup, and a
 // SIMD one wave, which waits for its own products half of the time: then two
 // teams of waves share a tile (1024 rows of 28 heads over 4, 224 tiles: 27.0 us
-// against 29.3; and 23.7, by now 22.4, with a late and an early half in every
+// against 29.3; and 23.7, by now 22.5, with a late and an early half in every
 // tile, so that none has more keys to go through), and the keys are split as far as one
 // workgroup per unit goes, in parts of 8 steps at least (113 rows over 14449
 // tokens, 28 tiles: 9 parts of two teams 49 us, 18 parts of one 55 us, 10
-// parts, past one workgroup per unit, 75 us).
+// parts, past one workgroup per unit, 75 us).  Parts of 4 steps at least instead:
+// 26.9 us against 25.1 for 300 rows over 3000 tokens, 8 heads over 2, 13.1
+// against 15.1 for 40 rows over 2000, 8 heads; of 16: 29.3 and 20.1.
 constexpr int64_t kMinTileSteps = 8;
 
 Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
   Plan p;
   const int64_t group = heads / c.kv_heads, rows = b.max_rows * group, cus = device_cu_count();
   p.teams = 1;
-  p.few = rows <= 32;
+  p.few = rows <= kFewRows;
   p.width = p.few ? 16 : kTileRows;
   p.keys = p.few ? 32 : kTileKeys;
   p.tiles = (rows + p.width - 1) / p.width;
@@ -987,6 +996,10 @@ Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int si
     per = even < kMinSteps ? kMinSteps : even > kMostSteps ? kMostSteps : even;
     per = (per + kWaves - 1) / kWaves * kWaves;
     // sixteen tiles for every compute unit fill the card evenly by themselves
+    // (512 sequences of up to 4000 tokens, 8 kv heads of 64: 198 us, split 224;
+    // two tiles for each do not: 64 sequences above.  Eight, which are split,
+    // would do better without: 256 sequences of up to 4000, 32 heads over 8, 127
+    // us, unsplit 110)
     if (p.items >= 16 * cus) per = steps;
   } else {
     per = steps;

@@ -63,9 +63,12 @@ struct Rows {
 // dwords of a quad of values and pieces of four key rows.  Memory bound: the
 // new rows are read once and their codes written once; a block that was full
 // in part also has its old codes read, once more written where the scale grew.
-// 14449 fp32 tokens of 8 heads of 128 (148 MB): 26 us in a trace = 5.7 TB/s; a
-// single token 4.5 us, three dependent trips to memory after an empty launch's
-// 1.6.
+// 14449 fp32 tokens of 8 heads of 128 (148 MB): 26 us in a trace = 5.7 TB/s.  A
+// single token, 4.7 us of which 1.6 an empty launch, is bound by trips to memory
+// one after the other: its place among the rows, the length, the page id beside
+// the rows, the old scale, and then the VEC dwords of the quad of values that it
+// is a byte of, each read, merged and stored before the next is read, since the
+// stores might change what the reads see.
 template <bool F32, int D>
 __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, KvBatch b, Rows x,
                                                      int64_t blocks_per_seq) {
@@ -366,9 +369,12 @@ __global__ __launch_bounds__(kPlanThreads) void assign_pages_kernel(KvCache c, K
 }
 
 // Page copies are cut into pieces of 16 KB of codes per workgroup, four 16-byte
-// loads in flight for each of 256 lanes (eight: a third slower).  Memory bound:
-// 32 forks of a page of 1.8 MB each (28 layers) 25 us = 4.7 TB/s, the 465 MB of
-// a compaction 107 us = 4.3 TB/s; a large copy reaches 5.1.
+// loads for each of 256 lanes.  The compiler holds what is loaded in LDS (16 KB a
+// workgroup) and waits for each load before the next, so that a lane has one in
+// flight, and the many workgroups are what keeps the memory busy (pieces twice
+// as large, which halve them: a third slower).  Memory bound: 32 forks of a page
+// of 1.8 MB each (28 layers) 25 us = 4.7 TB/s, the 465 MB of a compaction 107 us
+// = 4.3 TB/s; a large copy reaches 5.1.
 constexpr int kPieceLoads = 4;
 constexpr int kPieceBytes = kPieceLoads * 256 * 16;
 

@@ -504,7 +504,8 @@ class KVBatch:
     """The new rows of a step: int32 device tensors kv_len [seqs] and table
     [seqs][entries] (rows or columns of a wider one, too), row_start [seqs + 1]
     where sequences have other than one row each, and the host's bounds on
-    rows and lengths."""
+    rows (in all, by default one for each sequence, and of one sequence, by
+    default 1) and lengths: rows past them are not processed."""
 
     def __init__(self, kv_len, table, row_start=None, rows=None, max_rows: int = 1, max_len=None):
         seqs = kv_len.numel()

@@ -477,7 +477,9 @@ size_t nf4_kv_attention_workspace_bytes(const nf4_kv_cache *cache, const nf4_kv_
  * the products exactly, q as the bf16 values it holds, the weights exp(s -
  * max) rounded to bf16 (up to 32 rows of a kv head: to two bf16 terms); sums
  * are fp32, and the one that the result is divided by is of the unrounded
- * weights.  Bitwise reproducible run to run for a given device.
+ * weights.  Bitwise reproducible run to run for a given device.  max_rows picks
+ * the kernel for the whole call: long prompts and single tokens together are
+ * right, but take less time as two calls.
  *
  * workspace: at least nf4_kv_attention_workspace_bytes bytes, any contents
  * (NULL when that is 0); calls sharing one must be ordered.  scale must be finite and
