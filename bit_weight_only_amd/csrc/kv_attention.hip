@@ -86,6 +86,11 @@ __device__ inline int kv_scale_exponent(float s) {
 constexpr float kSlack = 8.0f, kLift = 27.0f;
 constexpr int kLiftExp = 80;
 
+// m of a row that saw keys whose scores are all NaN or -inf (past the range of
+// 32 bits): NaN ones make its sums NaN, -inf ones have weight 0, and any finite
+// score raises m.  So m is -inf for a row that saw no key, and only for that.
+constexpr float kLeast = -3.402823466e38f;
+
 // A lane's value as a scalar.
 __device__ inline float lane_float(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
@@ -174,12 +179,9 @@ __device__ inline uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Adds sums (m, l, x) of other keys to (mm, ll, xx).  l is 0 where no key was
-// seen, and only there: the key at m has a weight.  m says less, since it leaves
-// NaN scores out and is -inf still if there were no others; l and x are NaN then
-// and make the result NaN.
+// Adds sums (m, l, x) of other keys to (mm, ll, xx).
 __device__ inline void join(float &mm, float &ll, f32x4 &xx, float m, float l, f32x4 x) {
-  if (l == 0.0f) return;  // no key of these was seen
+  if (m == -INFINITY) return;  // no key of these was seen
   const float top = fmaxf(mm, m);
   const float f = exp2_fast(mm - top), g = exp2_fast(m - top);
   ll = ll * f + l * g;
@@ -187,18 +189,24 @@ __device__ inline void join(float &mm, float &ll, f32x4 &xx, float m, float l, f
   mm = top;
 }
 
+// The log of a row's sum of weights: -inf if it saw no key, NaN if it has no sum.
+__device__ inline float log_sum(float m, float l) {
+  if (m == -INFINITY) return m;
+  return l == 0.0f ? NAN : (m + __log2f(l)) * kLn2;
+}
+
 // The result of row `cc` of a tile, values d .. d + 3, from its sums.
 __device__ inline void store_row(const KvCache &c, const KvAttention &a, const Tile &tl, int head,
                                  int cc, int d, f32x4 x, float m, float l) {
   const uint32_t r = tl.r0 + cc;
   const int64_t at = (tl.row0 + r / tl.group) * a.heads + head * tl.group + r % tl.group;
-  const bool none = l == 0.0f;  // no key was seen
-  const float inv = none ? 0.0f : 1.0f / l;
+  const bool none = m == -INFINITY;  // no key was seen
+  const float inv = 1.0f / l;
   uint2 y;
   y.x = none ? 0u : bf16_pair(x[0] * inv, x[1] * inv);
   y.y = none ? 0u : bf16_pair(x[2] * inv, x[3] * inv);
   *reinterpret_cast<uint2 *>(a.out + at * c.head_dim + d) = y;
-  if (a.lse && d == 0) a.lse[at] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
+  if (a.lse && d == 0) a.lse[at] = log_sum(m, l);
 }
 
 // NaN codes in places that some row does not see would reach it as 0 * NaN, so
@@ -386,7 +394,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
           if (!v) s[h][e] = -INFINITY;
         }
     }
-    float mx = s[0][0];
+    float mx = see != 0 ? kLeast : -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -493,8 +501,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 #pragma unroll
     for (int v = 0; v < W; ++v) {
       const float mv = ml[0][v][cc];
-      const float lv = ml[1][v][cc];
-      ll += lv == 0.0f ? 0.0f : lv * exp2_fast(mv - mm);  // (0: no key was seen)
+      ll += mv == -INFINITY ? 0.0f : ml[1][v][cc] * exp2_fast(mv - mm);
       x += *reinterpret_cast<const f32x4 *>(sums + (v * 16 + cc) * PITCH + d);
     }
     if (splits == 1) {
@@ -689,7 +696,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       }
     }
     const uint8_t *vt = st + L::kV;
-    float least = -INFINITY;  // of the m that weights are taken against
+    float mx = kLeast;
     // blocks whose values need kLift (lanes 4 to 7 hold the values' exponents)
     uint32_t high = (uint32_t)__ballot(ve_l > kLiftExp) & 0xF0u;
     if (hole != 0 || !visible.all(key0, kTileKeys, w_lo, w_hi)) {
@@ -697,9 +704,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (hole >> k & 1) bits &= ~(0xFFFFull << (16 * k));
-      // a row that has seen nothing yet has only -inf here, whose weights are to
-      // be 0; -inf or NaN that it does see makes them NaN
-      least = bits == 0 && m == -INFINITY ? 0.0f : -INFINITY;
+      mx = bits != 0 ? kLeast : -INFINITY;
       high &= ~(hole << 4);  // a hole's exponent is another block's
       bits >>= 4 * h;
       // bit 8a + e for element 4a + e of s[u]
@@ -738,7 +743,6 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       }
     }
     float kc[4];
-    float mx = -INFINITY;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       kc[k] = lane_float(kc_l, k);
@@ -760,7 +764,8 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] *= alpha;
     }
-    const float base = fmaxf(m, least);
+    // (a row that has seen nothing yet has only -inf here, which stays 0)
+    const float base = m == -INFINITY ? 0.0f : m;
     union {
       bf16x8 v[4];
       bf16x2 e[16];
@@ -842,9 +847,8 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   if (r0 + my_col >= tl.rows) return;
   // element 4a + e of tile t is value DT (8a + 4h + e) + t
   if (splits == 1) {
-    const bool none = sum == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / sum;
-    const uint32_t keep = none ? 0u : ~0u;
+    const float inv = 1.0f / sum;
+    const uint32_t keep = m == -INFINITY ? 0u : ~0u;  // no key was seen
     const uint32_t row = r0 + my_col;
     const int64_t at = (tl.row0 + row / tl.group) * a.heads + head * tl.group + row % tl.group;
     uint16_t *to = a.out + at * D + my_h * (4 * DT);
@@ -861,7 +865,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
         *reinterpret_cast<uint4 *>(to + i * 8 * DT + 8 * x) =
             make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
     }
-    if (a.lse && my_h == 0) a.lse[at] = none ? -INFINITY : (m + __log2f(sum)) * kLn2;
+    if (a.lse && my_h == 0) a.lse[at] = log_sum(m, sum);
     return;
   }
   const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;

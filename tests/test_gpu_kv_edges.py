@@ -5,7 +5,7 @@ import pytest
 from oracle import kv
 
 from gpu_helpers import say
-from test_gpu_kv import Case, PoolCase, bf16, device_batch, device_cache, i32, same_cache, side  # noqa: F401
+from test_gpu_kv import Case, PoolCase, bf16, bounds, device_batch, device_cache, i32, same_cache, side  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -360,3 +360,32 @@ def test_lengths_at_the_end_of_their_type(side, window, sinks):
         side.nf4.nf4_kv_append(d, 0, b, x, heads * dim, x, heads * dim, 1, stream=side.stream)
         side.sync()
         same_cache(case.c, d)
+
+
+@pytest.mark.parametrize("form", range(len(NAN_FORMS)))
+@pytest.mark.parametrize("first", [True, False])
+def test_scores_past_the_least_float_have_no_weight(side, form, first):
+    """Keys whose scores are under -2^128 (-infinity in 32 bits), before or
+    after all others: the rest of the keys make the result."""
+    heads, kv_heads, kv_len, count = NAN_FORMS[form]
+    page = 16
+    n = kv_len[0]
+    c = Case(side, 38, 64, page, heads, kv_heads, kv_len, count)
+    c.c.k[..., 5] = 0
+    c.q.reshape(-1, heads, 64)[..., 5] = -2.0 ** 33
+    # (the last row of sequence 0 sees other keys in either case)
+    entries = range(0, max(1, n // 3 // page)) if first else range((n - 1) // page - max(0, n // 3 // page), (n - 1) // page)
+    for e in entries:
+        p = c.table[0, e]
+        c.c.k[0, p], c.c.ks[0, p] = 0, 2.0 ** 100
+        c.c.k[0, p, :, :, 5] = 0x7E
+    out, z = c.run(check=False)
+    rows = count[0]
+    c.table[0, entries.start:entries.stop] = -1  # as if they were not there
+    q = c.q.reshape(-1, heads, 64).astype(np.float64)
+    want, lse, mag, big = kv.attention(c.c, 0, c.table, c.start, c.kv_len, q, float(np.float32(0.09)), 0, 0)
+    ok = ~np.isneginf(lse[:rows])  # rows that see nothing else are 0 / 0
+    tol, tol_lse = bounds(64, n, want, lse, mag, big)
+    assert ok[-1].all()
+    assert (np.abs(out - want) <= tol)[:rows][ok].all()
+    assert (np.abs(z - lse) <= tol_lse)[:rows][ok].all()
