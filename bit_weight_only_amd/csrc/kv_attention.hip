@@ -524,7 +524,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
 // take 32 matrix instructions of 32 cycles, and widening the codes 128 vector
 // instructions, the softmax some 130 and 32 exponentials, 4 and 8 cycles each.
 // 14449 rows of 28 heads over 4: 1385 to 1430 us = 1045 to 1080 TFLOP/s, the
-// vector unit busy 0.74 of the time and the matrix cores 0.50; a product of
+// vector unit busy 0.73 of the time and the matrix cores 0.50; a product of
 // large bf16 matrices reaches 1222 TFLOP/s.  Keys and values widened once per
 // workgroup, bf16 in LDS, took 1538 us (LDS is then full), the scores of the
 // next 32 keys beside the weights of these 1486 us.
@@ -974,7 +974,7 @@ constexpr int64_t kFewRows = 32;
 // Many rows: no more tiles than compute units leave a unit one workgroup, and a
 // SIMD one wave, which waits for its own products half of the time: then two
 // teams of waves share a tile (1024 rows of 28 heads over 4, 224 tiles: 27.0 us
-// against 29.3; and 23.7, by now 22.5, with a late and an early half in every
+// against 29.3; and 23.7, by now 22.2, with a late and an early half in every
 // tile, so that none has more keys to go through), and the keys are split as far as one
 // workgroup per unit goes, in parts of 8 steps at least (113 rows over 14449
 // tokens, 28 tiles: 9 parts of two teams 49 us, 18 parts of one 55 us, 10
