@@ -20,7 +20,7 @@ OUT = os.path.join(PKG, "libnf4.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["nf4_abi.hip", "pack.hip", "gemv.hip", "gemm.hip", "kv_abi.hip", "kv_cache.hip",
-           "kv_attention.hip"]
+           "kv_rotary.hip", "kv_attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [

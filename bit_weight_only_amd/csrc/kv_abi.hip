@@ -92,6 +92,29 @@ bool attention_shape_ok(const nf4::KvCache &c, int64_t rows, int64_t heads, int6
   return window >= 0 && sinks >= 0;
 }
 
+bool type_ok(int type) { return type == NF4_KV_BF16 || type == NF4_KV_F32; }
+
+// Rows of `width` values: a stride that holds them, in whole 16-byte pieces.
+nf4_status check_rows(const void *p, int64_t stride, int64_t width, nf4_kv_type type) {
+  if (stride < width || stride > kMaxElems) return NF4_ERR_SHAPE;
+  return aligned(p, 16) && stride % (type == NF4_KV_F32 ? 4 : 8) == 0 ? NF4_OK : NF4_ERR_ALIGN;
+}
+
+// The norms' eps: what is divided by stays a normal float.
+bool eps_ok(float eps) { return isfinite(eps) && eps >= 0x1p-100f; }
+
+nf4_status check_rotary(const nf4_rotary *r, int64_t head_dim, nf4::KvRotary &out) {
+  if (!r) return NF4_ERR_NULL;
+  if (r->dims < 0 || r->dims > head_dim || r->dims % 2 != 0) return NF4_ERR_SHAPE;
+  if (r->layout != NF4_ROTARY_HALVES && r->layout != NF4_ROTARY_PAIRS) return NF4_ERR_SHAPE;
+  if (!isfinite(r->gain)) return NF4_ERR_SHAPE;
+  out.dims = (int)r->dims;
+  out.pairs = r->layout == NF4_ROTARY_PAIRS;
+  out.gain = r->gain;
+  for (int i = 0; i < 64; ++i) out.turns[i] = r->turns[i];
+  return NF4_OK;
+}
+
 // Windows and first tokens past any position are as good as the longest one.
 int held(int64_t v) { return (int)(v > nf4::kKvLongest ? nf4::kKvLongest : v); }
 static_assert(nf4::kKvLongest == kMaxLen + kMaxRows, "no row of the longest sequence is held");
@@ -130,6 +153,144 @@ nf4_status nf4_kv_append(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_
     return NF4_ERR_ALIGN;
   return from_hip(nf4::launch_kv_append(c, layer, b, k, k_stride, v, v_stride,
                                         type == NF4_KV_F32, stream));
+}
+
+nf4_status nf4_rotary_frequencies(int64_t dims, double base, nf4_rotary_scaling scaling,
+                                  double factor, double original, double low, double high,
+                                  double *frequency) {
+  if (!frequency) return NF4_ERR_NULL;
+  if (dims < 0 || dims > 128 || dims % 2 != 0) return NF4_ERR_SHAPE;
+  if (!isfinite(base) || !(base > 1.0)) return NF4_ERR_SHAPE;
+  if (scaling < NF4_SCALING_PLAIN || scaling > NF4_SCALING_SMOOTH) return NF4_ERR_SHAPE;
+  const bool by_turns = scaling == NF4_SCALING_RAMP || scaling == NF4_SCALING_SMOOTH;
+  if (scaling != NF4_SCALING_PLAIN && (!isfinite(factor) || !(factor > 0.0))) return NF4_ERR_SHAPE;
+  if (by_turns && (!isfinite(original) || !isfinite(high) || !(original > 0.0) || !(low > 0.0) ||
+                   !(high > low)))
+    return NF4_ERR_SHAPE;
+  const double turn = 2.0 * M_PI, n = (double)dims;
+  if (scaling == NF4_SCALING_BASE && dims > 2) base *= pow(factor, n / (n - 2.0));
+  if (!isfinite(base) || !(base > 1.0)) return NF4_ERR_SHAPE;
+  // number of the pair that makes so many turns over the original context
+  auto pair = [&](double turns) { return n * log(original / (turns * turn)) / (2.0 * log(base)); };
+  double from = 0.0, to = 0.0;
+  if (scaling == NF4_SCALING_RAMP) {
+    from = fmax(floor(pair(high)), 0.0);
+    to = fmin(ceil(pair(low)), n - 1.0);
+    if (from == to) to += 0.001;
+  }
+  for (int64_t i = 0; i < dims / 2; ++i) {
+    const double f = pow(base, -2.0 * (double)i / n);
+    double kept = 1.0;  // how much of f stays as it is, the rest divided by the factor
+    if (scaling == NF4_SCALING_LINEAR) kept = 0.0;
+    if (scaling == NF4_SCALING_RAMP) kept = 1.0 - ((double)i - from) / (to - from);
+    if (scaling == NF4_SCALING_SMOOTH) kept = (original * f / turn - low) / (high - low);
+    kept = fmin(fmax(kept, 0.0), 1.0);
+    frequency[i] = kept == 1.0 ? f : f * kept + f / factor * (1.0 - kept);
+  }
+  return NF4_OK;
+}
+
+nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout layout,
+                           const double *frequency, double gain) {
+  if (!rotary || (!frequency && dims > 0)) return NF4_ERR_NULL;
+  if (dims < 0 || dims > 128 || dims % 2 != 0 || !isfinite(gain)) return NF4_ERR_SHAPE;
+  if (layout != NF4_ROTARY_HALVES && layout != NF4_ROTARY_PAIRS) return NF4_ERR_SHAPE;
+  for (int64_t i = 0; i < dims / 2; ++i)
+    if (!(fabs(frequency[i]) <= 0x1p20)) return NF4_ERR_SHAPE;
+  rotary->dims = dims;
+  rotary->layout = layout;
+  rotary->gain = gain;
+  for (int64_t i = 0; i < 64; ++i) {
+    uint64_t turns = 0;
+    if (i < dims / 2) {
+      // the part of a turn past the last whole one, in 80 bits: 2^-65 of a turn off
+      long double t = (long double)frequency[i] / 6.283185307179586476925286766559L;
+      t -= floorl(t);
+      t = rintl(ldexpl(t, 64));
+      turns = t >= 0x1p64L ? 0 : (uint64_t)t;
+    }
+    rotary->turns[i] = turns;
+  }
+  return NF4_OK;
+}
+
+nf4_status nf4_rotate(const nf4_rotary *rotary, const void *x, int64_t x_stride,
+                      nf4_kv_type x_type, const int32_t *positions, int64_t rows, int64_t heads,
+                      int64_t head_dim, const float *weight, float eps, void *y, int64_t y_stride,
+                      nf4_kv_type y_type, hipStream_t stream) {
+  nf4::KvRotary rot;
+  if (!x || !positions || !y) return NF4_ERR_NULL;
+  if (head_dim != 64 && head_dim != 128) return NF4_ERR_SHAPE;
+  nf4_status st = check_rotary(rotary, head_dim, rot);
+  if (st != NF4_OK) return st;
+  if (rows < 1 || rows > kMaxRows || heads < 1 || heads > kMaxHeads * 64) return NF4_ERR_SHAPE;
+  if (!type_ok(x_type) || !type_ok(y_type) || (weight && !eps_ok(eps))) return NF4_ERR_SHAPE;
+  if ((st = check_rows(x, x_stride, heads * head_dim, x_type)) != NF4_OK) return st;
+  if ((st = check_rows(y, y_stride, heads * head_dim, y_type)) != NF4_OK) return st;
+  // in place each value's reader is its writer only where it stays where it was
+  if (x == y && (x_stride != y_stride || x_type != y_type)) return NF4_ERR_SHAPE;
+  if (!aligned(positions, 4) || !aligned(weight, 16)) return NF4_ERR_ALIGN;
+  return from_hip(nf4::launch_rotate(rot, {const_cast<void *>(x), x_stride, x_type == NF4_KV_F32},
+                                     positions, rows, (int)heads, (int)head_dim, weight, eps,
+                                     {y, y_stride, y_type == NF4_KV_F32}, stream));
+}
+
+nf4_status nf4_kv_append_rotated(const nf4_kv_cache *cache, int64_t layer,
+                                 const nf4_kv_batch *batch, const nf4_rotary *rotary, const void *q,
+                                 int64_t q_stride, int64_t heads, const float *q_weight,
+                                 const void *k, int64_t k_stride, const float *k_weight,
+                                 const void *v, int64_t v_stride, nf4_kv_type type, float eps,
+                                 hip_bfloat16 *q_out, hipStream_t stream) {
+  nf4::KvCache c;
+  nf4::KvBatch b;
+  nf4::KvRotary rot;
+  if (!q || !k || !v || !q_out) return NF4_ERR_NULL;
+  nf4_status st = check_cache(cache, c);
+  if (st != NF4_OK) return st;
+  if ((st = check_batch(batch, c, b)) != NF4_OK) return st;
+  if ((st = check_rotary(rotary, c.head_dim, rot)) != NF4_OK) return st;
+  if (layer < 0 || layer >= c.layers || !type_ok(type)) return NF4_ERR_SHAPE;
+  if (heads < 1 || heads > kMaxHeads * 64 || heads % c.kv_heads != 0 ||
+      b.rows * heads > int64_t(1) << 31)
+    return NF4_ERR_SHAPE;
+  if ((q_weight || k_weight) && !eps_ok(eps)) return NF4_ERR_SHAPE;
+  const int64_t width = (int64_t)c.kv_heads * c.head_dim;
+  if ((st = check_rows(q, q_stride, heads * c.head_dim, type)) != NF4_OK) return st;
+  if ((st = check_rows(k, k_stride, width, type)) != NF4_OK) return st;
+  if ((st = check_rows(v, v_stride, width, type)) != NF4_OK) return st;
+  if (q == q_out && (type != NF4_KV_BF16 || q_stride != heads * c.head_dim)) return NF4_ERR_SHAPE;
+  if (!aligned(q_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16)) return NF4_ERR_ALIGN;
+  const int64_t size = type == NF4_KV_F32 ? 4 : 2;
+  const nf4::KvTurned a{static_cast<const uint8_t *>(q),
+                        static_cast<const uint8_t *>(k),
+                        static_cast<const uint8_t *>(v),
+                        q_stride * size,
+                        k_stride * size,
+                        v_stride * size,
+                        (int)heads,
+                        q_weight,
+                        k_weight,
+                        eps,
+                        reinterpret_cast<uint16_t *>(q_out)};
+  return from_hip(
+      nf4::launch_kv_append_rotated(c, layer, b, rot, a, type == NF4_KV_F32, stream));
+}
+
+nf4_status nf4_kv_read(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch, void *k,
+                       int64_t k_stride, void *v, int64_t v_stride, nf4_kv_type type,
+                       hipStream_t stream) {
+  nf4::KvCache c;
+  nf4::KvBatch b;
+  if (!k || !v) return NF4_ERR_NULL;
+  nf4_status st = check_cache(cache, c);
+  if (st != NF4_OK) return st;
+  if ((st = check_batch(batch, c, b)) != NF4_OK) return st;
+  if (layer < 0 || layer >= c.layers || !type_ok(type)) return NF4_ERR_SHAPE;
+  const int64_t width = (int64_t)c.kv_heads * c.head_dim;
+  if ((st = check_rows(k, k_stride, width, type)) != NF4_OK) return st;
+  if ((st = check_rows(v, v_stride, width, type)) != NF4_OK) return st;
+  const bool f32 = type == NF4_KV_F32;
+  return from_hip(nf4::launch_kv_read(c, layer, b, {k, k_stride, f32}, {v, v_stride, f32}, stream));
 }
 
 size_t nf4_kv_attention_workspace_bytes(const nf4_kv_cache *cache, const nf4_kv_batch *batch,

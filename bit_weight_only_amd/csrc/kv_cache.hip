@@ -6,52 +6,10 @@
 // slots of a server share.  The block format, its scales and every rule of the pool are this
 // library's own (include/nf4.h states them).
 #include "kv_internal.h"
+#include "kv_quant.h"
 
 namespace nf4 {
 namespace {
-
-constexpr int kWave = 64;
-
-__device__ inline uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint32_t w = __shfl_xor(v, o);
-    v = w > v ? w : v;
-  }
-  return v;
-}
-
-// Exponent of the block scale for the bits of a magnitude a = m 2^E, 1 <= m <
-// 2: the least e with a <= 448 2^e = 1.75 2^(8 + e), clamped.  Zero and
-// subnormals have E = -127 here, which the clamp takes to kKvExpMin either way.
-__device__ inline int block_exponent(uint32_t bits) {
-  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return e < kKvExpMin ? kKvExpMin : e > kKvExpMax ? kKvExpMax : e;
-}
-
-__device__ inline float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// Exponent of a scale that the cache holds; whatever else lies there is
-// taken into the range (it can only be a block that was never written).
-__device__ inline int scale_exponent(float s) {
-  const int e = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
-  return e < kKvExpMin ? kKvExpMin : e > kKvExpMax ? kKvExpMax : e;
-}
-
-// e4m3 codes of four values (byte i = value i): to nearest even, past +-448
-// as +-448, NaN as NaN.
-__device__ inline uint32_t codes4(float a, float b, float c, float d) {
-  auto hold = [](float x) { return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f); };
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(hold(a), hold(b), 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(hold(c), hold(d), w, true);
-}
-
-// The codes of a dword at a scale 2^shift times as large.
-__device__ inline uint32_t rescale4(uint32_t w, float factor) {
-  auto v = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-  auto u = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-  return codes4(v[0] * factor, v[1] * factor, u[0] * factor, u[1] * factor);
-}
 
 struct Rows {
   const void *k, *v;
@@ -72,10 +30,8 @@ struct Rows {
 template <bool F32, int D>
 __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, KvBatch b, Rows x,
                                                      int64_t blocks_per_seq) {
-  constexpr int VEC = F32 ? 4 : 8;     // values in 16 bytes
-  constexpr int CHUNKS = D / VEC;      // 16-byte pieces of a row
-  constexpr int TASKS = 4 * CHUNKS;    // (quad, piece)
-  constexpr int PER = (TASKS + kWave - 1) / kWave;
+  using B = Block<F32, D>;
+  constexpr int VEC = B::VEC, CHUNKS = B::CHUNKS, TASKS = B::TASKS, PER = B::PER;
   const int lane = threadIdx.x & 63;
   int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int kv = (int)(w & 1);
@@ -123,65 +79,107 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
   }
   // the rows are on their way before the page is known
   if (page < 0 || page >= c.pages) return;
-  const int64_t block = ((layer * c.pages + page) * c.kv_heads + head) *
+  store_block<F32, D>(c, layer, page, head, kv, t0, first, last, val, top);
+}
+
+struct ReadRows {
+  uint8_t *k, *v;
+  int64_t k_stride, v_stride;  // bytes
+};
+
+// The reverse of append_kernel, by the same division of the work: a wave per
+// (sequence, block that its rows touch, head, keys or values).  Rows that have no
+// place get zeros.  Memory bound.
+template <bool F32, int D>
+__global__ __launch_bounds__(256) void read_kernel(KvCache c, int64_t layer, KvBatch b, ReadRows y,
+                                                   int64_t blocks_per_seq) {
+  using B = Block<F32, D>;
+  constexpr int VEC = B::VEC, CHUNKS = B::CHUNKS, TASKS = B::TASKS, PER = B::PER;
+  const int lane = threadIdx.x & 63;
+  int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int kv = (int)(w & 1);
+  w >>= 1;
+  const int head = (int)(w % c.kv_heads);
+  w /= c.kv_heads;
+  const int64_t seq = w / blocks_per_seq;
+  if (seq >= b.seqs) return;
+  int64_t row0;
+  int n, len, end;
+  b.sequence(seq, row0, n, len, end);
+  const int begin = len - n;                // position of row 0, may be negative
+  const int first = begin < 0 ? 0 : begin;  // first token
+  const int past = begin + (n < b.max_rows ? n : b.max_rows);  // past the last row's position
+  uint8_t *to = kv ? y.v : y.k;
+  const int64_t stride = kv ? y.v_stride : y.k_stride;
+  if (begin < 0 && w % blocks_per_seq == 0) {
+    const int none = min(-begin, min(n, b.max_rows));  // rows that are no tokens
+    for (int64_t i = lane; i < (int64_t)none * CHUNKS; i += kWave)
+      *reinterpret_cast<uint4 *>(to + (row0 + i / CHUNKS) * stride +
+                                 ((int64_t)head * CHUNKS + i % CHUNKS) * 16) =
+          make_uint4(0, 0, 0, 0);
+  }
+  const int blk = first / kKvBlock + (int)(w % blocks_per_seq), t0 = blk * kKvBlock;
+  if (first >= past || t0 >= past) return;
+  int page = -1;
+  if (t0 < end) page = b.table[seq * b.table_stride + (t0 >> c.page_shift)];
+  const bool there = page >= 0 && page < c.pages;
+  const int64_t block = ((layer * c.pages + (there ? page : 0)) * c.kv_heads + head) *
                             (int64_t)(1 << (c.page_shift - 4)) +
                         ((t0 & (c.page_tokens() - 1)) >> 4);
-  uint8_t *codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
-  float *scale = (kv ? c.vs : c.ks) + block;
-  int e = block_exponent(wave_max(top));
-  const bool has_old = first > t0;
-  int e_old = e;
-  if (has_old) {
-    e_old = scale_exponent(*scale);
-    e = e_old > e ? e_old : e;
-  }
-  const float inv = pow2(-e), factor = pow2(e_old - e < -126 ? -126 : e_old - e);
-  const bool grew = has_old && e != e_old;
-
+  const uint8_t *codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
+  const float scale = pow2(scale_exponent((kv ? c.vs : c.ks)[block]));
+  const int last = min(past, end);  // past the last token with a place
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int task = lane + i * kWave, quad = task / CHUNKS, piece = task % CHUNKS;
     if (task >= TASKS) continue;
-    const int q0 = t0 + 4 * quad;
+    // four tokens' codes of VEC values: dword h of token t
+    uint32_t code[4][VEC / 4];
     if (kv == 0) {
-      // keys: VEC bytes of each of the four rows
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int tok = q0 + t;
-        uint32_t *p = reinterpret_cast<uint32_t *>(codes + (4 * quad + t) * D + piece * VEC);
-        if (tok >= first && tok < last) {
+      for (int t = 0; t < 4; ++t)
+        __builtin_memcpy(code[t], __builtin_assume_aligned(codes + (4 * quad + t) * D + piece * VEC, VEC),
+                         VEC);
+    } else {
+      uint32_t q[VEC];  // a value's four tokens each
+      __builtin_memcpy(q, __builtin_assume_aligned(codes + (quad * D + piece * VEC) * 4, 16), 4 * VEC);
 #pragma unroll
-          for (int h = 0; h < VEC / 4; ++h)
-            p[h] = codes4(val[i][t][4 * h] * inv, val[i][t][4 * h + 1] * inv,
-                          val[i][t][4 * h + 2] * inv, val[i][t][4 * h + 3] * inv);
-        } else if (tok < first && grew) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int h = 0; h < VEC / 4; ++h) p[h] = rescale4(p[h], factor);
+        for (int h = 0; h < VEC / 4; ++h) {
+          code[t][h] = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) code[t][h] |= (q[4 * h + e] >> (8 * t) & 255u) << (8 * e);
         }
-      }
-    } else if (q0 < last && (q0 + 3 >= first || grew)) {
-      // values: VEC dwords of a quad, each byte a token
-      uint32_t *p = reinterpret_cast<uint32_t *>(codes + (quad * D + piece * VEC) * 4);
-      uint32_t keep = 0, old = 0;  // bytes of the quad that are not new
+    }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (q0 + t < first || q0 + t >= last) keep |= 0xFFu << (8 * t);
-        if (q0 + t < first) old |= 0xFFu << (8 * t);
-      }
+    for (int t = 0; t < 4; ++t) {
+      const int tok = t0 + 4 * quad + t;
+      if (tok < first || tok >= past) continue;
+      float v[VEC];
 #pragma unroll
-      for (int d = 0; d < VEC; ++d) {
-        uint32_t y = codes4(val[i][0][d] * inv, val[i][1][d] * inv, val[i][2][d] * inv,
-                            val[i][3][d] * inv);
-        if (keep) {
-          const uint32_t had = p[d];
-          const uint32_t kept = grew ? (rescale4(had, factor) & old) | (had & ~old) : had;
-          y = (y & ~keep) | (kept & keep);
-        }
-        p[d] = y;
+      for (int h = 0; h < VEC / 4; ++h) {
+        const auto x = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[t][h], false);
+        const auto z = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[t][h], true);
+        v[4 * h] = x[0] * scale;
+        v[4 * h + 1] = x[1] * scale;
+        v[4 * h + 2] = z[0] * scale;
+        v[4 * h + 3] = z[1] * scale;
       }
+      uint4 out = make_uint4(0, 0, 0, 0);
+      if (there && tok < last) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // few bits each: as bf16, a value is its upper half
+          u[e] = F32 ? __float_as_uint(v[e])
+                     : __float_as_uint(v[(2 * e) % VEC]) >> 16 |
+                           (__float_as_uint(v[(2 * e + 1) % VEC]) & 0xFFFF0000u);
+        out = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+      *reinterpret_cast<uint4 *>(to + (row0 + (tok - begin)) * stride +
+                                 ((int64_t)head * CHUNKS + piece) * 16) = out;
     }
   }
-  if (lane == 0) *scale = pow2(e);
 }
 
 // ------------------------------------------------------------------ the pool
@@ -583,6 +581,28 @@ hipError_t launch_kv_append(const KvCache &c, int64_t layer, const KvBatch &b, c
   } else {
     if (c.head_dim == 128) go(append_kernel<false, 128>);
     else go(append_kernel<false, 64>);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const KvCache &c, int64_t layer, const KvBatch &b, const KvRows &k,
+                          const KvRows &v, hipStream_t s) {
+  const int64_t blocks = ((int64_t)b.max_rows + 2 * kKvBlock - 2) / kKvBlock;  // as in an append
+  const int64_t waves = b.seqs * blocks * c.kv_heads * 2;
+  const int64_t grid = (waves + 3) / 4;
+  if (grid > 0x7FFFFFFF / 256) return hipErrorInvalidConfiguration;
+  const int64_t size = k.f32 ? 4 : 2;
+  const ReadRows y{static_cast<uint8_t *>(k.at), static_cast<uint8_t *>(v.at), k.stride * size,
+                   v.stride * size};
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, c, layer, b, y, blocks);
+  };
+  if (k.f32) {
+    if (c.head_dim == 128) go(read_kernel<true, 128>);
+    else go(read_kernel<true, 64>);
+  } else {
+    if (c.head_dim == 128) go(read_kernel<false, 128>);
+    else go(read_kernel<false, 64>);
   }
   return hipGetLastError();
 }

@@ -76,6 +76,41 @@ hipError_t launch_kv_append(const KvCache &c, int64_t layer, const KvBatch &b, c
                             int64_t k_stride, const void *v, int64_t v_stride, bool f32,
                             hipStream_t s);
 
+// How heads turn: the first `dims` values, pair i by turns[i] / 2^64 of a full turn a
+// token; `pairs`: neighbouring values, else value i and i + dims / 2.
+struct KvRotary {
+  int dims;
+  bool pairs;
+  double gain;
+  uint64_t turns[64];
+};
+
+// Rows of values, `stride` of them apart.
+struct KvRows {
+  void *at;
+  int64_t stride;
+  bool f32;
+};
+hipError_t launch_rotate(const KvRotary &rot, const KvRows &x, const int32_t *positions,
+                         int64_t rows, int heads, int head_dim, const float *weight, double eps,
+                         const KvRows &y, hipStream_t s);
+
+// The new rows of an append that turns queries and keys, strides in bytes.
+struct KvTurned {
+  const uint8_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  int heads;
+  const float *q_weight, *k_weight;  // of the norms, or null
+  double eps;
+  uint16_t *q_out;
+};
+hipError_t launch_kv_append_rotated(const KvCache &c, int64_t layer, const KvBatch &b,
+                                    const KvRotary &rot, const KvTurned &a, bool f32,
+                                    hipStream_t s);
+
+hipError_t launch_kv_read(const KvCache &c, int64_t layer, const KvBatch &b, const KvRows &k,
+                          const KvRows &v, hipStream_t s);
+
 struct KvAttention {
   const uint16_t *q;
   int64_t q_stride;

@@ -24,11 +24,16 @@ EXPORTS = ("nf4_status_string", "nf4_codebook", "nf4_qweight_bytes", "nf4_absmax
            "nf4_awq_params_bytes", "nf4_awq_workspace_bytes", "nf4_awq_pack", "nf4_awq_repack",
            "nf4_awq_unpack", "nf4_awq_dequant", "nf4_gather_columns", "nf4_awq_gemv_prefetch", "nf4_awq_gemv", "nf4_awq_gemm",
            "nf4_kv_code_bytes", "nf4_kv_scale_bytes", "nf4_kv_append",
+           "nf4_kv_read", "nf4_rotary_frequencies", "nf4_rotary_init", "nf4_rotate",
+           "nf4_kv_append_rotated",
            "nf4_kv_attention_workspace_bytes", "nf4_kv_attention", "nf4_kv_copy_pages",
            "nf4_kv_reserve", "nf4_kv_fork", "nf4_kv_release", "nf4_kv_compact_workspace_bytes",
            "nf4_kv_compact")
 
 NF4_KV_BF16, NF4_KV_F32 = range(2)
+NF4_ROTARY_HALVES, NF4_ROTARY_PAIRS = range(2)
+NF4_SCALING_PLAIN, NF4_SCALING_LINEAR, NF4_SCALING_BASE, NF4_SCALING_RAMP, \
+    NF4_SCALING_SMOOTH = range(5)
 
 _lib = None
 
@@ -49,6 +54,11 @@ class _KVPool(ctypes.Structure):
     _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int64), ("table_stride", ctypes.c_int64),
                 ("len", ctypes.c_void_p), ("missing", ctypes.c_void_p)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int64), ("layout", ctypes.c_int64), ("gain", ctypes.c_double),
+                ("turns", ctypes.c_uint64 * 64)]
 
 
 class NF4Error(RuntimeError):
@@ -121,6 +131,18 @@ def lib() -> ctypes.CDLL:
             f.argtypes = [cache]
         L.nf4_kv_append.restype = st
         L.nf4_kv_append.argtypes = [cache, i64, batch, vp, i64, vp, i64, st, vp]
+        rotary, f64, f32 = ctypes.POINTER(_Rotary), ctypes.c_double, ctypes.c_float
+        L.nf4_kv_read.restype = st
+        L.nf4_kv_read.argtypes = [cache, i64, batch, vp, i64, vp, i64, st, vp]
+        L.nf4_rotary_frequencies.restype = st
+        L.nf4_rotary_frequencies.argtypes = [i64, f64, st, f64, f64, f64, f64, ctypes.POINTER(f64)]
+        L.nf4_rotary_init.restype = st
+        L.nf4_rotary_init.argtypes = [rotary, i64, st, ctypes.POINTER(f64), f64]
+        L.nf4_rotate.restype = st
+        L.nf4_rotate.argtypes = [rotary, vp, i64, st, vp, i64, i64, i64, vp, f32, vp, i64, st, vp]
+        L.nf4_kv_append_rotated.restype = st
+        L.nf4_kv_append_rotated.argtypes = [cache, i64, batch, rotary, vp, i64, i64, vp, vp, i64, vp,
+                                            vp, i64, st, f32, vp, vp]
         L.nf4_kv_attention_workspace_bytes.restype = sz
         L.nf4_kv_attention_workspace_bytes.argtypes = [cache, batch, i64, i64, i64]
         L.nf4_kv_attention.restype = st
@@ -345,6 +367,74 @@ def nf4_kv_append(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, 
                                type, _stream(stream)), "nf4_kv_append")
 
 
+def _operands(where: str, gpu: int, type: int, *tensors) -> None:
+    """Tensors (None and addresses are left out) lie on that GPU and hold what `type`
+    says: the kernels take them as they are told to."""
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda or t.device.index != gpu:
+            raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on one GPU")
+        if t.element_size() != (4 if type == NF4_KV_F32 else 2) or not t.is_floating_point():
+            raise NF4Error(NF4_ERR_SHAPE, f"{where}: a tensor of another type")
+
+
+def nf4_kv_read(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, type: int,
+                stream=None) -> None:
+    _on_gpu("nf4_kv_read", cache.gpu, batch.gpu)
+    _operands("nf4_kv_read", cache.gpu, type, k, v)
+    _check(lib().nf4_kv_read(cache.arg, layer, batch.arg, _ptr(k), k_stride, _ptr(v), v_stride,
+                             type, _stream(stream)), "nf4_kv_read")
+
+
+def nf4_rotary_frequencies(dims: int, base: float, scaling: int = NF4_SCALING_PLAIN,
+                           factor: float = 1.0, original: float = 0.0, low: float = 0.0,
+                           high: float = 0.0) -> np.ndarray:
+    """Radians a token of each pair (host computation, 64 bits)."""
+    out = (ctypes.c_double * 64)()
+    _check(lib().nf4_rotary_frequencies(dims, base, scaling, factor, original, low, high, out),
+           "nf4_rotary_frequencies")
+    return np.array(out[:dims // 2], dtype=np.float64)
+
+
+def nf4_rotary_init(struct, dims: int, layout: int, frequency, gain: float = 1.0) -> None:
+    f = np.ascontiguousarray(frequency, dtype=np.float64).reshape(-1)
+    if len(f) * 2 != dims:
+        raise NF4Error(NF4_ERR_SHAPE, "nf4_rotary_init")
+    _check(lib().nf4_rotary_init(ctypes.byref(struct), dims, layout,
+                                 f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), gain),
+           "nf4_rotary_init")
+
+
+def nf4_rotate(rotary, x, x_stride: int, x_type: int, positions, rows: int, heads: int,
+               head_dim: int, weight, eps: float, y, y_stride: int, y_type: int,
+               stream=None) -> None:
+    if not isinstance(x, int) and x is not None:
+        gpu = _gpu(x)
+        _on_gpu("nf4_rotate", gpu)
+        _operands("nf4_rotate", gpu, x_type, x)
+        _operands("nf4_rotate", gpu, y_type, y)
+        _operands("nf4_rotate", gpu, NF4_KV_F32, weight)
+        if not isinstance(positions, int) and positions is not None:
+            _on_gpu("nf4_rotate", gpu, _gpu(_int32(positions)))
+    _check(lib().nf4_rotate(rotary.arg, _ptr(x), x_stride, x_type, _ptr(positions), rows, heads,
+                            head_dim, _ptr(weight), eps, _ptr(y), y_stride, y_type,
+                            _stream(stream)), "nf4_rotate")
+
+
+def nf4_kv_append_rotated(cache, layer: int, batch, rotary, q, q_stride: int, heads: int, q_weight,
+                          k, k_stride: int, k_weight, v, v_stride: int, type: int, eps: float,
+                          q_out, stream=None) -> None:
+    _on_gpu("nf4_kv_append_rotated", cache.gpu, batch.gpu)
+    _operands("nf4_kv_append_rotated", cache.gpu, type, q, k, v)
+    _operands("nf4_kv_append_rotated", cache.gpu, NF4_KV_BF16, q_out)
+    _operands("nf4_kv_append_rotated", cache.gpu, NF4_KV_F32, q_weight, k_weight)
+    _check(lib().nf4_kv_append_rotated(cache.arg, layer, batch.arg, rotary.arg, _ptr(q), q_stride,
+                                       heads, _ptr(q_weight), _ptr(k), k_stride, _ptr(k_weight),
+                                       _ptr(v), v_stride, type, eps, _ptr(q_out),
+                                       _stream(stream)), "nf4_kv_append_rotated")
+
+
 def nf4_kv_attention_workspace_bytes(cache, batch, heads: int, window: int = 0,
                                      sinks: int = 0) -> int:
     return lib().nf4_kv_attention_workspace_bytes(cache.arg, batch.arg, heads, window, sinks)
@@ -523,6 +613,21 @@ class KVBatch:
                                table.shape[1])
         self.arg = ctypes.pointer(self.struct)
         self.gpu = _gpu(kv_len, table, row_start)
+
+
+class Rotary:
+    """How heads turn by their positions: the first `dims` values, in halves or
+    pairs, at the usual frequencies of `base` (scaled for longer contexts as
+    include/nf4.h states) or at the given ones (radians a token)."""
+
+    def __init__(self, dims: int, layout: int = NF4_ROTARY_HALVES, base: float = 10000.0,
+                 scaling: int = NF4_SCALING_PLAIN, factor: float = 1.0, original: float = 0.0,
+                 low: float = 0.0, high: float = 0.0, gain: float = 1.0, frequencies=None):
+        if frequencies is None:
+            frequencies = nf4_rotary_frequencies(dims, base, scaling, factor, original, low, high)
+        self.struct = _Rotary()
+        nf4_rotary_init(self.struct, dims, layout, frequencies, gain)
+        self.arg = ctypes.pointer(self.struct)
 
 
 class KVPool:

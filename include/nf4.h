@@ -456,6 +456,101 @@ nf4_status nf4_kv_append(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_
                          const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                          nf4_kv_type type, hipStream_t stream);
 
+/* Tokens of one layer of the cache as rows, the reverse of nf4_kv_append: row
+ * row_start[s] + i of k and v gets the keys and values of the token at position
+ * kv_len[s] - (row_start[s + 1] - row_start[s]) + i of sequence s, code * scale, which
+ * bfloat16 and fp32 hold exactly (NaN codes as NaN).  Rows that are no tokens, and
+ * tokens in holes or past the table, read as zeros; rows of no sequence and rows past
+ * max_rows are left as they are.  k, v: kv_heads * head_dim values a row, k_stride and
+ * v_stride of them apart (a multiple of 16 bytes), which must not overlap each other.
+ * Errors: as nf4_kv_append. */
+nf4_status nf4_kv_read(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch, void *k,
+                       int64_t k_stride, void *v, int64_t v_stride, nf4_kv_type type,
+                       hipStream_t stream);
+
+/* ---- rotary positions: what queries and keys go through between the projection
+ * and the cache.  The first `dims` values of a head form pairs (a, b); at
+ * position p pair i turns by the angle p * frequency[i]:
+ *   a' = gain (a cos - b sin),  b' = gain (a sin + b cos).
+ * The other values stay as they are.  A norm may come first, over all values
+ * of the head: x / sqrt(mean x^2 + eps) * weight. */
+typedef enum nf4_rotary_layout {
+  NF4_ROTARY_HALVES = 0, /* pair i: values i and i + dims / 2 */
+  NF4_ROTARY_PAIRS = 1   /* pair i: values 2i and 2i + 1 */
+} nf4_rotary_layout;
+
+/* Host memory, read during a call (a captured graph keeps its values). */
+typedef struct nf4_rotary {
+  int64_t dims;       /* even, 0 (nothing turns) .. head_dim */
+  int64_t layout;     /* nf4_rotary_layout */
+  double gain;
+  uint64_t turns[64]; /* pair i turns by turns[i] / 2^64 of a full turn a token */
+} nf4_rotary;
+
+typedef enum nf4_rotary_scaling {
+  NF4_SCALING_PLAIN = 0,
+  NF4_SCALING_LINEAR = 1,
+  NF4_SCALING_BASE = 2,
+  NF4_SCALING_RAMP = 3,
+  NF4_SCALING_SMOOTH = 4
+} nf4_rotary_scaling;
+
+/* The usual frequencies (host; radians a token): f_i = base^(-2i / dims),
+ * i < dims / 2, for contexts `factor` times as long as the original one:
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   BASE    f_i with base * factor^(dims / (dims - 2))
+ *   RAMP    f_i (1 - r) + f_i / factor r, r rising from 0 to 1 between the
+ *           numbers of the pairs that make `high` and `low` turns over `original` tokens,
+ *           rounded down and up: r = (i - a) / (b - a), held to 0 .. 1, with
+ *           a = max(floor(c(high)), 0), b = min(ceil(c(low)), dims - 1) (a + 0.001 if
+ *           they are equal), c(t) = dims log(original / (2 pi t)) / (2 log base)
+ *   SMOOTH  the same with r = 1 - (t_i - low) / (high - low) for the t_i turns that
+ *           pair i makes over `original` tokens
+ * What a scaling does not name is not looked at.  dims even, 0 .. 128; base > 1;
+ * factor, original and low > 0, high > low (else NF4_ERR_SHAPE, nothing written). */
+nf4_status nf4_rotary_frequencies(int64_t dims, double base, nf4_rotary_scaling scaling,
+                                  double factor, double original, double low, double high,
+                                  double *frequency);
+
+/* Fills the structure from frequencies (host, radians a token, at most 2^20 in
+ * magnitude; negative ones turn back).  A turn is kept to 2^-65, so that
+ * angles are right to 2^-35 of a turn at positions up to 2^30. */
+nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout layout,
+                           const double *frequency, double gain);
+
+/* Turns the heads of rows.  x: heads * head_dim values a row, bfloat16 or fp32,
+ * x_stride of them apart; y the same, of its own type and stride (both multiples of 16
+ * bytes, so that slices of a fused projection's rows are taken as they are).
+ * positions: device int32[rows], any values (a negative one turns back, so
+ * that -p undoes p).  weight: device fp32[head_dim], 16-byte aligned, of the norm, or NULL
+ * for none; eps: at least 2^-100, not looked at without a norm.  y may be x with
+ * the same type and stride; else they must not overlap.  Sines, cosines and the norm's
+ * sum are worked out in 64 bits, the rest in fp32, and the result rounded once to y's
+ * type.  head_dim: 64 or 128; rows <= 2^23.
+ * Errors: NF4_ERR_NULL, NF4_ERR_SHAPE, NF4_ERR_ALIGN. */
+nf4_status nf4_rotate(const nf4_rotary *rotary, const void *x, int64_t x_stride,
+                      nf4_kv_type x_type, const int32_t *positions, int64_t rows, int64_t heads,
+                      int64_t head_dim, const float *weight, float eps, void *y, int64_t y_stride,
+                      nf4_kv_type y_type, hipStream_t stream);
+
+/* nf4_kv_append for queries and keys as the projection leaves them: the new rows'
+ * queries and keys are normed (q_weight, k_weight: as in nf4_rotate, NULL for no norm)
+ * and turned by the rows' positions; the queries go to q_out, bfloat16
+ * [rows][heads * head_dim], as nf4_kv_attention takes them, and the keys and values
+ * into their pages as by nf4_kv_append, the keys straight from fp32.  One launch.
+ * q, k, v: rows of one type, each with its stride (a multiple of 16 bytes); heads a
+ * multiple of kv_heads.  q_out may be q where that is bfloat16 with q_stride = heads *
+ * head_dim; else it must not overlap q, k or v.  q_out gets zeros for rows that are no
+ * tokens; rows of no sequence and rows past max_rows are left as they are.
+ * Errors: NF4_ERR_NULL, NF4_ERR_SHAPE, NF4_ERR_ALIGN. */
+nf4_status nf4_kv_append_rotated(const nf4_kv_cache *cache, int64_t layer,
+                                 const nf4_kv_batch *batch, const nf4_rotary *rotary, const void *q,
+                                 int64_t q_stride, int64_t heads, const float *q_weight,
+                                 const void *k, int64_t k_stride, const float *k_weight,
+                                 const void *v, int64_t v_stride, nf4_kv_type type, float eps,
+                                 hip_bfloat16 *q_out, hipStream_t stream);
+
 /* Bytes of workspace nf4_kv_attention needs for a call with these arguments
  * on the current device (the arrays of the structures are not looked at); 0
  * when it needs none or rejects the call. */
