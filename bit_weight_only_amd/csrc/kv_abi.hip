@@ -119,6 +119,65 @@ nf4_status check_rotary(const nf4_rotary *r, int64_t head_dim, nf4::KvRotary &ou
 int held(int64_t v) { return (int)(v > nf4::kKvLongest ? nf4::kKvLongest : v); }
 static_assert(nf4::kKvLongest == kMaxLen + kMaxRows, "no row of the longest sequence is held");
 
+bool groups_shape_ok(const nf4_kv_groups &g, const nf4_kv_batch &b) {
+  if (g.groups < 1 || g.groups > b.seqs || (!g.first && g.groups != 1)) return false;
+  return g.max_rows >= 0 && g.max_prefix >= 0 && g.max_prefix <= kMaxLen;
+}
+
+nf4::KvGroups as_groups(const nf4_kv_groups &g, const nf4_kv_batch &b) {
+  return nf4::KvGroups{g.groups, (int)(g.max_rows == 0 || g.max_rows > b.rows ? b.rows : g.max_rows),
+                       (int)g.max_prefix, g.first, g.prefix_len};
+}
+
+struct Attention {
+  nf4::KvCache c;
+  nf4::KvBatch b;
+  nf4::KvGroups g;
+  nf4::KvAttention a;
+};
+
+// What both attentions check; groups: of the one that has them, or null.
+nf4_status check_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch,
+                           const nf4_kv_groups *groups, const hip_bfloat16 *q, int64_t q_stride,
+                           int64_t heads, float scale, int64_t window, int64_t sinks,
+                           hip_bfloat16 *out, float *lse, void *workspace, size_t ws_bytes,
+                           Attention &x) {
+  if (!q || !out || (groups && !groups->prefix_len)) return NF4_ERR_NULL;
+  nf4_status st = check_cache(cache, x.c);
+  if (st != NF4_OK) return st;
+  if ((st = check_batch(batch, x.c, x.b)) != NF4_OK) return st;
+  if (groups && !groups_shape_ok(*groups, *batch)) return NF4_ERR_SHAPE;
+  if (layer < 0 || layer >= x.c.layers) return NF4_ERR_SHAPE;
+  if (!attention_shape_ok(x.c, x.b.rows, heads, window, sinks)) return NF4_ERR_SHAPE;
+  if (!isfinite(scale) || !(scale > 0.0f)) return NF4_ERR_SHAPE;
+  if (q_stride < heads * x.c.head_dim || q_stride > kMaxElems) return NF4_ERR_SHAPE;
+  if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(lse, 4))
+    return NF4_ERR_ALIGN;
+  if (groups && (!aligned(groups->first, 4) || !aligned(groups->prefix_len, 4)))
+    return NF4_ERR_ALIGN;
+  size_t need;
+  if (groups) {
+    x.g = as_groups(*groups, *batch);
+    need = nf4::kv_attention_shared_workspace_bytes(x.c, x.b, x.g, (int)heads, held(window),
+                                                    held(sinks));
+  } else {
+    need = nf4::kv_attention_workspace_bytes(x.c, x.b, (int)heads, held(window), held(sinks));
+  }
+  if (need > 0 && !workspace) return NF4_ERR_NULL;
+  if (need > ws_bytes) return NF4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return NF4_ERR_ALIGN;
+  x.a = nf4::KvAttention{reinterpret_cast<const uint16_t *>(q),
+                         q_stride,
+                         (int)heads,
+                         scale,
+                         held(window),
+                         held(sinks),
+                         reinterpret_cast<uint16_t *>(out),
+                         lse,
+                         workspace};
+  return NF4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -306,33 +365,38 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_
                             const hip_bfloat16 *q, int64_t q_stride, int64_t heads, float scale,
                             int64_t window, int64_t sinks, hip_bfloat16 *out, float *lse,
                             void *workspace, size_t ws_bytes, hipStream_t stream) {
-  nf4::KvCache c;
-  nf4::KvBatch b;
-  if (!q || !out) return NF4_ERR_NULL;
-  nf4_status st = check_cache(cache, c);
+  Attention x;
+  const nf4_status st = check_attention(cache, layer, batch, nullptr, q, q_stride, heads, scale,
+                                        window, sinks, out, lse, workspace, ws_bytes, x);
   if (st != NF4_OK) return st;
-  if ((st = check_batch(batch, c, b)) != NF4_OK) return st;
-  if (layer < 0 || layer >= c.layers) return NF4_ERR_SHAPE;
-  if (!attention_shape_ok(c, b.rows, heads, window, sinks)) return NF4_ERR_SHAPE;
-  if (!isfinite(scale) || !(scale > 0.0f)) return NF4_ERR_SHAPE;
-  if (q_stride < heads * c.head_dim || q_stride > kMaxElems) return NF4_ERR_SHAPE;
-  if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(lse, 4))
-    return NF4_ERR_ALIGN;
-  const size_t need =
-      nf4::kv_attention_workspace_bytes(c, b, (int)heads, held(window), held(sinks));
-  if (need > 0 && !workspace) return NF4_ERR_NULL;
-  if (need > ws_bytes) return NF4_ERR_WORKSPACE;
-  if (need > 0 && !aligned(workspace, 16)) return NF4_ERR_ALIGN;
-  const nf4::KvAttention a{reinterpret_cast<const uint16_t *>(q),
-                           q_stride,
-                           (int)heads,
-                           scale,
-                           held(window),
-                           held(sinks),
-                           reinterpret_cast<uint16_t *>(out),
-                           lse,
-                           workspace};
-  return from_hip(nf4::launch_kv_attention(c, layer, b, a, stream));
+  return from_hip(nf4::launch_kv_attention(x.c, layer, x.b, x.a, stream));
+}
+
+size_t nf4_kv_attention_shared_workspace_bytes(const nf4_kv_cache *cache,
+                                               const nf4_kv_batch *batch,
+                                               const nf4_kv_groups *groups, int64_t heads,
+                                               int64_t window, int64_t sinks) {
+  nf4::KvCache c;
+  if (!cache || !batch || !groups || !shape_ok(*cache, c) || !batch_shape_ok(*batch)) return 0;
+  if (!groups_shape_ok(*groups, *batch)) return 0;
+  if (!attention_shape_ok(c, batch->rows, heads, window, sinks)) return 0;
+  return nf4::kv_attention_shared_workspace_bytes(c, as_batch(*batch, c),
+                                                  as_groups(*groups, *batch), (int)heads,
+                                                  held(window), held(sinks));
+}
+
+nf4_status nf4_kv_attention_shared(const nf4_kv_cache *cache, int64_t layer,
+                                   const nf4_kv_batch *batch, const nf4_kv_groups *groups,
+                                   const hip_bfloat16 *q, int64_t q_stride, int64_t heads,
+                                   float scale, int64_t window, int64_t sinks, hip_bfloat16 *out,
+                                   float *lse, void *workspace, size_t ws_bytes,
+                                   hipStream_t stream) {
+  if (!groups) return NF4_ERR_NULL;
+  Attention x;
+  const nf4_status st = check_attention(cache, layer, batch, groups, q, q_stride, heads, scale,
+                                        window, sinks, out, lse, workspace, ws_bytes, x);
+  if (st != NF4_OK) return st;
+  return from_hip(nf4::launch_kv_attention_shared(x.c, layer, x.b, x.g, x.a, stream));
 }
 
 nf4_status nf4_kv_copy_pages(const nf4_kv_cache *cache, const int32_t *src, const int32_t *dst,

@@ -96,12 +96,37 @@ __device__ inline float lane_float(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
+__device__ inline int lanes_min(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// What a launch takes of the keys: all that its rows see, or, where sequences share
+// their first tokens, those of the shared ones (rows of a whole group at once, its
+// keys split at fixed places) or those past them.  The parts of the latter two meet in
+// the workspace.
+struct Whole {
+  static constexpr bool kPrefix = false, kSuffix = false;
+};
+struct Prefix {
+  static constexpr bool kPrefix = true, kSuffix = false;
+  KvGroups g;
+};
+struct Suffix {
+  static constexpr bool kPrefix = false, kSuffix = true;
+  KvGroups g;
+  int64_t parts;  // of the workspace, in floats: where the suffixes' begin
+};
+
 // The keys of one row: up to its position, inside the window or among the
 // first tokens.
+template <class S>
 struct Visible {
-  int window, sinks;
+  int window, sinks, shared;  // shared: keys before it are the prefix's
   __device__ bool operator()(int key, int pos) const {
-    return (key <= pos) & ((window == 0) | (key > pos - window) | (key < sinks));
+    return (key <= pos) & ((window == 0) | (key > pos - window) | (key < sinks)) &
+           (!S::kPrefix | (key < shared)) & (!S::kSuffix | (key >= shared));
   }
   // Bit x: whether the row sees key + x, x = 0 .. 63.
   __device__ uint64_t bits(int key, int pos) const {
@@ -110,30 +135,36 @@ struct Visible {
     };
     uint64_t b = upto(pos - key);
     if (window > 0) b &= ~upto(pos - window - key) | upto(sinks - 1 - key);
+    if (S::kPrefix) b &= upto(shared - 1 - key);
+    if (S::kSuffix) b &= ~upto(shared - 1 - key);
     return b;
   }
   // Whether every row at p_lo .. p_hi sees all of key .. key + n - 1.
   __device__ bool all(int key, int n, int p_lo, int p_hi) const {
-    return key + n - 1 <= p_lo && (window == 0 || key > p_hi - window || key + n <= sinks);
+    return key + n - 1 <= p_lo && (window == 0 || key > p_hi - window || key + n <= sinks) &&
+           (!S::kPrefix || key + n <= shared) && (!S::kSuffix || key >= shared);
   }
 };
 
-// The steps of N keys that rows from p_lo on can see, as a list: those with
-// first tokens, then from the start of the lowest row's window to the key `last`.
+// The steps of N keys from step `low` on that rows from p_lo on can see, as a list:
+// those with first tokens, then from the start of the lowest row's window to the
+// key `last`.
 template <int N>
 struct Steps {
-  int sink_steps, from, count;
-  __device__ Steps(int p_lo, int last, int window, int sinks) {
-    sink_steps = from = 0;
+  int low, sink_steps, from, count;
+  __device__ Steps(int low_step, int p_lo, int last, int window, int sinks) {
+    low = from = low_step;
+    sink_steps = 0;
     const int steps = last < 0 ? 0 : last / N + 1;
-    if (window > 0 && p_lo - window + 1 > 0) {
+    if (window > 0 && p_lo - window + 1 > low * N) {
       from = (p_lo - window + 1) / N;
-      sink_steps = min((int)(((int64_t)sinks + N - 1) / N), steps);
-      if (sink_steps >= from) from = sink_steps = 0;
+      const int past = min((int)(((int64_t)sinks + N - 1) / N), steps);
+      if (past >= from) from = low;
+      else sink_steps = max(past - low, 0);
     }
     count = sink_steps + max(steps - from, 0);
   }
-  __device__ int key(int i) const { return (i < sink_steps ? i : i - sink_steps + from) * N; }
+  __device__ int key(int i) const { return (i < sink_steps ? i + low : i - sink_steps + from) * N; }
 };
 
 // Most steps of N keys that any N-aligned list above can have, for the host.
@@ -164,6 +195,132 @@ struct Tile {
   __device__ bool empty() const { return r0 >= rows; }
   // The last key that a row at p may see: not past the table.
   __device__ int last_key(int p) const { return min(p, end - 1); }
+
+  // A tile of all rows of a group of sequences over the tokens that they share; `at` are
+  // the positions of its tokens, lane l those of tokens l and 64 + l from its first on.
+  __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, const KvGroups &g,
+                  int64_t first, int64_t past, int shared, uint32_t tile, uint32_t width,
+                  int (&at)[2]) {
+    group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
+    row0 = b.first_row(first);
+    const int64_t all = first < past ? b.first_row(past) - row0 : 0;
+    n = (int)(all < 0 ? 0 : all < g.max_rows ? all : g.max_rows);
+    len = end = shared;
+    rows = (uint32_t)n * group;
+    r0 = tile * width;
+    p_lo = 0x7FFFFFFF;
+    p_hi = -1;
+    if (empty()) return;
+    const int lane = threadIdx.x & 63;
+    const int t0 = (int)(r0 / group), t1 = (int)(min(r0 + width, rows) - 1) / (int)group;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + 64 * i + lane;
+      at[i] = -1;
+      if (t <= t1) {
+        at[i] = b.position(row0 + t, first, past);
+        p_lo = min(p_lo, at[i]);
+        p_hi = max(p_hi, at[i]);
+      }
+    }
+    p_lo = lanes_min(p_lo);
+    p_hi = -lanes_min(-p_hi);
+  }
+  // Position of the tile's token t (counted from its first) from what the lanes hold.
+  __device__ static int position(const int (&at)[2], int t) {
+    const int x = __shfl(at[0], t & 63), y = __shfl(at[1], t & 63);
+    return t < 64 ? x : y;
+  }
+};
+
+// Where a workgroup works: the tile `index` of sequence (or group) `seq`, part `split` of
+// its keys.
+template <class S, int N>
+struct Place;
+
+template <int N>
+struct Place<Whole, N> {
+  const KvCache &c;
+  const KvBatch &b;
+  const KvAttention &a;
+  int64_t seq;
+  uint32_t index, width;
+  int split, split_steps;
+  const int32_t *table;
+  static constexpr int shared = 0;
+  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const Whole &,
+                   int64_t seq, uint32_t index, uint32_t width, int split, int split_steps)
+      : c(c), b(b), a(a), seq(seq), index(index), width(width), split(split),
+        split_steps(split_steps), table(b.table + seq * b.table_stride) {}
+  __device__ static uint32_t count(const KvBatch &b, const Whole &) { return (uint32_t)b.seqs; }
+  __device__ Tile tile(int (&)[2]) const { return Tile(c, b, a, seq, index, width); }
+  __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
+    return Steps<N>(0, tl.p_lo, tl.last_key(p_hi), a.window, a.sinks);
+  }
+  __device__ int splits(const Steps<N> &s) const {
+    return s.count <= split_steps ? 1 : (s.count + split_steps - 1) / split_steps;
+  }
+  __device__ int begin() const { return split * split_steps; }
+  __device__ int end(const Steps<N> &s) const { return min(s.count, (split + 1) * split_steps); }
+  __device__ bool whole(int splits) const { return splits == 1; }
+  __device__ float *parts(float *ws) const { return ws; }
+};
+
+// A suffix is summed as a whole sequence is, from its first key past the prefix on.
+template <int N>
+struct Place<Suffix, N> : Place<Whole, N> {
+  using Base = Place<Whole, N>;
+  int shared;
+  int64_t first_part;
+  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const Suffix &s,
+                   int64_t seq, uint32_t index, uint32_t width, int split, int split_steps)
+      : Base(c, b, a, Whole{}, seq, index, width, split, split_steps),
+        shared(s.g.shared_of(b, seq)), first_part(s.parts) {}
+  __device__ static uint32_t count(const KvBatch &b, const Suffix &) { return (uint32_t)b.seqs; }
+  __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
+    return Steps<N>(shared / N, tl.p_lo, tl.last_key(p_hi), this->a.window, this->a.sinks);
+  }
+  __device__ bool whole(int splits) const { return splits == 1 && shared == 0; }
+  __device__ float *parts(float *ws) const { return ws + first_part; }
+};
+
+// A prefix is split at fixed keys, so that which parts there are depends on its length
+// only; each leaves its sums, also where its rows see none of its keys.
+template <int N>
+struct Place<Prefix, N> {
+  const KvCache &c;
+  const KvBatch &b;
+  const KvAttention &a;
+  const KvGroups &g;
+  int64_t first, past;
+  uint32_t index, width;
+  int split, split_steps, shared;
+  const int32_t *table;
+  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const Prefix &s,
+                   int64_t group, uint32_t index, uint32_t width, int split, int split_steps)
+      : c(c), b(b), a(a), g(s.g), index(index), width(width), split(split),
+        split_steps(split_steps) {
+    first = g.first_of(b, group);
+    past = g.first_of(b, group + 1);
+    shared = g.shared(b, group);
+    // (a group without sequences has no rows: nothing of its table is read)
+    table = b.table + (first < b.seqs ? first : 0) * b.table_stride;
+  }
+  __device__ static uint32_t count(const KvBatch &, const Prefix &s) { return (uint32_t)s.g.groups; }
+  __device__ Tile tile(int (&at)[2]) const {
+    return Tile(c, b, a, g, first, past, shared, index, width, at);
+  }
+  __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
+    const int low = split * split_steps;
+    const int64_t keys = (int64_t)(low + split_steps) * N;
+    const int last = (int)(keys < shared ? keys : shared) - 1;
+    return Steps<N>(low, tl.p_lo, min(p_hi, last), a.window, a.sinks);
+  }
+  __device__ int splits(const Steps<N> &) const { return g.parts(shared, split_steps * N); }
+  __device__ int begin() const { return 0; }
+  __device__ int end(const Steps<N> &s) const { return s.count; }
+  __device__ bool whole(int) const { return false; }
+  __device__ float *parts(float *ws) const { return ws; }
 };
 
 // Workspace of a call whose keys are split: for every (item, split), an item
@@ -259,11 +416,11 @@ struct Step {
   uint4 k[2][D / 64], v[2][D / 64];
 };
 
-template <int D, int W>
+template <int D, int W, class S>
 __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer, KvBatch b,
                                                         KvAttention a, uint32_t tiles,
                                                         int max_splits,
-                                                        int split_steps) {
+                                                        int split_steps, S scope) {
   constexpr int KS = D / 32;   // k-steps of the first product
   constexpr int DT = D / 16;   // tiles of 16 values of the second
   constexpr int PITCH = D + 4; // of a row of sums in LDS, in floats
@@ -279,27 +436,29 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   w /= (uint32_t)c.kv_heads;
   const int split = w % (uint32_t)max_splits;
   w /= (uint32_t)max_splits;
-  const int64_t seq = w / tiles;
   const uint32_t item = w * (uint32_t)c.kv_heads + head;
-  const int32_t *table = b.table + seq * b.table_stride;
+  const Place<S, 32> place(c, b, a, scope, w / tiles, w % tiles, 16, split, split_steps);
+  const int32_t *table = place.table;
   // without a window, where the first page ids stand does not depend on the
   // lengths: they are read beside them (as far as the longest one may reach)
   int page_ahead = -1;
-  if (a.window == 0) {
+  if (!S::kSuffix && a.window == 0) {
     const int64_t t0 = (int64_t)(split * split_steps + wave + (lane >> 1) * W) * 32 + 16 * (lane & 1);
     page_ahead = table[min(t0, (int64_t)max(b.max_len - 1, 0)) >> c.page_shift];
   }
-  const Tile tl(c, b, a, seq, w % tiles, 16);
+  int at[2];
+  const Tile tl = place.tile(at);
   if (tl.empty()) return;
-  const Steps<32> steps(tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
-  const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
+  const Steps<32> steps = place.steps(tl, tl.p_hi);
+  const int splits = place.splits(steps);
   if (split >= splits) return;
-  const int end = min(steps.count, (split + 1) * split_steps);
+  const int end = place.end(steps);
 
   const bool mine = tl.r0 + col < tl.rows;
   const uint32_t r = mine ? tl.r0 + col : tl.rows - 1;
   const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
-  const int pos = mine ? tl.len - tl.n + tok : -1;
+  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
+  const int pos = mine ? row_pos : -1;
 
   const int64_t layer_pages = layer * c.pages;
   const int page_blocks = 1 << (c.page_shift - 4);
@@ -308,7 +467,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   // the values' scale 2^e e and 2^-e.  Read ahead of the steps as vectors: a
   // scalar read per step would cost the step its whole latency, since scalar
   // reads return out of order and any use waits for all of them.
-  const int first = split * split_steps + wave;
+  const int first = place.begin() + wave;
   int page_l = -1;
   float kc_l = 0.0f, ve_l = 0.0f, vi_l = 1.0f;
   uint64_t high_l = 0;  // bit 2s + h: that block's values need kLift
@@ -321,7 +480,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     const int t0 = steps.key(i) + 16 * (lane & 1);
     page_l = -1;
     if (i < end && t0 < tl.end)
-      page_l = a.window == 0 && i0 == first ? page_ahead : table[t0 >> c.page_shift];
+      page_l = !S::kSuffix && a.window == 0 && i0 == first ? page_ahead : table[t0 >> c.page_shift];
     if (page_l >= c.pages) page_l = -1;
     const int64_t block = block_of(page_l < 0 ? 0 : page_l, t0);
     kc_l = c.ks[block];
@@ -360,7 +519,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   for (int j = 0; j < KS; ++j)
     q[j] = *reinterpret_cast<const bf16x8 *>(qp + 64 * (j / 2) + 8 * (j % 2));
 
-  const Visible visible{a.window, a.sinks};
+  const Visible<S> visible{a.window, a.sinks, place.shared};
   float m = -INFINITY, l = 0.0f;
   f32x4 o[DT] = {};
 
@@ -490,7 +649,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   // a thread's four neighbouring values of a row, over the waves
   constexpr int QUADS = D / 4;
   const int cols = (int)min(16u, tl.rows - tl.r0);
-  float *part = static_cast<float *>(a.ws) +
+  float *part = place.parts(static_cast<float *>(a.ws)) +
                 ((int64_t)item * max_splits + split) * part_floats(16, D);
   for (int u = threadIdx.x; u < cols * QUADS; u += 64 * W) {
     const int cc = u / QUADS, d = (u % QUADS) * 4;
@@ -504,7 +663,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
       ll += mv == -INFINITY ? 0.0f : ml[1][v][cc] * exp2_fast(mv - mm);
       x += *reinterpret_cast<const f32x4 *>(sums + (v * 16 + cc) * PITCH + d);
     }
-    if (splits == 1) {
+    if (place.whole(splits)) {
       store_row(c, a, tl, head, cc, d, x, mm, ll);
     } else {
       *reinterpret_cast<f32x4 *>(part + cc * D + d) = x;
@@ -543,12 +702,12 @@ struct TileLds {
   static constexpr int kCopies = 2 * (D / 64) + 2;      // per wave and stage
 };
 
-template <int D, int G>
+template <int D, int G, class S>
 __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c, int64_t layer,
                                                                       KvBatch b, KvAttention a,
                                                                       uint32_t tiles,
                                                                       int max_splits,
-                                                                      int split_steps) {
+                                                                      int split_steps, S scope) {
   using L = TileLds<D>;
   constexpr int DT = D / 32;   // tiles of 32 values
   constexpr int CH = D / 16;   // 16-byte pieces of a key
@@ -566,16 +725,19 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   w /= (uint32_t)c.kv_heads;
   const int split = w % (uint32_t)max_splits;
   w /= (uint32_t)max_splits;
-  const uint32_t seq = w % (uint32_t)b.seqs;
-  const uint32_t tile = tiles - 1 - w / (uint32_t)b.seqs;
-  const Tile tl(c, b, a, seq, tile, kTileRows);
+  const uint32_t seqs = Place<S, kTileKeys>::count(b, scope);
+  const uint32_t seq = w % seqs;
+  const uint32_t tile = tiles - 1 - w / seqs;
+  const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows, split, split_steps);
+  int at[2];
+  const Tile tl = place.tile(at);
   if (tl.empty()) return;
   // the wave's rows: with two teams, waves w and w + 4 share a SIMD and hold
   // different halves of the tile
   const int sub = team == 0 ? wave : wave ^ 2;
   uint32_t r0 = tl.r0 + 32 * sub;
   int p_hi = tl.p_hi;
-  if (G > 1 && a.window == 0 && max_splits == 1) {
+  if (!S::kPrefix && !S::kSuffix && G > 1 && a.window == 0 && max_splits == 1) {
     // the halves are the sequence's 64 rows number `tile` from its end (sub 0
     // and 1) and from its start, so that every tile has as much to do
     const uint32_t high = (2 * ((tl.rows + kTileRows - 1) / kTileRows) - 1 - tile) * 64;
@@ -583,22 +745,27 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     const uint32_t end = high < tl.rows ? high + 64 : 64 * tile + 64;
     p_hi = tl.len - tl.n + (int)((min(end, tl.rows) - 1) / tl.group);
   }
-  const Steps<kTileKeys> steps(tl.p_lo, tl.last_key(p_hi), a.window, a.sinks);
-  const int splits = steps.count <= split_steps ? 1 : (steps.count + split_steps - 1) / split_steps;
+  const Steps<kTileKeys> steps = place.steps(tl, p_hi);
+  const int splits = place.splits(steps);
   if (split >= splits) return;
-  const int begin = split * split_steps + team;
-  const int turns = (min(steps.count - split * split_steps, split_steps) + G - 1) / G;
-  const int n = (min(steps.count - split * split_steps, split_steps) - team + G - 1) / G;
+  const int begin = place.begin() + team, mine_steps = place.end(steps) - place.begin();
+  const int turns = (mine_steps + G - 1) / G;
+  const int n = (mine_steps - team + G - 1) / G;
 
   const bool mine = r0 + col < tl.rows, idle = r0 >= tl.rows;
   const uint32_t r = mine ? r0 + col : tl.rows - 1;
   const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
-  const int pos = mine ? tl.len - tl.n + tok : -1;
-  const int w_lo = idle ? 0 : tl.len - tl.n + (int)(r0 / tl.group);
-  const int w_hi = idle ? -1 : tl.len - tl.n + (int)(min(r0 + 31, tl.rows - 1) / tl.group);
+  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
+  const int pos = mine ? row_pos : -1;
+  int w_lo = idle ? 0 : tl.len - tl.n + (int)(r0 / tl.group);
+  int w_hi = idle ? -1 : tl.len - tl.n + (int)(min(r0 + 31, tl.rows - 1) / tl.group);
+  if (S::kPrefix) {
+    w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
+    w_hi = -lanes_min(-pos);
+  }
 
   // copies of one step: the wave's block of 16 keys and values, and its scales
-  const int32_t *table = b.table + (int64_t)seq * b.table_stride;
+  const int32_t *table = place.table;
   uint32_t koff[D / 64];  // where in the block the lane's 16 bytes of each copy lie
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
@@ -664,7 +831,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 #pragma unroll
   for (int j = 0; j < D / 16; ++j)
     q[j] = *reinterpret_cast<const bf16x8 *>(qp + 32 * (j / 2) + 8 * (j % 2));
-  const Visible visible{a.window, a.sinks};
+  const Visible<S> visible{a.window, a.sinks, place.shared};
   const float cscale = a.scale * kLog2e;
   float m = -INFINITY, l[2] = {0.0f, 0.0f};
   f32x16 o[DT] = {};
@@ -846,7 +1013,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   const int my_col = lane2 & 31, my_h = lane2 >> 5;
   if (r0 + my_col >= tl.rows) return;
   // element 4a + e of tile t is value DT (8a + 4h + e) + t
-  if (splits == 1) {
+  if (place.whole(splits)) {
     const float inv = 1.0f / sum;
     const uint32_t keep = m == -INFINITY ? 0u : ~0u;  // no key was seen
     const uint32_t row = r0 + my_col;
@@ -869,7 +1036,8 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     return;
   }
   const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
-  float *part = static_cast<float *>(a.ws) + (item * max_splits + split) * part_floats(kTileRows, D);
+  float *part =
+      place.parts(static_cast<float *>(a.ws)) + (item * max_splits + split) * part_floats(kTileRows, D);
   const int row = 32 * sub + my_col;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -920,7 +1088,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
   load(turn);
   const Tile tl(c, b, a, w / tiles, w % tiles, width);
   if (tl.empty()) return;
-  const Steps<N> steps(tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
+  const Steps<N> steps(0, tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
   if (steps.count <= split_steps) return;  // written already
   const int splits = (steps.count + split_steps - 1) / split_steps;
   const bool on = cc < width && tl.r0 + cc < tl.rows;
@@ -940,6 +1108,91 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
       for (int j = 1; j < turns; ++j) {
         const float2 other = mls[threadIdx.x + j * QUADS];
         join(mm, ll, x, other.x, other.y, xs[threadIdx.x + j * QUADS]);
+      }
+  }
+  if (on && turn == 0) store_row(c, a, tl, head, cc, d, x, mm, ll);
+}
+
+// What the join of shared prefixes and suffixes needs to know of both plans.
+struct SharedJoin {
+  KvGroups g;
+  uint32_t tiles;           // of a sequence
+  int width, rows_each, turns, max_splits, split_steps;
+  uint32_t prefix_tiles;    // of a group
+  int prefix_width, prefix_splits, prefix_keys;  // keys of a part
+  int64_t suffix_parts;     // floats before them
+};
+
+// The same as join_kernel for rows whose keys are those of a shared prefix and of the
+// sequence's own suffix (in steps of N).
+template <int D, int N>
+__global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, KvAttention a,
+                                                          SharedJoin j) {
+  constexpr int QUADS = D / 4;
+  __shared__ f32x4 xs[256];
+  __shared__ float2 mls[256];
+  const int d = (threadIdx.x % QUADS) * 4, t = threadIdx.x / QUADS, turn = t % j.turns;
+  const int rows = 256 / QUADS / j.turns;
+  uint32_t w = blockIdx.x;
+  const int cc = (w % (uint32_t)j.rows_each) * rows + t / j.turns;
+  w /= (uint32_t)j.rows_each;
+  const uint32_t item = w;
+  const int head = w % (uint32_t)c.kv_heads;
+  w /= (uint32_t)c.kv_heads;
+  const int64_t seq = w / j.tiles;
+  const Tile tl(c, b, a, seq, w % j.tiles, j.width);
+  if (tl.empty()) return;
+  const int64_t group = j.g.group_of(b, seq);
+  const int shared = group < 0 ? 0 : j.g.shared(b, group);
+  const Steps<N> steps(shared / N, tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
+  const int splits = steps.count <= j.split_steps ? 1 : (steps.count + j.split_steps - 1) / j.split_steps;
+  if (shared == 0 && splits == 1) return;  // written already
+  const bool on = cc < j.width && tl.r0 + cc < tl.rows;
+  const uint32_t r = on ? tl.r0 + cc : tl.rows - 1;
+  const float *own = static_cast<const float *>(a.ws) + j.suffix_parts +
+                     (int64_t)item * j.max_splits * part_floats(j.width, D);
+  const int own_row = (int)(r - tl.r0);
+  // the row among its group's
+  const float *others = own;
+  int others_row = 0, others_count = 0;
+  if (shared > 0) {
+    const int64_t at = tl.row0 + r / tl.group - b.first_row(j.g.first_of(b, group));
+    if (at >= 0 && at < j.g.max_rows) {
+      const uint32_t i = (uint32_t)at * tl.group + r % tl.group;
+      const int64_t part = (group * j.prefix_tiles + i / (uint32_t)j.prefix_width) * c.kv_heads + head;
+      others = static_cast<const float *>(a.ws) + part * j.prefix_splits * part_floats(j.prefix_width, D);
+      others_row = (int)(i % (uint32_t)j.prefix_width);
+      others_count = j.g.parts(shared, j.prefix_keys);
+    }
+  }
+  float mm = -INFINITY, ll = 0.0f;
+  f32x4 x = {0, 0, 0, 0};
+  const int parts = others_count + splits;
+  for (int s0 = turn; s0 < parts; s0 += 8 * j.turns) {
+    float2 ml[8];
+    f32x4 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = min(s0 + i * j.turns, parts - 1);
+      const bool mine = s >= others_count;
+      const int width = mine ? j.width : j.prefix_width, row = mine ? own_row : others_row;
+      const float *from = mine ? own + (s - others_count) * part_floats(j.width, D)
+                               : others + s * part_floats(j.prefix_width, D);
+      ml[i] = *reinterpret_cast<const float2 *>(from + width * D + 2 * row);
+      y[i] = *reinterpret_cast<const f32x4 *>(from + row * D + d);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i * j.turns < parts) join(mm, ll, x, ml[i].x, ml[i].y, y[i]);
+  }
+  if (j.turns > 1) {
+    xs[threadIdx.x] = x;
+    mls[threadIdx.x] = make_float2(mm, ll);
+    __syncthreads();
+    if (turn == 0)
+      for (int i = 1; i < j.turns; ++i) {
+        const float2 other = mls[threadIdx.x + i * QUADS];
+        join(mm, ll, x, other.x, other.y, xs[threadIdx.x + i * QUADS]);
       }
   }
   if (on && turn == 0) store_row(c, a, tl, head, cc, d, x, mm, ll);
@@ -983,17 +1236,20 @@ constexpr int64_t kFewRows = 32;
 // against 15.1 for 40 rows over 2000, 8 heads; of 16: 29.3 and 20.1.
 constexpr int64_t kMinTileSteps = 8;
 
-Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
+// `seqs` sequences (or groups) of up to `max_rows` rows; most(keys, span): the most steps of
+// that many keys for a tile whose rows stand at `span` positions.
+template <class Most>
+Plan plan_for(const KvCache &c, int64_t seqs, int64_t max_rows, int heads, Most most) {
   Plan p;
-  const int64_t group = heads / c.kv_heads, rows = b.max_rows * group, cus = device_cu_count();
+  const int64_t group = heads / c.kv_heads, rows = max_rows * group, cus = device_cu_count();
   p.teams = 1;
   p.few = rows <= kFewRows;
   p.width = p.few ? 16 : kTileRows;
   p.keys = p.few ? 32 : kTileKeys;
   p.tiles = (rows + p.width - 1) / p.width;
-  p.items = b.seqs * p.tiles * c.kv_heads;
+  p.items = seqs * p.tiles * c.kv_heads;
   const int64_t span = (p.width - 1 + group) / group + 1;  // positions of a tile's rows
-  const int64_t steps = most_steps(p.keys, b, (int)span, window, sinks);
+  const int64_t steps = most(p.keys, (int)span);
   const int64_t even = (p.items * steps + cus - 1) / cus;
   int64_t per;
   if (p.few) {
@@ -1020,46 +1276,93 @@ Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int si
   return p;
 }
 
+Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int sinks) {
+  return plan_for(c, b.seqs, b.max_rows, heads, [&](int keys, int span) {
+    return most_steps(keys, b, span, window, sinks);
+  });
+}
+
+// A group's rows may stand anywhere, so that some may see any of the shared keys.
+Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads) {
+  const int64_t longest = std::min<int64_t>(g.max_shared, b.max_len);
+  return plan_for(c, g.groups, g.max_rows, heads, [&](int keys, int) {
+    return std::max<int64_t>((longest + keys - 1) / keys, 1);
+  });
+}
+
+// Whether a call takes the shared keys apart: not where there are none, nor where a
+// sequence's own rows fill the tiles that its keys are read for.
+bool apart(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads) {
+  return g.max_shared > 0 && b.max_len > 0 && (int64_t)b.max_rows * (heads / c.kv_heads) <= kTileRows;
+}
+
+int64_t plan_floats(const Plan &p, int head_dim) {
+  return p.items * p.splits * part_floats(p.width, head_dim);
+}
+
+// Rows of a tile side by side in a workgroup of the join, and turns over the parts: as
+// many turns as there are four parts for each, the rest of the threads on other rows.
+int join_turns(int head_dim, int64_t parts) {
+  int turns = 256 / (head_dim / 4);
+  while (turns > 1 && parts <= 2 * turns) turns /= 2;
+  return turns;
+}
+
 }  // namespace
 
 size_t kv_attention_workspace_bytes(const KvCache &c, const KvBatch &b, int heads, int window,
                                     int sinks) {
   const Plan p = make_plan(c, b, heads, window, sinks);
   if (p.splits == 1) return 0;
-  return (size_t)(p.items * p.splits * part_floats(p.width, c.head_dim)) * sizeof(float);
+  return (size_t)plan_floats(p, c.head_dim) * sizeof(float);
 }
+
+size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, const KvGroups &g,
+                                           int heads, int window, int sinks) {
+  if (!apart(c, b, g, heads)) return kv_attention_workspace_bytes(c, b, heads, window, sinks);
+  const Plan p = prefix_plan(c, b, g, heads), own = make_plan(c, b, heads, window, sinks);
+  return (size_t)(plan_floats(p, c.head_dim) + plan_floats(own, c.head_dim)) * sizeof(float);
+}
+
+namespace {
+
+// Up to 2^31 threads a launch.
+bool fits(const Plan &p) { return p.items * p.splits <= 0x7FFFFFFF / (256 * p.teams); }
+
+template <class S>
+hipError_t launch_part(const KvCache &c, int64_t layer, const KvBatch &b, const KvAttention &a,
+                       const Plan &p, const S &scope, hipStream_t s) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits)), dim3(256 * p.teams), 0, s, c,
+                       layer, b, a, (uint32_t)p.tiles, (int)p.splits, p.split_steps, scope);
+  };
+  if (p.few) {
+    if (c.head_dim == 128) go(decode_kernel<128, kWaves, S>);
+    else go(decode_kernel<64, kWaves, S>);
+  } else {
+    if (p.teams == 1) {
+      if (c.head_dim == 128) go(tile_kernel<128, 1, S>);
+      else go(tile_kernel<64, 1, S>);
+    } else {
+      if (c.head_dim == 128) go(tile_kernel<128, 2, S>);
+      else go(tile_kernel<64, 2, S>);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
 
 hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b,
                                const KvAttention &a, hipStream_t s) {
   const Plan p = make_plan(c, b, a.heads, a.window, a.sinks);
-  const int64_t grid = p.items * p.splits;
-  // the join: as many turns as there are four parts for each, the rest of the
-  // threads on other rows
   const int64_t cols = std::min<int64_t>(p.width, (int64_t)b.max_rows * (a.heads / c.kv_heads));
-  int turns = 256 / (c.head_dim / 4);
-  while (turns > 1 && p.splits <= 2 * turns) turns /= 2;
+  const int turns = join_turns(c.head_dim, p.splits);
   const int at_once = 256 / (c.head_dim / 4) / turns;
   const int64_t groups = (cols + at_once - 1) / at_once;
-  // up to 2^31 threads a launch
-  if (grid > 0x7FFFFFFF / (256 * p.teams)) return hipErrorInvalidConfiguration;
+  if (!fits(p)) return hipErrorInvalidConfiguration;
   if (p.splits > 1 && p.items * groups > 0x7FFFFFFF / 256) return hipErrorInvalidConfiguration;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256 * p.teams), 0, s, c, layer, b, a,
-                       (uint32_t)p.tiles, (int)p.splits, p.split_steps);
-  };
-  if (p.few) {
-    if (c.head_dim == 128) go(decode_kernel<128, kWaves>);
-    else go(decode_kernel<64, kWaves>);
-  } else {
-    if (p.teams == 1) {
-      if (c.head_dim == 128) go(tile_kernel<128, 1>);
-      else go(tile_kernel<64, 1>);
-    } else {
-      if (c.head_dim == 128) go(tile_kernel<128, 2>);
-      else go(tile_kernel<64, 2>);
-    }
-  }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = launch_part(c, layer, b, a, p, Whole{}, s);
   if (e != hipSuccess || p.splits == 1) return e;
   auto join = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * groups)), dim3(256), 0, s, c, b, a,
@@ -1072,6 +1375,46 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
   } else {
     if (c.head_dim == 128) join(join_kernel<128, kTileKeys>);
     else join(join_kernel<64, kTileKeys>);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvBatch &b,
+                                      const KvGroups &g, const KvAttention &a, hipStream_t s) {
+  if (!apart(c, b, g, a.heads)) return launch_kv_attention(c, layer, b, a, s);
+  const Plan p = prefix_plan(c, b, g, a.heads), own = make_plan(c, b, a.heads, a.window, a.sinks);
+  const int64_t cols = std::min<int64_t>(own.width, (int64_t)b.max_rows * (a.heads / c.kv_heads));
+  const int turns = join_turns(c.head_dim, p.splits + own.splits);
+  const int at_once = 256 / (c.head_dim / 4) / turns;
+  const int64_t groups = (cols + at_once - 1) / at_once;
+  if (!fits(p) || !fits(own) || own.items * groups > 0x7FFFFFFF / 256)
+    return hipErrorInvalidConfiguration;
+  const int64_t floats = plan_floats(p, c.head_dim);
+  hipError_t e = launch_part(c, layer, b, a, p, Prefix{g}, s);
+  if (e != hipSuccess) return e;
+  e = launch_part(c, layer, b, a, own, Suffix{g, floats}, s);
+  if (e != hipSuccess) return e;
+  const SharedJoin j{g,
+                     (uint32_t)own.tiles,
+                     own.width,
+                     (int)groups,
+                     turns,
+                     (int)own.splits,
+                     own.split_steps,
+                     (uint32_t)p.tiles,
+                     p.width,
+                     (int)p.splits,
+                     p.split_steps * p.keys,
+                     floats};
+  auto join = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(own.items * groups)), dim3(256), 0, s, c, b, a, j);
+  };
+  if (own.few) {
+    if (c.head_dim == 128) join(join_shared_kernel<128, 32>);
+    else join(join_shared_kernel<64, 32>);
+  } else {
+    if (c.head_dim == 128) join(join_shared_kernel<128, kTileKeys>);
+    else join(join_shared_kernel<64, kTileKeys>);
   }
   return hipGetLastError();
 }

@@ -61,6 +61,69 @@ struct KvBatch {
     len = l < 0 ? 0 : l > held_len ? held_len : l;
     end = len > max_len ? max_len : len;
   }
+  // The first row of sequence s, s = seqs: past the last one's.
+  __device__ int64_t first_row(int64_t s) const {
+    const int64_t r = row_start ? row_start[s] : s;
+    return r < 0 ? 0 : r > rows ? rows : r;
+  }
+  // The position of a row of one of the sequences first .. past - 1 (of the last of them
+  // whose rows begin no later).
+  __device__ int position(int64_t row, int64_t first, int64_t past) const {
+    int64_t lo = first, hi = past;
+    if (!row_start) {
+      lo = row;
+    } else {
+      // as many rows each, most often: then this is the one
+      const int64_t r0 = row_start[first], n = row_start[past] - r0;
+      const int64_t guess = n > 0 && row >= r0 ? first + (row - r0) * (past - first) / n : first;
+      if (guess < past && row_start[guess] <= row && row < row_start[guess + 1]) {
+        lo = guess;
+      } else {
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) / 2;
+          (row_start[mid] <= row ? lo : hi) = mid;
+        }
+      }
+    }
+    int64_t row0;
+    int n, len, end;
+    sequence(lo, row0, n, len, end);
+    return len - n + (int)(row - row0);
+  }
+};
+
+// Sequences first[g] .. first[g + 1] - 1 begin with the same shared_len[g] tokens.
+struct KvGroups {
+  int64_t groups;
+  int max_rows, max_shared;
+  const int32_t *first, *shared_len;  // first null: one group of all
+
+  __device__ int64_t first_of(const KvBatch &b, int64_t g) const {
+    const int64_t s = first ? first[g] : g == 0 ? 0 : b.seqs;
+    return s < 0 ? 0 : s > b.seqs ? b.seqs : s;
+  }
+  // The group of a sequence, -1: of none.
+  __device__ int64_t group_of(const KvBatch &b, int64_t s) const {
+    int64_t lo = 0, hi = groups;
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) / 2;
+      (first_of(b, mid) <= s ? lo : hi) = mid;
+    }
+    return first_of(b, lo) <= s && s < first_of(b, lo + 1) ? lo : -1;
+  }
+  // Tokens that group g shares and the table has a place for.
+  __device__ int shared(const KvBatch &b, int64_t g) const {
+    const int n = shared_len[g], most = max_shared < b.max_len ? max_shared : b.max_len;
+    return n < 0 ? 0 : n > most ? most : n;
+  }
+  __device__ int shared_of(const KvBatch &b, int64_t s) const {
+    const int64_t g = group_of(b, s);
+    return g < 0 ? 0 : shared(b, g);
+  }
+  // Parts of so many shared tokens.
+  __device__ static int parts(int shared, int keys) {
+    return (int)(((int64_t)shared + keys - 1) / keys);
+  }
 };
 
 struct KvPool {
@@ -125,6 +188,11 @@ size_t kv_attention_workspace_bytes(const KvCache &c, const KvBatch &b, int head
                                     int sinks);
 hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b,
                                const KvAttention &a, hipStream_t s);
+
+size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, const KvGroups &g,
+                                           int heads, int window, int sinks);
+hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvBatch &b,
+                                      const KvGroups &g, const KvAttention &a, hipStream_t s);
 
 hipError_t launch_kv_copy_pages(const KvCache &c, const int32_t *src, const int32_t *dst,
                                 int64_t n, hipStream_t s);

@@ -26,7 +26,9 @@ EXPORTS = ("nf4_status_string", "nf4_codebook", "nf4_qweight_bytes", "nf4_absmax
            "nf4_kv_code_bytes", "nf4_kv_scale_bytes", "nf4_kv_append",
            "nf4_kv_read", "nf4_rotary_frequencies", "nf4_rotary_init", "nf4_rotate",
            "nf4_kv_append_rotated",
-           "nf4_kv_attention_workspace_bytes", "nf4_kv_attention", "nf4_kv_copy_pages",
+           "nf4_kv_attention_workspace_bytes", "nf4_kv_attention",
+           "nf4_kv_attention_shared_workspace_bytes", "nf4_kv_attention_shared",
+           "nf4_kv_copy_pages",
            "nf4_kv_reserve", "nf4_kv_fork", "nf4_kv_release", "nf4_kv_compact_workspace_bytes",
            "nf4_kv_compact")
 
@@ -48,6 +50,11 @@ class _KVBatch(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in ("seqs", "rows", "max_rows", "max_len")] + \
                [(f, ctypes.c_void_p) for f in ("row_start", "kv_len", "table")] + \
                [("table_stride", ctypes.c_int64), ("table_entries", ctypes.c_int64)]
+
+
+class _KVGroups(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in ("groups", "max_rows", "max_prefix")] + \
+               [(f, ctypes.c_void_p) for f in ("first", "prefix_len")]
 
 
 class _KVPool(ctypes.Structure):
@@ -148,6 +155,12 @@ def lib() -> ctypes.CDLL:
         L.nf4_kv_attention.restype = st
         L.nf4_kv_attention.argtypes = [cache, i64, batch, vp, i64, i64, ctypes.c_float, i64, i64,
                                        vp, vp, vp, sz, vp]
+        groups = ctypes.POINTER(_KVGroups)
+        L.nf4_kv_attention_shared_workspace_bytes.restype = sz
+        L.nf4_kv_attention_shared_workspace_bytes.argtypes = [cache, batch, groups, i64, i64, i64]
+        L.nf4_kv_attention_shared.restype = st
+        L.nf4_kv_attention_shared.argtypes = [cache, i64, batch, groups, vp, i64, i64,
+                                              ctypes.c_float, i64, i64, vp, vp, vp, sz, vp]
         L.nf4_kv_copy_pages.restype = st
         L.nf4_kv_copy_pages.argtypes = [cache, vp, vp, i64, vp]
         L.nf4_kv_reserve.restype = st
@@ -449,6 +462,25 @@ def nf4_kv_attention(cache, layer: int, batch, q, q_stride: int, heads: int, sca
                                   _stream(stream)), "nf4_kv_attention")
 
 
+def nf4_kv_attention_shared_workspace_bytes(cache, batch, groups, heads: int, window: int = 0,
+                                            sinks: int = 0) -> int:
+    return lib().nf4_kv_attention_shared_workspace_bytes(cache.arg, batch.arg, groups.arg, heads,
+                                                         window, sinks)
+
+
+def nf4_kv_attention_shared(cache, layer: int, batch, groups, q, q_stride: int, heads: int,
+                            scale: float, window: int, sinks: int, out, lse=None, workspace=None,
+                            ws_bytes: int = 0, stream=None) -> None:
+    where = "nf4_kv_attention_shared"
+    _on_gpu(where, cache.gpu, batch.gpu)
+    _on_gpu(where, cache.gpu, groups.gpu)
+    _operands(where, cache.gpu, NF4_KV_BF16, q, out)
+    _operands(where, cache.gpu, NF4_KV_F32, lse)
+    _check(lib().nf4_kv_attention_shared(cache.arg, layer, batch.arg, groups.arg, _ptr(q), q_stride,
+                                         heads, scale, window, sinks, _ptr(out), _ptr(lse),
+                                         _ptr(workspace), ws_bytes, _stream(stream)), where)
+
+
 def nf4_kv_copy_pages(cache, src, dst, n: int, stream=None) -> None:
     _on_gpu("nf4_kv_copy_pages", cache.gpu)
     _check(lib().nf4_kv_copy_pages(cache.arg, _ptr(src), _ptr(dst), n, _stream(stream)),
@@ -613,6 +645,24 @@ class KVBatch:
                                table.shape[1])
         self.arg = ctypes.pointer(self.struct)
         self.gpu = _gpu(kv_len, table, row_start)
+
+
+class KVGroups:
+    """Sequences of a batch that begin with the same tokens: int32 device tensors
+    prefix_len [groups] and first [groups + 1] (None: one group of all), and the
+    host's bounds on the rows of a group (None: the batch's) and on the lengths."""
+
+    def __init__(self, prefix_len, first=None, max_rows=None, max_prefix=None):
+        groups = prefix_len.numel()
+        if groups < 1 or (groups != 1 if first is None else first.numel() != groups + 1):
+            raise NF4Error(NF4_ERR_SHAPE, "KVGroups")
+        self.prefix_len, self.first = prefix_len, first
+        self.struct = _KVGroups(groups, 0 if max_rows is None else max_rows,
+                                (1 << 30) if max_prefix is None else max_prefix,
+                                None if first is None else _int32(first).data_ptr(),
+                                _int32(prefix_len).data_ptr())
+        self.arg = ctypes.pointer(self.struct)
+        self.gpu = _gpu(prefix_len, first)
 
 
 class Rotary:

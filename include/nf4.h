@@ -585,6 +585,43 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_
                             int64_t window, int64_t sinks, hip_bfloat16 *out, float *lse,
                             void *workspace, size_t ws_bytes, hipStream_t stream);
 
+/* Sequences of a batch that begin with the same tokens, as nf4_kv_fork leaves them:
+ * sequences first[g] .. first[g + 1] - 1 (device int32[groups + 1], ascending) all
+ * have the same keys and values in their first prefix_len[g] tokens (device
+ * int32[groups]; less than 1: none), in the same pages or in copies.  Sequences of no
+ * group share nothing.  first NULL: one group of all sequences (groups == 1).
+ * max_rows bounds the rows of a group together, as the host knows it (0: the
+ * batch's rows): rows of a group past it do not see what is shared.  max_prefix, 0 ..
+ * 2^30, bounds the lengths: longer ones count as max_prefix. */
+typedef struct nf4_kv_groups {
+  int64_t groups;     /* 1 .. seqs */
+  int64_t max_rows, max_prefix;
+  const int32_t *first, *prefix_len;
+} nf4_kv_groups;
+
+/* Bytes of workspace nf4_kv_attention_shared needs, as
+ * nf4_kv_attention_workspace_bytes. */
+size_t nf4_kv_attention_shared_workspace_bytes(const nf4_kv_cache *cache,
+                                               const nf4_kv_batch *batch,
+                                               const nf4_kv_groups *groups, int64_t heads,
+                                               int64_t window, int64_t sinks);
+
+/* nf4_kv_attention for a batch whose sequences share their first tokens: what it
+ * computes, with the keys and values of a group's shared tokens read once for all of the
+ * group's rows, through the table of its first sequence (or, where each sequence's own rows
+ * are many, each through its own), and the tokens past them sequence by sequence;
+ * the two meet through the workspace.  Rows may stand anywhere, among the shared
+ * tokens too.  The weights of shared tokens are rounded to bf16 (groups of up to 32 rows
+ * of a kv head: to two bf16 terms).  Bitwise reproducible run to run for a given
+ * device.  Other arguments and errors as nf4_kv_attention; NF4_ERR_NULL for a missing
+ * structure or prefix_len, NF4_ERR_SHAPE for its sizes. */
+nf4_status nf4_kv_attention_shared(const nf4_kv_cache *cache, int64_t layer,
+                                   const nf4_kv_batch *batch, const nf4_kv_groups *groups,
+                                   const hip_bfloat16 *q, int64_t q_stride, int64_t heads,
+                                   float scale, int64_t window, int64_t sinks, hip_bfloat16 *out,
+                                   float *lse, void *workspace, size_t ws_bytes,
+                                   hipStream_t stream);
+
 /* Copy page src[i] to page dst[i], every layer, codes and scales, for i < n
  * (device int32[n] each).  Pairs with a page outside the cache are skipped; no
  * dst may be another pair's src or dst. */

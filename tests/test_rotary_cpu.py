@@ -176,6 +176,62 @@ def test_read_refusals():
         assert status(i, v) == nf4.NF4_ERR_ALIGN, (i, v)
 
 
+def groups(**kw):
+    v = dict(groups=2, max_rows=0, max_prefix=64, first=A, prefix_len=A) | kw
+    return ctypes.pointer(nf4._KVGroups(**v))
+
+
+def test_shared_attention_refusals():
+    f, size = nf4.lib().nf4_kv_attention_shared, nf4.lib().nf4_kv_attention_shared_workspace_bytes
+    ok = [cache(), 0, batch(), groups(), A, 1024, 8, 0.1, 0, 0, A, None, A, 1 << 30, None]
+
+    def status(*changes):
+        a = list(ok)
+        for i, v in changes:
+            a[i] = v
+        return f(*a)
+    for i in (0, 2, 3, 4, 10):
+        assert status((i, None)) == nf4.NF4_ERR_NULL
+    assert status((3, groups(prefix_len=None))) == nf4.NF4_ERR_NULL
+    for bad in (dict(groups=0), dict(groups=3), dict(groups=-1), dict(first=None), dict(max_rows=-1),
+                dict(max_prefix=-1), dict(max_prefix=(1 << 30) + 1)):
+        assert status((3, groups(**bad))) == nf4.NF4_ERR_SHAPE, bad
+        assert size(cache(), batch(), groups(**bad), 8, 0, 0) == 0
+    for bad in (dict(first=A + 2), dict(prefix_len=A + 1)):
+        assert status((3, groups(**bad))) == nf4.NF4_ERR_ALIGN
+    for bad, want in BAD_BATCHES:
+        assert status((2, batch(**bad))) == want
+    for bad in BAD_SHAPES:
+        assert status((0, cache(**bad))) == nf4.NF4_ERR_SHAPE
+        assert size(cache(**bad), batch(), groups(), 8, 0, 0) == 0
+    for i, v in ((1, 2), (5, 1016), (6, 0), (6, 6), (7, 0.0), (7, math.nan), (8, -1), (9, -1)):
+        assert status((i, v)) == nf4.NF4_ERR_SHAPE, (i, v)
+    for i, v in ((4, A + 8), (5, 1028), (10, A + 4), (11, A + 2)):
+        assert status((i, v)) == nf4.NF4_ERR_ALIGN, (i, v)
+    need = size(cache(), batch(), groups(), 8, 0, 0)
+    assert need > 0 and need % 16 == 0
+    assert status((12, None)) == nf4.NF4_ERR_NULL
+    assert status((13, need - 1)) == nf4.NF4_ERR_WORKSPACE
+    assert status((12, A + 8)) == nf4.NF4_ERR_ALIGN
+    # nothing shared, and rows that fill tiles by themselves: as without groups
+    plain_size = nf4.lib().nf4_kv_attention_workspace_bytes
+    assert size(cache(), batch(), groups(max_prefix=0), 8, 0, 0) == plain_size(cache(), batch(), 8, 0, 0)
+    many = batch(seqs=2, rows=400, max_rows=200, max_len=60000, table_stride=1000)
+    assert size(cache(), many, groups(), 8, 0, 0) == plain_size(cache(), many, 8, 0, 0) > 0
+
+
+def test_python_groups():
+    torch = pytest.importorskip("torch")
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    for bad in ((i(2),), (i(2), i(2)), (i(0), i(1)), (i(1).long(),), (i(2), i(3).long()), (i(2), i(6)[::2])):
+        with pytest.raises(nf4.NF4Error) as e:
+            nf4.KVGroups(*bad)
+        assert e.value.status == nf4.NF4_ERR_SHAPE
+    g = nf4.KVGroups(i(2), i(3), max_rows=5)
+    assert (g.struct.groups, g.struct.max_rows, g.struct.max_prefix, g.gpu) == (2, 5, 1 << 30, -1)
+    assert nf4.KVGroups(i(1)).struct.first is None and ctypes.sizeof(nf4._KVGroups) == 40
+
+
 def test_tensors_on_the_host_are_refused():
     torch = pytest.importorskip("torch")
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
@@ -191,6 +247,8 @@ def test_tensors_on_the_host_are_refused():
         with pytest.raises(nf4.NF4Error) as e:
             call()
         assert e.value.status == nf4.NF4_ERR_SHAPE
+    with pytest.raises(nf4.NF4Error, match="not on one GPU"):
+        nf4.nf4_kv_attention_shared(c, 0, b, nf4.KVGroups(i32(1)), out, 128, 2, 0.1, 0, 0, out, stream=0)
     c.gpu = b.gpu = 0  # structures made out to be on a GPU, rows that are not
     for call in calls[:2]:
         with pytest.raises(nf4.NF4Error, match="not on one GPU"):
