@@ -102,21 +102,31 @@ __device__ inline int lanes_min(int v) {
   return __builtin_amdgcn_readfirstlane(v);
 }
 
-// What a launch takes of the keys: all that its rows see, or, where sequences share
+// What a workgroup takes of the keys: all that its rows see, or, where sequences share
 // their first tokens, those of the shared ones (rows of a whole group at once, its
 // keys split at fixed places) or those past them.  The parts of the latter two meet in
-// the workspace.
+// the workspace: slot i holds the i-th part's sums of every row and head, [rows][heads][D],
+// the prefix's parts before the suffix's; behind all slots (m, l) of each.
+struct Shared {
+  KvGroups g;
+  int64_t row_heads;
+  int prefix_slots, slots;
+  __device__ float *sums(void *ws, int slot, int64_t row_head, int dim) const {
+    return static_cast<float *>(ws) + (slot * row_heads + row_head) * dim;
+  }
+  __device__ float2 *ml(void *ws, int slot, int64_t row_head, int dim) const {
+    return reinterpret_cast<float2 *>(static_cast<float *>(ws) + slots * row_heads * dim) +
+           (slot * row_heads + row_head);
+  }
+};
 struct Whole {
   static constexpr bool kPrefix = false, kSuffix = false;
 };
-struct Prefix {
+struct Prefix : Shared {
   static constexpr bool kPrefix = true, kSuffix = false;
-  KvGroups g;
 };
-struct Suffix {
+struct Suffix : Shared {
   static constexpr bool kPrefix = false, kSuffix = true;
-  KvGroups g;
-  int64_t parts;  // of the workspace, in floats: where the suffixes' begin
 };
 
 // The keys of one row: up to its position, inside the window or among the
@@ -193,14 +203,16 @@ struct Tile {
     p_hi = len - n + (int)(last / group);
   }
   __device__ bool empty() const { return r0 >= rows; }
+  // Row r of the tile's (counted as r0 is) among all rows and heads.
+  __device__ int64_t row_head(const KvAttention &a, int head, uint32_t r) const {
+    return (row0 + r / group) * a.heads + head * group + r % group;
+  }
   // The last key that a row at p may see: not past the table.
   __device__ int last_key(int p) const { return min(p, end - 1); }
 
-  // A tile of all rows of a group of sequences over the tokens that they share; `at` are
-  // the positions of its tokens, lane l those of tokens l and 64 + l from its first on.
+  // A tile of all rows of a group of sequences over the tokens that they share.
   __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, const KvGroups &g,
-                  int64_t first, int64_t past, int shared, uint32_t tile, uint32_t width,
-                  int (&at)[2]) {
+                  int64_t first, int64_t past, int shared, uint32_t tile, uint32_t width) {
     group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
     row0 = b.first_row(first);
     const int64_t all = first < past ? b.first_row(past) - row0 : 0;
@@ -208,11 +220,15 @@ struct Tile {
     len = end = shared;
     rows = (uint32_t)n * group;
     r0 = tile * width;
-    p_lo = 0x7FFFFFFF;
+    p_lo = 0;
     p_hi = -1;
-    if (empty()) return;
+  }
+  // The positions of its tokens: lane l has those of tokens l and 64 + l from its first on.
+  __device__ void positions(const KvBatch &b, int64_t first, int64_t past, uint32_t width,
+                            int (&at)[2]) {
     const int lane = threadIdx.x & 63;
-    const int t0 = (int)(r0 / group), t1 = (int)(min(r0 + width, rows) - 1) / (int)group;
+    const int t0 = (int)(r0 / group), t1 = (int)((min(r0 + width, rows) - 1) / group);
+    p_lo = 0x7FFFFFFF;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t0 + 64 * i + lane;
@@ -235,92 +251,80 @@ struct Tile {
 
 // Where a workgroup works: the tile `index` of sequence (or group) `seq`, part `split` of
 // its keys.
-template <class S, int N>
-struct Place;
+struct Range {
+  int begin, end, splits;  // of the list of steps; parts that the list has
+};
 
-template <int N>
-struct Place<Whole, N> {
+template <class S, int N>
+struct Place {
   const KvCache &c;
   const KvBatch &b;
   const KvAttention &a;
+  const S &scope;
   int64_t seq;
   uint32_t index, width;
-  int split, split_steps;
-  const int32_t *table;
-  static constexpr int shared = 0;
-  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const Whole &,
-                   int64_t seq, uint32_t index, uint32_t width, int split, int split_steps)
-      : c(c), b(b), a(a), seq(seq), index(index), width(width), split(split),
-        split_steps(split_steps), table(b.table + seq * b.table_stride) {}
-  __device__ static uint32_t count(const KvBatch &b, const Whole &) { return (uint32_t)b.seqs; }
-  __device__ Tile tile(int (&)[2]) const { return Tile(c, b, a, seq, index, width); }
-  __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
-    return Steps<N>(0, tl.p_lo, tl.last_key(p_hi), a.window, a.sinks);
-  }
-  __device__ int splits(const Steps<N> &s) const {
-    return s.count <= split_steps ? 1 : (s.count + split_steps - 1) / split_steps;
-  }
-  __device__ int begin() const { return split * split_steps; }
-  __device__ int end(const Steps<N> &s) const { return min(s.count, (split + 1) * split_steps); }
-  __device__ bool whole(int splits) const { return splits == 1; }
-  __device__ float *parts(float *ws) const { return ws; }
-};
-
-// A suffix is summed as a whole sequence is, from its first key past the prefix on.
-template <int N>
-struct Place<Suffix, N> : Place<Whole, N> {
-  using Base = Place<Whole, N>;
+  int split, max_splits, split_steps;
+  int64_t first, past;  // sequences of the group
   int shared;
-  int64_t first_part;
-  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const Suffix &s,
-                   int64_t seq, uint32_t index, uint32_t width, int split, int split_steps)
-      : Base(c, b, a, Whole{}, seq, index, width, split, split_steps),
-        shared(s.g.shared_of(b, seq)), first_part(s.parts) {}
-  __device__ static uint32_t count(const KvBatch &b, const Suffix &) { return (uint32_t)b.seqs; }
-  __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
-    return Steps<N>(shared / N, tl.p_lo, tl.last_key(p_hi), this->a.window, this->a.sinks);
-  }
-  __device__ bool whole(int splits) const { return splits == 1 && shared == 0; }
-  __device__ float *parts(float *ws) const { return ws + first_part; }
-};
-
-// A prefix is split at fixed keys, so that which parts there are depends on its length
-// only; each leaves its sums, also where its rows see none of its keys.
-template <int N>
-struct Place<Prefix, N> {
-  const KvCache &c;
-  const KvBatch &b;
-  const KvAttention &a;
-  const KvGroups &g;
-  int64_t first, past;
-  uint32_t index, width;
-  int split, split_steps, shared;
   const int32_t *table;
-  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const Prefix &s,
-                   int64_t group, uint32_t index, uint32_t width, int split, int split_steps)
-      : c(c), b(b), a(a), g(s.g), index(index), width(width), split(split),
-        split_steps(split_steps) {
-    first = g.first_of(b, group);
-    past = g.first_of(b, group + 1);
-    shared = g.shared(b, group);
+
+  __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const S &scope,
+                   int64_t seq, uint32_t index, uint32_t width, int split, int max_splits,
+                   int split_steps)
+      : c(c), b(b), a(a), scope(scope), seq(seq), index(index), width(width), split(split),
+        max_splits(max_splits), split_steps(split_steps), first(seq), past(seq + 1), shared(0) {
+    if constexpr (S::kPrefix) {
+      first = scope.g.first_of(b, seq);
+      past = scope.g.first_of(b, seq + 1);
+      shared = scope.g.shared(b, seq);
+    }
+    if constexpr (S::kSuffix) shared = scope.g.shared_of(b, seq);
     // (a group without sequences has no rows: nothing of its table is read)
     table = b.table + (first < b.seqs ? first : 0) * b.table_stride;
   }
-  __device__ static uint32_t count(const KvBatch &, const Prefix &s) { return (uint32_t)s.g.groups; }
-  __device__ Tile tile(int (&at)[2]) const {
-    return Tile(c, b, a, g, first, past, shared, index, width, at);
+  __device__ static uint32_t count(const KvBatch &b, const S &scope) {
+    if constexpr (S::kPrefix) return (uint32_t)scope.g.groups;
+    return (uint32_t)b.seqs;
   }
+  __device__ Tile tile() const {
+    if constexpr (S::kPrefix) return Tile(c, b, a, scope.g, first, past, shared, index, width);
+    return Tile(c, b, a, seq, index, width);
+  }
+  // Without a window what a prefix's rows see does not wait for their positions.
+  __device__ bool ahead() const { return S::kPrefix && a.window == 0; }
   __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
-    const int low = split * split_steps;
-    const int64_t keys = (int64_t)(low + split_steps) * N;
-    const int last = (int)(keys < shared ? keys : shared) - 1;
-    return Steps<N>(low, tl.p_lo, min(p_hi, last), a.window, a.sinks);
+    if constexpr (S::kPrefix) {
+      const int low = split * split_steps;
+      const int64_t keys = (int64_t)(low + split_steps) * N;
+      const int last = (int)(keys < shared ? keys : shared) - 1;
+      return Steps<N>(low, tl.p_lo, ahead() ? last : min(p_hi, last), a.window, a.sinks);
+    }
+    return Steps<N>(shared / N, tl.p_lo, tl.last_key(p_hi), a.window, a.sinks);
   }
-  __device__ int splits(const Steps<N> &) const { return g.parts(shared, split_steps * N); }
-  __device__ int begin() const { return 0; }
-  __device__ int end(const Steps<N> &s) const { return s.count; }
-  __device__ bool whole(int) const { return false; }
-  __device__ float *parts(float *ws) const { return ws; }
+  // Whether the part is one of the prefix's, which are those of its length: each leaves
+  // its sums, also where its rows see none of its keys.
+  __device__ bool there() const {
+    if constexpr (S::kPrefix) return split < KvGroups::parts(shared, split_steps * N);
+    return true;
+  }
+  __device__ Range range(const Steps<N> &s) const {
+    if constexpr (S::kPrefix) return Range{0, s.count, 1};
+    const int per = S::kSuffix ? suffix_steps(s.count, split_steps, max_splits) : split_steps;
+    return Range{split * per, min(s.count, (split + 1) * per),
+                 s.count <= per ? 1 : (s.count + per - 1) / per};
+  }
+  // Whether a range holds all keys that the rows see.
+  __device__ bool whole(const Range &r) const {
+    return !S::kPrefix && r.splits == 1 && shared == 0;
+  }
+  __device__ int slot() const {
+    if constexpr (S::kSuffix) return scope.prefix_slots + split;
+    return split;
+  }
+  // Steps of a suffix's parts: more where the host has made no room for as many parts.
+  __device__ static int suffix_steps(int count, int split_steps, int max_splits) {
+    return max(split_steps, (count + max_splits - 1) / max_splits);
+  }
 };
 
 // Workspace of a call whose keys are split: for every (item, split), an item
@@ -352,11 +356,9 @@ __device__ inline float log_sum(float m, float l) {
   return l == 0.0f ? NAN : (m + __log2f(l)) * kLn2;
 }
 
-// The result of row `cc` of a tile, values d .. d + 3, from its sums.
-__device__ inline void store_row(const KvCache &c, const KvAttention &a, const Tile &tl, int head,
-                                 int cc, int d, f32x4 x, float m, float l) {
-  const uint32_t r = tl.r0 + cc;
-  const int64_t at = (tl.row0 + r / tl.group) * a.heads + head * tl.group + r % tl.group;
+// The result of a row and head, values d .. d + 3, from its sums.
+__device__ inline void store_sums(const KvCache &c, const KvAttention &a, int64_t at, int d, f32x4 x,
+                                  float m, float l) {
   const bool none = m == -INFINITY;  // no key was seen
   const float inv = 1.0f / l;
   uint2 y;
@@ -364,6 +366,11 @@ __device__ inline void store_row(const KvCache &c, const KvAttention &a, const T
   y.y = none ? 0u : bf16_pair(x[2] * inv, x[3] * inv);
   *reinterpret_cast<uint2 *>(a.out + at * c.head_dim + d) = y;
   if (a.lse && d == 0) a.lse[at] = log_sum(m, l);
+}
+// The same of row `cc` of a tile.
+__device__ inline void store_row(const KvCache &c, const KvAttention &a, const Tile &tl, int head,
+                                 int cc, int d, f32x4 x, float m, float l) {
+  store_sums(c, a, tl.row_head(a, head, tl.r0 + cc), d, x, m, l);
 }
 
 // NaN codes in places that some row does not see would reach it as 0 * NaN, so
@@ -416,28 +423,34 @@ struct Step {
   uint4 k[2][D / 64], v[2][D / 64];
 };
 
+template <int D, int W>
+struct DecodeLds {
+  static constexpr int kPitch = D + 4;  // of a row of sums, in floats
+  float sums[W * 16 * kPitch];
+  float ml[2][W][16];
+};
+
 template <int D, int W, class S>
-__global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer, KvBatch b,
-                                                        KvAttention a, uint32_t tiles,
-                                                        int max_splits,
-                                                        int split_steps, S scope) {
+__device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatch &b,
+                                   const KvAttention &a, uint32_t tiles, int max_splits,
+                                   int split_steps, const S &scope, uint32_t w,
+                                   DecodeLds<D, W> &lds) {
   constexpr int KS = D / 32;   // k-steps of the first product
   constexpr int DT = D / 16;   // tiles of 16 values of the second
-  constexpr int PITCH = D + 4; // of a row of sums in LDS, in floats
-  __shared__ float sums[W * 16 * PITCH];
-  __shared__ float ml[2][W][16];
+  constexpr int PITCH = DecodeLds<D, W>::kPitch;
+  auto &sums = lds.sums;
+  auto &ml = lds.ml;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   // neighbouring workgroups take the heads of one page, so that what is read
   // at a time lies side by side (64 sequences of up to 16384 tokens: 256 us
   // with the parts of a head side by side instead, 217 us this way)
-  uint32_t w = blockIdx.x;
   const int head = w % (uint32_t)c.kv_heads;
   w /= (uint32_t)c.kv_heads;
   const int split = w % (uint32_t)max_splits;
   w /= (uint32_t)max_splits;
   const uint32_t item = w * (uint32_t)c.kv_heads + head;
-  const Place<S, 32> place(c, b, a, scope, w / tiles, w % tiles, 16, split, split_steps);
+  const Place<S, 32> place(c, b, a, scope, w / tiles, w % tiles, 16, split, max_splits, split_steps);
   const int32_t *table = place.table;
   // without a window, where the first page ids stand does not depend on the
   // lengths: they are read beside them (as far as the longest one may reach)
@@ -446,19 +459,19 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
     const int64_t t0 = (int64_t)(split * split_steps + wave + (lane >> 1) * W) * 32 + 16 * (lane & 1);
     page_ahead = table[min(t0, (int64_t)max(b.max_len - 1, 0)) >> c.page_shift];
   }
-  int at[2];
-  const Tile tl = place.tile(at);
+  if (!place.there()) return;
+  Tile tl = place.tile();
   if (tl.empty()) return;
+  int at[2];
+  if (S::kPrefix && !place.ahead()) tl.positions(b, place.first, place.past, 16, at);
   const Steps<32> steps = place.steps(tl, tl.p_hi);
-  const int splits = place.splits(steps);
-  if (split >= splits) return;
-  const int end = place.end(steps);
+  const Range range = place.range(steps);
+  if (!S::kPrefix && split >= range.splits) return;
+  const int end = range.end;
 
   const bool mine = tl.r0 + col < tl.rows;
   const uint32_t r = mine ? tl.r0 + col : tl.rows - 1;
   const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
-  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
-  const int pos = mine ? row_pos : -1;
 
   const int64_t layer_pages = layer * c.pages;
   const int page_blocks = 1 << (c.page_shift - 4);
@@ -467,7 +480,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   // the values' scale 2^e e and 2^-e.  Read ahead of the steps as vectors: a
   // scalar read per step would cost the step its whole latency, since scalar
   // reads return out of order and any use waits for all of them.
-  const int first = place.begin() + wave;
+  const int first = range.begin + wave;
   int page_l = -1;
   float kc_l = 0.0f, ve_l = 0.0f, vi_l = 1.0f;
   uint64_t high_l = 0;  // bit 2s + h: that block's values need kLift
@@ -512,6 +525,9 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   };
 
   look(first);
+  if (S::kPrefix && place.ahead()) tl.positions(b, place.first, place.past, 16, at);
+  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
+  const int pos = mine ? row_pos : -1;
 
   bf16x8 q[KS];
   const uint16_t *qp = a.q + (tl.row0 + tok) * a.q_stride + (int64_t)qh * D + g * 16;
@@ -649,7 +665,7 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
   // a thread's four neighbouring values of a row, over the waves
   constexpr int QUADS = D / 4;
   const int cols = (int)min(16u, tl.rows - tl.r0);
-  float *part = place.parts(static_cast<float *>(a.ws)) +
+  float *part = static_cast<float *>(a.ws) +
                 ((int64_t)item * max_splits + split) * part_floats(16, D);
   for (int u = threadIdx.x; u < cols * QUADS; u += 64 * W) {
     const int cc = u / QUADS, d = (u % QUADS) * 4;
@@ -663,13 +679,25 @@ __global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer
       ll += mv == -INFINITY ? 0.0f : ml[1][v][cc] * exp2_fast(mv - mm);
       x += *reinterpret_cast<const f32x4 *>(sums + (v * 16 + cc) * PITCH + d);
     }
-    if (place.whole(splits)) {
+    if (place.whole(range)) {
       store_row(c, a, tl, head, cc, d, x, mm, ll);
+    } else if constexpr (S::kPrefix || S::kSuffix) {
+      const int64_t at = tl.row_head(a, head, tl.r0 + cc);
+      *reinterpret_cast<f32x4 *>(scope.sums(a.ws, place.slot(), at, D) + d) = x;
+      if (d == 0) *scope.ml(a.ws, place.slot(), at, D) = make_float2(mm, ll);
     } else {
       *reinterpret_cast<f32x4 *>(part + cc * D + d) = x;
       if (d == 0) *reinterpret_cast<float2 *>(part + 16 * D + 2 * cc) = make_float2(mm, ll);
     }
   }
+}
+
+template <int D, int W>
+__global__ __launch_bounds__(64 * W) void decode_kernel(KvCache c, int64_t layer, KvBatch b,
+                                                        KvAttention a, uint32_t tiles,
+                                                        int max_splits, int split_steps) {
+  __shared__ DecodeLds<D, W> lds;
+  decode_part(c, layer, b, a, tiles, max_splits, split_steps, Whole{}, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -703,15 +731,13 @@ struct TileLds {
 };
 
 template <int D, int G, class S>
-__global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c, int64_t layer,
-                                                                      KvBatch b, KvAttention a,
-                                                                      uint32_t tiles,
-                                                                      int max_splits,
-                                                                      int split_steps, S scope) {
+__device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch &b,
+                                 const KvAttention &a, uint32_t tiles, int max_splits,
+                                 int split_steps, const S &scope, uint32_t w,
+                                 uint8_t *all_lds) {
   using L = TileLds<D>;
   constexpr int DT = D / 32;   // tiles of 32 values
   constexpr int CH = D / 16;   // 16-byte pieces of a key
-  __shared__ __align__(16) uint8_t all_lds[G * L::kBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & (kTileWaves - 1);
   // the team of four waves: team g takes steps g, g + G, .. with its own LDS
@@ -720,7 +746,6 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   const int col = lane & 31, h = lane >> 5;
   // heads first: a kv head's workgroups run on the same dies and find its keys
   // in their cache; the last rows, which see most, start first
-  uint32_t w = blockIdx.x;
   const int head = w % (uint32_t)c.kv_heads;
   w /= (uint32_t)c.kv_heads;
   const int split = w % (uint32_t)max_splits;
@@ -728,10 +753,12 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   const uint32_t seqs = Place<S, kTileKeys>::count(b, scope);
   const uint32_t seq = w % seqs;
   const uint32_t tile = tiles - 1 - w / seqs;
-  const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows, split, split_steps);
-  int at[2];
-  const Tile tl = place.tile(at);
+  const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows, split, max_splits, split_steps);
+  if (!place.there()) return;
+  Tile tl = place.tile();
   if (tl.empty()) return;
+  int at[2];
+  if (S::kPrefix && !place.ahead()) tl.positions(b, place.first, place.past, kTileRows, at);
   // the wave's rows: with two teams, waves w and w + 4 share a SIMD and hold
   // different halves of the tile
   const int sub = team == 0 ? wave : wave ^ 2;
@@ -746,23 +773,18 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     p_hi = tl.len - tl.n + (int)((min(end, tl.rows) - 1) / tl.group);
   }
   const Steps<kTileKeys> steps = place.steps(tl, p_hi);
-  const int splits = place.splits(steps);
-  if (split >= splits) return;
-  const int begin = place.begin() + team, mine_steps = place.end(steps) - place.begin();
+  const Range range = place.range(steps);
+  if (!S::kPrefix && split >= range.splits) return;
+  const int begin = range.begin + team, mine_steps = range.end - range.begin;
   const int turns = (mine_steps + G - 1) / G;
   const int n = (mine_steps - team + G - 1) / G;
 
   const bool mine = r0 + col < tl.rows, idle = r0 >= tl.rows;
   const uint32_t r = mine ? r0 + col : tl.rows - 1;
   const int tok = (int)(r / tl.group), qh = head * tl.group + (int)(r % tl.group);
-  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
-  const int pos = mine ? row_pos : -1;
+  int pos = mine ? tl.len - tl.n + tok : -1;
   int w_lo = idle ? 0 : tl.len - tl.n + (int)(r0 / tl.group);
   int w_hi = idle ? -1 : tl.len - tl.n + (int)(min(r0 + 31, tl.rows - 1) / tl.group);
-  if (S::kPrefix) {
-    w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
-    w_hi = -lanes_min(-pos);
-  }
 
   // copies of one step: the wave's block of 16 keys and values, and its scales
   const int32_t *table = place.table;
@@ -823,6 +845,19 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     }
     to = to == lds0 + (kStages - 1) * L::kStage ? lds0 : to + L::kStage;
   };
+
+  if constexpr (S::kPrefix) {
+    // the copies go out before the positions come in
+    issue(0);
+    holes >>= 4;
+    issue(1);
+    holes >>= 4;
+    if (place.ahead()) tl.positions(b, place.first, place.past, kTileRows, at);
+    const int row_pos = Tile::position(at, tok - (int)(tl.r0 / tl.group));
+    pos = mine ? row_pos : -1;
+    w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
+    w_hi = -lanes_min(-pos);
+  }
 
   // the element of key piece 2m + h that step 2m + e of the first product takes
   // is value 32m + 16h + 8e
@@ -960,10 +995,12 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     }
   };
 
-  issue(0);
-  holes >>= 4;
-  issue(1);
-  holes >>= 4;  // steps 0 and 1 now have the two low places
+  if constexpr (!S::kPrefix) {
+    issue(0);
+    holes >>= 4;
+    issue(1);
+    holes >>= 4;  // steps 0 and 1 now have the two low places
+  }
   // q is waited for here: a wait inside the loop would be for the copies too
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
@@ -1013,11 +1050,11 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
   const int my_col = lane2 & 31, my_h = lane2 >> 5;
   if (r0 + my_col >= tl.rows) return;
   // element 4a + e of tile t is value DT (8a + 4h + e) + t
-  if (place.whole(splits)) {
+  if (place.whole(range)) {
     const float inv = 1.0f / sum;
     const uint32_t keep = m == -INFINITY ? 0u : ~0u;  // no key was seen
     const uint32_t row = r0 + my_col;
-    const int64_t at = (tl.row0 + row / tl.group) * a.heads + head * tl.group + row % tl.group;
+    const int64_t at = tl.row_head(a, head, row);
     uint16_t *to = a.out + at * D + my_h * (4 * DT);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1035,10 +1072,19 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
     if (a.lse && my_h == 0) a.lse[at] = log_sum(m, sum);
     return;
   }
-  const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
-  float *part =
-      place.parts(static_cast<float *>(a.ws)) + (item * max_splits + split) * part_floats(kTileRows, D);
-  const int row = 32 * sub + my_col;
+  float *x_to;
+  float2 *ml_to;
+  if constexpr (S::kPrefix || S::kSuffix) {
+    const int64_t at = tl.row_head(a, head, r0 + my_col);
+    x_to = scope.sums(a.ws, place.slot(), at, D);
+    ml_to = scope.ml(a.ws, place.slot(), at, D);
+  } else {
+    const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
+    float *part = static_cast<float *>(a.ws) + (item * max_splits + split) * part_floats(kTileRows, D);
+    const int row = 32 * sub + my_col;
+    x_to = part + row * D;
+    ml_to = reinterpret_cast<float2 *>(part + kTileRows * D) + row;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1046,9 +1092,51 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
       f32x4 y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = o[(4 * x + e) % DT][4 * i + (4 * x + e) / DT];
-      *reinterpret_cast<f32x4 *>(part + row * D + i * 8 * DT + my_h * 4 * DT + 4 * x) = y;
+      *reinterpret_cast<f32x4 *>(x_to + i * 8 * DT + my_h * 4 * DT + 4 * x) = y;
     }
-  if (my_h == 0) *reinterpret_cast<float2 *>(part + kTileRows * D + 2 * row) = make_float2(m, sum);
+  if (my_h == 0) *ml_to = make_float2(m, sum);
+}
+
+template <int D, int G>
+__global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c, int64_t layer,
+                                                                      KvBatch b, KvAttention a,
+                                                                      uint32_t tiles,
+                                                                      int max_splits,
+                                                                      int split_steps) {
+  __shared__ __align__(16) uint8_t lds[G * TileLds<D>::kBytes];
+  tile_part<D, G, Whole>(c, layer, b, a, tiles, max_splits, split_steps, Whole{}, blockIdx.x, lds);
+}
+
+// Shared first tokens: the first workgroups take the prefixes of all groups, the others
+// the suffixes of all sequences, in one launch: the former are bound by the vector
+// unit, the latter by memory.
+struct SharedPlan {
+  uint32_t prefix_grid, prefix_tiles, tiles;
+  int prefix_splits, prefix_steps, splits, steps;
+};
+
+template <int D, bool FEW_PREFIX, bool FEW>
+__global__ __launch_bounds__(256, 2) void shared_kernel(KvCache c, int64_t layer, KvBatch b,
+                                                        KvAttention a, Shared scope, SharedPlan p) {
+  using Decode = DecodeLds<D, 4>;
+  constexpr int kTile = TileLds<D>::kBytes;
+  static_assert(kTile >= (int)sizeof(Decode), "the larger of the two");
+  __shared__ __align__(16) uint8_t lds[FEW_PREFIX && FEW ? sizeof(Decode) : kTile];
+  if (blockIdx.x < p.prefix_grid) {
+    const Prefix s{scope};
+    if constexpr (FEW_PREFIX)
+      decode_part(c, layer, b, a, p.prefix_tiles, p.prefix_splits, p.prefix_steps, s, blockIdx.x,
+                  *reinterpret_cast<Decode *>(lds));
+    else
+      tile_part<D, 1, Prefix>(c, layer, b, a, p.prefix_tiles, p.prefix_splits, p.prefix_steps, s, blockIdx.x, lds);
+    return;
+  }
+  const Suffix s{scope};
+  if constexpr (FEW)
+    decode_part(c, layer, b, a, p.tiles, p.splits, p.steps, s, blockIdx.x - p.prefix_grid,
+                *reinterpret_cast<Decode *>(lds));
+  else
+    tile_part<D, 1, Suffix>(c, layer, b, a, p.tiles, p.splits, p.steps, s, blockIdx.x - p.prefix_grid, lds);
 }
 
 // Joins the parts of rows: 256 threads take four neighbouring values each of
@@ -1113,89 +1201,78 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
   if (on && turn == 0) store_row(c, a, tl, head, cc, d, x, mm, ll);
 }
 
-// What the join of shared prefixes and suffixes needs to know of both plans.
+// The same for rows whose keys are those of a shared prefix and of the sequence's own
+// suffix: a workgroup takes `256 / (D / 4) / turns` rows and heads of a sequence, which lie
+// side by side in every slot.
 struct SharedJoin {
-  KvGroups g;
-  uint32_t tiles;           // of a sequence
-  int width, rows_each, turns, max_splits, split_steps;
-  uint32_t prefix_tiles;    // of a group
-  int prefix_width, prefix_splits, prefix_keys;  // keys of a part
-  int64_t suffix_parts;     // floats before them
+  int prefix_keys;                   // of a part
+  int width, keys, splits, steps;    // the suffix's plan
+  int turns;
+  uint32_t per_seq;                  // workgroups of a sequence
 };
 
-// The same as join_kernel for rows whose keys are those of a shared prefix and of the
-// sequence's own suffix (in steps of N).
 template <int D, int N>
 __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, KvAttention a,
-                                                          SharedJoin j) {
+                                                          Shared scope, SharedJoin j) {
   constexpr int QUADS = D / 4;
   __shared__ f32x4 xs[256];
   __shared__ float2 mls[256];
   const int d = (threadIdx.x % QUADS) * 4, t = threadIdx.x / QUADS, turn = t % j.turns;
-  const int rows = 256 / QUADS / j.turns;
-  uint32_t w = blockIdx.x;
-  const int cc = (w % (uint32_t)j.rows_each) * rows + t / j.turns;
-  w /= (uint32_t)j.rows_each;
-  const uint32_t item = w;
-  const int head = w % (uint32_t)c.kv_heads;
-  w /= (uint32_t)c.kv_heads;
-  const int64_t seq = w / j.tiles;
-  const Tile tl(c, b, a, seq, w % j.tiles, j.width);
-  if (tl.empty()) return;
-  const int64_t group = j.g.group_of(b, seq);
-  const int shared = group < 0 ? 0 : j.g.shared(b, group);
-  const Steps<N> steps(shared / N, tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
-  const int splits = steps.count <= j.split_steps ? 1 : (steps.count + j.split_steps - 1) / j.split_steps;
-  if (shared == 0 && splits == 1) return;  // written already
-  const bool on = cc < j.width && tl.r0 + cc < tl.rows;
-  const uint32_t r = on ? tl.r0 + cc : tl.rows - 1;
-  const float *own = static_cast<const float *>(a.ws) + j.suffix_parts +
-                     (int64_t)item * j.max_splits * part_floats(j.width, D);
-  const int own_row = (int)(r - tl.r0);
-  // the row among its group's
-  const float *others = own;
-  int others_row = 0, others_count = 0;
-  if (shared > 0) {
-    const int64_t at = tl.row0 + r / tl.group - b.first_row(j.g.first_of(b, group));
-    if (at >= 0 && at < j.g.max_rows) {
-      const uint32_t i = (uint32_t)at * tl.group + r % tl.group;
-      const int64_t part = (group * j.prefix_tiles + i / (uint32_t)j.prefix_width) * c.kv_heads + head;
-      others = static_cast<const float *>(a.ws) + part * j.prefix_splits * part_floats(j.prefix_width, D);
-      others_row = (int)(i % (uint32_t)j.prefix_width);
-      others_count = j.g.parts(shared, j.prefix_keys);
-    }
+  const int64_t seq = blockIdx.x / j.per_seq;
+  const uint32_t first_row_head = (blockIdx.x % j.per_seq) * (256 / QUADS / j.turns);
+  const uint32_t group_heads = (uint32_t)a.heads / (uint32_t)c.kv_heads;
+  int64_t row0;
+  int n, len, end;
+  b.sequence(seq, row0, n, len, end);
+  const int rows = n < b.max_rows ? n : b.max_rows;
+  int64_t first;
+  int shared = scope.g.shared_of(b, seq, &first);
+  if (first_row_head >= (uint32_t)rows * a.heads) return;
+  const uint32_t i = first_row_head + t / j.turns;
+  const bool on = i < (uint32_t)rows * a.heads;
+  const int tok = on ? (int)(i / a.heads) : 0;
+  // the steps of the tile that the row is in
+  const uint32_t r = tok * group_heads + (i % a.heads) % group_heads, r0 = r / j.width * j.width;
+  const uint32_t r1 = min(r0 + j.width, (uint32_t)rows * group_heads) - 1;
+  const int begin = len - n, p_lo = begin + (int)(r0 / group_heads), p_hi = begin + (int)(r1 / group_heads);
+  const Steps<N> steps(shared / N, p_lo, min(p_hi, end - 1), a.window, a.sinks);
+  const int per = Place<Suffix, N>::suffix_steps(steps.count, j.steps, j.splits);
+  const int splits = steps.count <= per ? 1 : (steps.count + per - 1) / per;
+  const bool written = shared == 0 && splits == 1;
+  int shared_parts = KvGroups::parts(shared, j.prefix_keys);
+  if (scope.g.max_rows < b.rows && shared > 0) {
+    const int64_t at = row0 + tok - b.first_row(first);  // the row among its group's
+    if (at < 0 || at >= scope.g.max_rows) shared_parts = 0;
   }
+  const int64_t row_head = row0 * a.heads + (on ? i : 0);
+  const int parts = on && !written ? shared_parts + splits : 0;
   float mm = -INFINITY, ll = 0.0f;
   f32x4 x = {0, 0, 0, 0};
-  const int parts = others_count + splits;
   for (int s0 = turn; s0 < parts; s0 += 8 * j.turns) {
     float2 ml[8];
     f32x4 y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = min(s0 + i * j.turns, parts - 1);
-      const bool mine = s >= others_count;
-      const int width = mine ? j.width : j.prefix_width, row = mine ? own_row : others_row;
-      const float *from = mine ? own + (s - others_count) * part_floats(j.width, D)
-                               : others + s * part_floats(j.prefix_width, D);
-      ml[i] = *reinterpret_cast<const float2 *>(from + width * D + 2 * row);
-      y[i] = *reinterpret_cast<const f32x4 *>(from + row * D + d);
+    for (int u = 0; u < 8; ++u) {
+      int s = min(s0 + u * j.turns, parts - 1);
+      s = s < shared_parts ? s : s - shared_parts + scope.prefix_slots;
+      ml[u] = *scope.ml(a.ws, s, row_head, D);
+      y[u] = *reinterpret_cast<const f32x4 *>(scope.sums(a.ws, s, row_head, D) + d);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (s0 + i * j.turns < parts) join(mm, ll, x, ml[i].x, ml[i].y, y[i]);
+    for (int u = 0; u < 8; ++u)
+      if (s0 + u * j.turns < parts) join(mm, ll, x, ml[u].x, ml[u].y, y[u]);
   }
   if (j.turns > 1) {
     xs[threadIdx.x] = x;
     mls[threadIdx.x] = make_float2(mm, ll);
     __syncthreads();
     if (turn == 0)
-      for (int i = 1; i < j.turns; ++i) {
-        const float2 other = mls[threadIdx.x + i * QUADS];
-        join(mm, ll, x, other.x, other.y, xs[threadIdx.x + i * QUADS]);
+      for (int u = 1; u < j.turns; ++u) {
+        const float2 other = mls[threadIdx.x + u * QUADS];
+        join(mm, ll, x, other.x, other.y, xs[threadIdx.x + u * QUADS]);
       }
   }
-  if (on && turn == 0) store_row(c, a, tl, head, cc, d, x, mm, ll);
+  if (parts > 0 && turn == 0) store_sums(c, a, row_head, d, x, mm, ll);
 }
 
 // How a call is launched: in tiles of `width` rows, a workgroup taking
@@ -1285,9 +1362,22 @@ Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int si
 // A group's rows may stand anywhere, so that some may see any of the shared keys.
 Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads) {
   const int64_t longest = std::min<int64_t>(g.max_shared, b.max_len);
-  return plan_for(c, g.groups, g.max_rows, heads, [&](int keys, int) {
+  Plan p = plan_for(c, g.groups, g.max_rows, heads, [&](int keys, int) {
     return std::max<int64_t>((longest + keys - 1) / keys, 1);
   });
+  p.teams = 1;
+  return p;
+}
+
+// The suffixes are as long as the bounds say if the longest sequence has the longest
+// prefix.  That is a guess: where it is not so, a part has more steps.
+Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window,
+                 int sinks) {
+  KvBatch guess = b;
+  if (g.max_shared < b.max_len) guess.max_len = b.max_len - g.max_shared;
+  Plan p = make_plan(c, guess, heads, window, sinks);
+  p.teams = 1;
+  return p;
 }
 
 // Whether a call takes the shared keys apart: not where there are none, nor where a
@@ -1320,36 +1410,14 @@ size_t kv_attention_workspace_bytes(const KvCache &c, const KvBatch &b, int head
 size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, const KvGroups &g,
                                            int heads, int window, int sinks) {
   if (!apart(c, b, g, heads)) return kv_attention_workspace_bytes(c, b, heads, window, sinks);
-  const Plan p = prefix_plan(c, b, g, heads), own = make_plan(c, b, heads, window, sinks);
-  return (size_t)(plan_floats(p, c.head_dim) + plan_floats(own, c.head_dim)) * sizeof(float);
+  const Plan p = prefix_plan(c, b, g, heads), own = suffix_plan(c, b, g, heads, window, sinks);
+  return (size_t)((p.splits + own.splits) * b.rows * heads * (c.head_dim + 2)) * sizeof(float);
 }
 
 namespace {
 
 // Up to 2^31 threads a launch.
 bool fits(const Plan &p) { return p.items * p.splits <= 0x7FFFFFFF / (256 * p.teams); }
-
-template <class S>
-hipError_t launch_part(const KvCache &c, int64_t layer, const KvBatch &b, const KvAttention &a,
-                       const Plan &p, const S &scope, hipStream_t s) {
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits)), dim3(256 * p.teams), 0, s, c,
-                       layer, b, a, (uint32_t)p.tiles, (int)p.splits, p.split_steps, scope);
-  };
-  if (p.few) {
-    if (c.head_dim == 128) go(decode_kernel<128, kWaves, S>);
-    else go(decode_kernel<64, kWaves, S>);
-  } else {
-    if (p.teams == 1) {
-      if (c.head_dim == 128) go(tile_kernel<128, 1, S>);
-      else go(tile_kernel<64, 1, S>);
-    } else {
-      if (c.head_dim == 128) go(tile_kernel<128, 2, S>);
-      else go(tile_kernel<64, 2, S>);
-    }
-  }
-  return hipGetLastError();
-}
 
 }  // namespace
 
@@ -1362,7 +1430,23 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
   const int64_t groups = (cols + at_once - 1) / at_once;
   if (!fits(p)) return hipErrorInvalidConfiguration;
   if (p.splits > 1 && p.items * groups > 0x7FFFFFFF / 256) return hipErrorInvalidConfiguration;
-  const hipError_t e = launch_part(c, layer, b, a, p, Whole{}, s);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits)), dim3(256 * p.teams), 0, s, c,
+                       layer, b, a, (uint32_t)p.tiles, (int)p.splits, p.split_steps);
+  };
+  if (p.few) {
+    if (c.head_dim == 128) go(decode_kernel<128, kWaves>);
+    else go(decode_kernel<64, kWaves>);
+  } else {
+    if (p.teams == 1) {
+      if (c.head_dim == 128) go(tile_kernel<128, 1>);
+      else go(tile_kernel<64, 1>);
+    } else {
+      if (c.head_dim == 128) go(tile_kernel<128, 2>);
+      else go(tile_kernel<64, 2>);
+    }
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   auto join = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * groups)), dim3(256), 0, s, c, b, a,
@@ -1382,32 +1466,38 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
 hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvBatch &b,
                                       const KvGroups &g, const KvAttention &a, hipStream_t s) {
   if (!apart(c, b, g, a.heads)) return launch_kv_attention(c, layer, b, a, s);
-  const Plan p = prefix_plan(c, b, g, a.heads), own = make_plan(c, b, a.heads, a.window, a.sinks);
-  const int64_t cols = std::min<int64_t>(own.width, (int64_t)b.max_rows * (a.heads / c.kv_heads));
+  const Plan p = prefix_plan(c, b, g, a.heads);
+  const Plan own = suffix_plan(c, b, g, a.heads, a.window, a.sinks);
   const int turns = join_turns(c.head_dim, p.splits + own.splits);
   const int at_once = 256 / (c.head_dim / 4) / turns;
-  const int64_t groups = (cols + at_once - 1) / at_once;
-  if (!fits(p) || !fits(own) || own.items * groups > 0x7FFFFFFF / 256)
+  const int64_t per_seq = ((int64_t)b.max_rows * a.heads + at_once - 1) / at_once;
+  if (!fits(p) || !fits(own) || b.seqs * per_seq > 0x7FFFFFFF / 256 ||
+      p.items * p.splits + own.items * own.splits > 0x7FFFFFFF / 256)
     return hipErrorInvalidConfiguration;
-  const int64_t floats = plan_floats(p, c.head_dim);
-  hipError_t e = launch_part(c, layer, b, a, p, Prefix{g}, s);
+  const Shared scope{g, b.rows * a.heads, (int)p.splits, (int)(p.splits + own.splits)};
+  const SharedPlan plan{(uint32_t)(p.items * p.splits), (uint32_t)p.tiles, (uint32_t)own.tiles,
+                        (int)p.splits, p.split_steps, (int)own.splits, own.split_steps};
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits + own.items * own.splits)), dim3(256),
+                       0, s, c, layer, b, a, scope, plan);
+  };
+  if (c.head_dim == 128) {
+    if (p.few && own.few) go(shared_kernel<128, true, true>);
+    else if (own.few) go(shared_kernel<128, false, true>);
+    else if (p.few) go(shared_kernel<128, true, false>);
+    else go(shared_kernel<128, false, false>);
+  } else {
+    if (p.few && own.few) go(shared_kernel<64, true, true>);
+    else if (own.few) go(shared_kernel<64, false, true>);
+    else if (p.few) go(shared_kernel<64, true, false>);
+    else go(shared_kernel<64, false, false>);
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = launch_part(c, layer, b, a, own, Suffix{g, floats}, s);
-  if (e != hipSuccess) return e;
-  const SharedJoin j{g,
-                     (uint32_t)own.tiles,
-                     own.width,
-                     (int)groups,
-                     turns,
-                     (int)own.splits,
-                     own.split_steps,
-                     (uint32_t)p.tiles,
-                     p.width,
-                     (int)p.splits,
-                     p.split_steps * p.keys,
-                     floats};
+  const SharedJoin j{p.split_steps * p.keys, own.width, own.keys, (int)own.splits, own.split_steps, turns,
+                     (uint32_t)per_seq};
   auto join = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(own.items * groups)), dim3(256), 0, s, c, b, a, j);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(b.seqs * per_seq)), dim3(256), 0, s, c, b, a, scope, j);
   };
   if (own.few) {
     if (c.head_dim == 128) join(join_shared_kernel<128, 32>);

@@ -69,25 +69,25 @@ struct KvBatch {
   // The position of a row of one of the sequences first .. past - 1 (of the last of them
   // whose rows begin no later).
   __device__ int position(int64_t row, int64_t first, int64_t past) const {
-    int64_t lo = first, hi = past;
-    if (!row_start) {
-      lo = row;
-    } else {
+    int64_t s = row;
+    if (row_start) {
       // as many rows each, most often: then this is the one
       const int64_t r0 = row_start[first], n = row_start[past] - r0;
-      const int64_t guess = n > 0 && row >= r0 ? first + (row - r0) * (past - first) / n : first;
-      if (guess < past && row_start[guess] <= row && row < row_start[guess + 1]) {
-        lo = guess;
-      } else {
-        while (hi - lo > 1) {
-          const int64_t mid = (lo + hi) / 2;
-          (row_start[mid] <= row ? lo : hi) = mid;
-        }
+      int64_t guess = n > 0 && row >= r0 ? first + (row - r0) * (past - first) / n : first;
+      guess = guess < past ? guess : past - 1;
+      const int from = row_start[guess], to = row_start[guess + 1], len = kv_len[guess];
+      if (from <= row && row < to && from >= 0 && to <= rows)
+        return (len < 0 ? 0 : len > held_len ? held_len : len) - (to - from) + (int)(row - from);
+      s = first;
+      int64_t hi = past;
+      while (hi - s > 1) {
+        const int64_t mid = (s + hi) / 2;
+        (row_start[mid] <= row ? s : hi) = mid;
       }
     }
     int64_t row0;
     int n, len, end;
-    sequence(lo, row0, n, len, end);
+    sequence(s, row0, n, len, end);
     return len - n + (int)(row - row0);
   }
 };
@@ -102,23 +102,33 @@ struct KvGroups {
     const int64_t s = first ? first[g] : g == 0 ? 0 : b.seqs;
     return s < 0 ? 0 : s > b.seqs ? b.seqs : s;
   }
-  // The group of a sequence, -1: of none.
-  __device__ int64_t group_of(const KvBatch &b, int64_t s) const {
-    int64_t lo = 0, hi = groups;
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) / 2;
-      (first_of(b, mid) <= s ? lo : hi) = mid;
-    }
-    return first_of(b, lo) <= s && s < first_of(b, lo + 1) ? lo : -1;
-  }
   // Tokens that group g shares and the table has a place for.
-  __device__ int shared(const KvBatch &b, int64_t g) const {
-    const int n = shared_len[g], most = max_shared < b.max_len ? max_shared : b.max_len;
+  __device__ int shared(const KvBatch &b, int64_t g) const { return held(b, shared_len[g]); }
+  __device__ int held(const KvBatch &b, int n) const {
+    const int most = max_shared < b.max_len ? max_shared : b.max_len;
     return n < 0 ? 0 : n > most ? most : n;
   }
-  __device__ int shared_of(const KvBatch &b, int64_t s) const {
-    const int64_t g = group_of(b, s);
-    return g < 0 ? 0 : shared(b, g);
+  // The same of the group that sequence s is in (0: in none), and that group's first
+  // sequence.  The whole wave looks, a lane at every 64th place, so that up to 64 groups
+  // take one trip to memory.
+  __device__ int shared_of(const KvBatch &b, int64_t s, int64_t *first_seq = nullptr) const {
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, hi = groups;
+    for (;;) {
+      const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
+      const int64_t here = at < hi ? at : hi - 1;
+      const int from = (int)first_of(b, here), to = (int)first_of(b, here + 1), len = shared_len[here];
+      const int in = __popcll(__ballot(at < hi && from <= s));  // ascending: the first ones
+      if (in == 0) return 0;
+      const int l = in - 1;
+      if (step == 1) {
+        const int f = __builtin_amdgcn_readlane(from, l), past = __builtin_amdgcn_readlane(to, l);
+        if (first_seq) *first_seq = f;
+        return s < past ? held(b, __builtin_amdgcn_readlane(len, l)) : 0;
+      }
+      lo += l * step;
+      hi = lo + step < hi ? lo + step : hi;
+    }
   }
   // Parts of so many shared tokens.
   __device__ static int parts(int shared, int keys) {
