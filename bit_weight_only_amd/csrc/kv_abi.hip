@@ -125,7 +125,7 @@ bool groups_shape_ok(const nf4_kv_groups &g, const nf4_kv_batch &b) {
 }
 
 nf4::KvGroups as_groups(const nf4_kv_groups &g, const nf4_kv_batch &b) {
-  return nf4::KvGroups{g.groups, (int)(g.max_rows == 0 || g.max_rows > b.rows ? b.rows : g.max_rows),
+  return nf4::KvGroups{(int)g.groups, (int)(g.max_rows == 0 || g.max_rows > b.rows ? b.rows : g.max_rows),
                        (int)g.max_prefix, g.first, g.prefix_len};
 }
 

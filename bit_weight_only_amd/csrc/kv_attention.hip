@@ -17,6 +17,7 @@
 // the weights of one query row, in the places where the right operand of
 // O^T = V^T W^T wants them.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_internal.h"
 #include "nf4_internal.h"
@@ -190,6 +191,7 @@ int64_t most_steps(int N, const KvBatch &b, int tile_rows, int window, int sinks
 // head r % group of its group.
 struct Tile {
   int64_t row0;
+  int all;                   // rows of a group, max_rows or no
   uint32_t rows, r0, group;  // rows of a kv head of one sequence stay under 2^31
   int n, len, end, p_lo, p_hi;
   __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, int64_t seq,
@@ -212,36 +214,43 @@ struct Tile {
 
   // A tile of all rows of a group of sequences over the tokens that they share.
   __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, const KvGroups &g,
-                  int64_t first, int64_t past, int shared, uint32_t tile, uint32_t width) {
+                  int first, int past, int shared, uint32_t tile, uint32_t width) {
     group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
     row0 = b.first_row(first);
-    const int64_t all = first < past ? b.first_row(past) - row0 : 0;
-    n = (int)(all < 0 ? 0 : all < g.max_rows ? all : g.max_rows);
+    const int64_t many = first < past ? b.first_row(past) - row0 : 0;
+    all = (int)(many < 0 ? 0 : many);
+    n = all < g.max_rows ? all : g.max_rows;
     len = end = shared;
     rows = (uint32_t)n * group;
     r0 = tile * width;
     p_lo = 0;
     p_hi = -1;
   }
-  // The positions of its tokens: lane l has those of tokens l and 64 + l from its first on.
-  __device__ void positions(const KvBatch &b, int64_t first, int64_t past, uint32_t width,
-                            int (&at)[2]) {
-    const int lane = threadIdx.x & 63;
-    const int t0 = (int)(r0 / group), t1 = (int)((min(r0 + width, rows) - 1) / group);
-    p_lo = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = t0 + 64 * i + lane;
-      at[i] = -1;
-      if (t <= t1) {
-        at[i] = b.position(row0 + t, first, past);
-        p_lo = min(p_lo, at[i]);
-        p_hi = max(p_hi, at[i]);
-      }
-    }
-    p_lo = lanes_min(p_lo);
-    p_hi = -lanes_min(-p_hi);
+  // The positions of its tokens: lane l has those of tokens l and 64 + l from its first on
+  // (a tile of no more than 64 rows has no others).
+  struct Guesses {
+    KvBatch::Guess low, high;
+  };
+  template <int WIDTH>
+  __device__ Guesses guess(const KvBatch &b, int first, int past) const {
+    const int last = (int)((min(r0 + WIDTH, rows) - 1) / group);
+    Guesses g;
+    g.high = g.low = b.guess(row0 + min(token(0), last), first, past, row0, all);
+    if (WIDTH > 64) g.high = b.guess(row0 + min(token(1), last), first, past, row0, all);
+    return g;
   }
+  template <int WIDTH>
+  __device__ void positions(const KvBatch &b, int first, int past, const Guesses &g,
+                            int (&at)[2]) {
+    const int last = (int)((min(r0 + WIDTH, rows) - 1) / group);
+    at[0] = token(0) <= last ? b.position(g.low, row0 + token(0), first, past) : -1;
+    at[1] = -1;
+    if (WIDTH > 64 && token(1) <= last) at[1] = b.position(g.high, row0 + token(1), first, past);
+    p_hi = -lanes_min(-max(at[0], at[1]));
+    p_lo = lanes_min(min(token(0) <= last ? at[0] : p_hi,
+                         WIDTH > 64 && token(1) <= last ? at[1] : p_hi));
+  }
+  __device__ int token(int i) const { return (int)(r0 / group) + 64 * i + (int)(threadIdx.x & 63); }
   // Position of the tile's token t (counted from its first) from what the lanes hold.
   __device__ static int position(const int (&at)[2], int t) {
     const int x = __shfl(at[0], t & 63), y = __shfl(at[1], t & 63);
@@ -261,15 +270,15 @@ struct Place {
   const KvBatch &b;
   const KvAttention &a;
   const S &scope;
-  int64_t seq;
+  int seq;
   uint32_t index, width;
   int split, max_splits, split_steps;
-  int64_t first, past;  // sequences of the group
+  int first, past;  // sequences of the group
   int shared;
   const int32_t *table;
 
   __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const S &scope,
-                   int64_t seq, uint32_t index, uint32_t width, int split, int max_splits,
+                   int seq, uint32_t index, uint32_t width, int split, int max_splits,
                    int split_steps)
       : c(c), b(b), a(a), scope(scope), seq(seq), index(index), width(width), split(split),
         max_splits(max_splits), split_steps(split_steps), first(seq), past(seq + 1), shared(0) {
@@ -280,7 +289,7 @@ struct Place {
     }
     if constexpr (S::kSuffix) shared = scope.g.shared_of(b, seq);
     // (a group without sequences has no rows: nothing of its table is read)
-    table = b.table + (first < b.seqs ? first : 0) * b.table_stride;
+    table = b.table + (int64_t)(first < b.seqs ? first : 0) * b.table_stride;
   }
   __device__ static uint32_t count(const KvBatch &b, const S &scope) {
     if constexpr (S::kPrefix) return (uint32_t)scope.g.groups;
@@ -463,7 +472,8 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   Tile tl = place.tile();
   if (tl.empty()) return;
   int at[2];
-  if (S::kPrefix && !place.ahead()) tl.positions(b, place.first, place.past, 16, at);
+  if (S::kPrefix && !place.ahead())
+    tl.positions<16>(b, place.first, place.past, tl.guess<16>(b, place.first, place.past), at);
   const Steps<32> steps = place.steps(tl, tl.p_hi);
   const Range range = place.range(steps);
   if (!S::kPrefix && split >= range.splits) return;
@@ -525,15 +535,17 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   };
 
   look(first);
-  if (S::kPrefix && place.ahead()) tl.positions(b, place.first, place.past, 16, at);
-  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
-  const int pos = mine ? row_pos : -1;
+  Tile::Guesses guesses = {};
+  if (S::kPrefix && place.ahead()) guesses = tl.guess<16>(b, place.first, place.past);
 
   bf16x8 q[KS];
   const uint16_t *qp = a.q + (tl.row0 + tok) * a.q_stride + (int64_t)qh * D + g * 16;
 #pragma unroll
   for (int j = 0; j < KS; ++j)
     q[j] = *reinterpret_cast<const bf16x8 *>(qp + 64 * (j / 2) + 8 * (j % 2));
+  if (S::kPrefix && place.ahead()) tl.positions<16>(b, place.first, place.past, guesses, at);
+  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
+  const int pos = mine ? row_pos : -1;
 
   const Visible<S> visible{a.window, a.sinks, place.shared};
   float m = -INFINITY, l = 0.0f;
@@ -730,7 +742,9 @@ struct TileLds {
   static constexpr int kCopies = 2 * (D / 64) + 2;      // per wave and stage
 };
 
-template <int D, int G, class S>
+// H = 2: tiles of 64 rows, two waves for each 32 of them, which take the first and the
+// last 32 keys of every step and meet in LDS at the end.
+template <int D, int G, int H, class S>
 __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch &b,
                                  const KvAttention &a, uint32_t tiles, int max_splits,
                                  int split_steps, const S &scope, uint32_t w,
@@ -743,6 +757,8 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   // the team of four waves: team g takes steps g, g + G, .. with its own LDS
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kTileWaves));
   uint8_t *const lds = all_lds + team * L::kBytes;
+  static_assert(G == 1 || H == 1, "one way to share a tile");
+  const int half = H == 2 ? wave >> 1 : 0;
   const int col = lane & 31, h = lane >> 5;
   // heads first: a kv head's workgroups run on the same dies and find its keys
   // in their cache; the last rows, which see most, start first
@@ -753,15 +769,16 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   const uint32_t seqs = Place<S, kTileKeys>::count(b, scope);
   const uint32_t seq = w % seqs;
   const uint32_t tile = tiles - 1 - w / seqs;
-  const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows, split, max_splits, split_steps);
+  const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows / H, split, max_splits, split_steps);
   if (!place.there()) return;
   Tile tl = place.tile();
   if (tl.empty()) return;
   int at[2];
-  if (S::kPrefix && !place.ahead()) tl.positions(b, place.first, place.past, kTileRows, at);
+  if (S::kPrefix && !place.ahead())
+    tl.positions<kTileRows / H>(b, place.first, place.past, tl.guess<kTileRows / H>(b, place.first, place.past), at);
   // the wave's rows: with two teams, waves w and w + 4 share a SIMD and hold
   // different halves of the tile
-  const int sub = team == 0 ? wave : wave ^ 2;
+  const int sub = H == 2 ? wave & 1 : team == 0 ? wave : wave ^ 2;
   uint32_t r0 = tl.r0 + 32 * sub;
   int p_hi = tl.p_hi;
   if (!S::kPrefix && !S::kSuffix && G > 1 && a.window == 0 && max_splits == 1) {
@@ -824,7 +841,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
         if (s + 16 < n) page_next = pages_of(s + 16);
       }
       const int at = 4 * (s & 15);
-      holes |= ((uint32_t)(hole_mask >> at) & 15u) << 8;
+      holes |= ((uint32_t)(hole_mask >> at) & 15u) << (4 * (kStages - 1));
       const int page = __builtin_amdgcn_readlane(page_l, at + wave);
       const int t0 = steps.key(begin + s * G) + 16 * wave;
       const uint64_t off = (uint64_t)(uint32_t)(page < 0 ? 0 : page) * page_bytes +
@@ -846,18 +863,8 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     to = to == lds0 + (kStages - 1) * L::kStage ? lds0 : to + L::kStage;
   };
 
-  if constexpr (S::kPrefix) {
-    // the copies go out before the positions come in
-    issue(0);
-    holes >>= 4;
-    issue(1);
-    holes >>= 4;
-    if (place.ahead()) tl.positions(b, place.first, place.past, kTileRows, at);
-    const int row_pos = Tile::position(at, tok - (int)(tl.r0 / tl.group));
-    pos = mine ? row_pos : -1;
-    w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
-    w_hi = -lanes_min(-pos);
-  }
+  Tile::Guesses guesses = {};
+  if (S::kPrefix && place.ahead()) guesses = tl.guess<kTileRows / H>(b, place.first, place.past);
 
   // the element of key piece 2m + h that step 2m + e of the first product takes
   // is value 32m + 16h + 8e
@@ -884,11 +891,11 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     const int ve_l = kv_scale_exponent(reinterpret_cast<const float *>(st + L::kS)[lane & 7]);
     const float kc_l = __uint_as_float((uint32_t)(127 + ve_l) << 23) * cscale;
     const float vi_l = __uint_as_float((uint32_t)(127 - ve_l) << 23);
-    f32x16 s[2];
+    f32x16 s[2 / H];  // of the wave's keys, 32 at a time
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2 / H; ++u) {
       s[u] = f32x16{};
-      const uint8_t *kr = st + (32 * u + col) * D;
+      const uint8_t *kr = st + (32 * (u + half) + col) * D;
 #pragma unroll
       for (int j = 0; j < CH / 2; ++j) {
         const uint4 k = *reinterpret_cast<const uint4 *>(
@@ -901,18 +908,19 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     float mx = kLeast;
     // blocks whose values need kLift (lanes 4 to 7 hold the values' exponents)
     uint32_t high = (uint32_t)__ballot(ve_l > kLiftExp) & 0xF0u;
-    if (hole != 0 || !visible.all(key0, kTileKeys, w_lo, w_hi)) {
+    if (hole != 0 || !visible.all(key0 + 32 * half, kTileKeys / H, w_lo, w_hi)) {
       uint64_t bits = visible.bits(key0, pos);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (hole >> k & 1) bits &= ~(0xFFFFull << (16 * k));
+      if (H == 2) bits = bits >> (32 * half) & 0xFFFFFFFFu;
       mx = bits != 0 ? kLeast : -INFINITY;
       high &= ~(hole << 4);  // a hole's exponent is another block's
       bits >>= 4 * h;
       // bit 8a + e for element 4a + e of s[u]
       const uint32_t see[2] = {(uint32_t)bits, (uint32_t)(bits >> 32)};
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2 / H; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint32_t on = (uint32_t)__builtin_amdgcn_sbfe((int)see[u], 8 * (i >> 2) + (i & 3), 1);
@@ -935,19 +943,19 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
               make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
         }
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4 / H; ++k) {
           uint32_t va[DT], vc[DT];
-          values(vt, k, va, vc);
+          values(vt, k + 2 * half, va, vc);
           const uint32_t w = (k >> 1 ? see[1] : see[0]) >> (16 * (k & 1));
           spread_nan<DT>(va, vc, (w & 15u) | (w >> 4 & 0xF0u), o);
         }
         vt = clean;
       }
     }
-    float kc[4];
+    float kc[4 / H];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      kc[k] = lane_float(kc_l, k);
+    for (int k = 0; k < 4 / H; ++k) {
+      kc[k] = lane_float(kc_l, k + 2 * half);
       const auto at = [&](int i) { return s[k >> 1][8 * (k & 1) + i]; };
       float t = max3(at(0), at(1), at(2));
       t = max3(t, at(3), at(4));
@@ -969,13 +977,13 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     // (a row that has seen nothing yet has only -inf here, which stays 0)
     const float base = m == -INFINITY ? 0.0f : m;
     union {
-      bf16x8 v[4];
-      bf16x2 e[16];
+      bf16x8 v[4 / H];
+      bf16x2 e[16 / H];
     } p;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float mk = (float)__builtin_amdgcn_readlane(ve_l, 4 + k) - base;
-      const float inv = lane_float(vi_l, 4 + k);
+    for (int k = 0; k < 4 / H; ++k) {
+      const float mk = (float)__builtin_amdgcn_readlane(ve_l, 4 + k + 2 * half) - base;
+      const float inv = lane_float(vi_l, 4 + k + 2 * half);
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const float x = exp2_fast(fmaf(s[k >> 1][8 * (k & 1) + i], kc[k], mk));
@@ -987,31 +995,37 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4 / H; ++k) {
       uint32_t va[DT], vc[DT];
-      values(vt, k, va, vc);
+      values(vt, k + 2 * half, va, vc);
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] = mfma(widen(va[t], vc[t]), p.v[k], o[t]);
     }
   };
 
-  if constexpr (!S::kPrefix) {
-    issue(0);
-    holes >>= 4;
-    issue(1);
-    holes >>= 4;  // steps 0 and 1 now have the two low places
+  for (int s = 0; s < kStages - 1; ++s) {
+    issue(s);
+    holes >>= 4;  // the steps issued now have the low places
+  }
+  if constexpr (S::kPrefix) {
+    // (all of these loads are in flight together)
+    if (place.ahead()) tl.positions<kTileRows / H>(b, place.first, place.past, guesses, at);
+    const int row_pos = Tile::position(at, tok - (int)(tl.r0 / tl.group));
+    pos = mine ? row_pos : -1;
+    w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
+    w_hi = -lanes_min(-pos);
   }
   // q is waited for here: a wait inside the loop would be for the copies too
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) asm volatile("" : "+v"(q[j]));
   const uint8_t *st = lds;
   for (int s = 0; s < turns; ++s) {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(L::kCopies) : "memory");
-    issue(s + 2);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kStages - 2) * L::kCopies) : "memory");
+    issue(s + kStages - 1);
     const int key0 = steps.key(begin + s * G);
     // rows of this wave that see nothing here leave it out
-    const bool none = s >= n || key0 > w_hi || (a.window > 0 && key0 + kTileKeys - 1 <= w_lo - a.window &&
-                                      key0 >= a.sinks);
+    const int k_lo = key0 + 32 * half, k_hi = k_lo + kTileKeys / H - 1;
+    const bool none = s >= n || k_lo > w_hi || (a.window > 0 && k_hi <= w_lo - a.window && k_lo >= a.sinks);
     if (!none) compute(st, key0, holes & 15u);
     st = st == lds + (kStages - 1) * L::kStage ? lds : st + L::kStage;
     holes >>= 4;
@@ -1021,10 +1035,11 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
 
   float sum = l[0] + l[1];
   sum += __shfl_xor(sum, 32);
-  if (G > 1) {  // the teams' sums, through LDS that nobody copies into any more
+  if (G > 1 || H > 1) {  // the teams' or halves' sums, through LDS that nobody copies into any more
+    const int second = G > 1 ? team : half;
     __syncthreads();
     float *of = reinterpret_cast<float *>(all_lds) + sub * (64 * (16 * DT + 2)) + lane;
-    if (team == 1) {
+    if (second == 1) {
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -1033,7 +1048,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
       of[64 * (16 * DT + 1)] = sum;
     }
     __syncthreads();
-    if (team == 1) return;
+    if (second == 1) return;
     const float m1 = of[64 * 16 * DT], sum1 = of[64 * (16 * DT + 1)];
     const float top = fmaxf(m, m1);
     const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
@@ -1104,7 +1119,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
                                                                       int max_splits,
                                                                       int split_steps) {
   __shared__ __align__(16) uint8_t lds[G * TileLds<D>::kBytes];
-  tile_part<D, G, Whole>(c, layer, b, a, tiles, max_splits, split_steps, Whole{}, blockIdx.x, lds);
+  tile_part<D, G, 1, Whole>(c, layer, b, a, tiles, max_splits, split_steps, Whole{}, blockIdx.x, lds);
 }
 
 // Shared first tokens: the first workgroups take the prefixes of all groups, the others
@@ -1115,28 +1130,47 @@ struct SharedPlan {
   int prefix_splits, prefix_steps, splits, steps;
 };
 
-template <int D, bool FEW_PREFIX, bool FEW>
-__global__ __launch_bounds__(256, 2) void shared_kernel(KvCache c, int64_t layer, KvBatch b,
-                                                        KvAttention a, Shared scope, SharedPlan p) {
-  using Decode = DecodeLds<D, 4>;
-  constexpr int kTile = TileLds<D>::kBytes;
-  static_assert(kTile >= (int)sizeof(Decode), "the larger of the two");
-  __shared__ __align__(16) uint8_t lds[FEW_PREFIX && FEW ? sizeof(Decode) : kTile];
-  if (blockIdx.x < p.prefix_grid) {
-    const Prefix s{scope};
-    if constexpr (FEW_PREFIX)
-      decode_part(c, layer, b, a, p.prefix_tiles, p.prefix_splits, p.prefix_steps, s, blockIdx.x,
-                  *reinterpret_cast<Decode *>(lds));
-    else
-      tile_part<D, 1, Prefix>(c, layer, b, a, p.prefix_tiles, p.prefix_splits, p.prefix_steps, s, blockIdx.x, lds);
-    return;
-  }
-  const Suffix s{scope};
-  if constexpr (FEW)
-    decode_part(c, layer, b, a, p.tiles, p.splits, p.steps, s, blockIdx.x - p.prefix_grid,
-                *reinterpret_cast<Decode *>(lds));
+// A workgroup's tile of ROWS rows: 16 or 64.
+template <int D, int ROWS, class S>
+__device__ inline void shared_part(const KvCache &c, int64_t layer, const KvBatch &b,
+                                   const KvAttention &a, uint32_t tiles, int splits, int steps,
+                                   const S &scope, uint32_t w, uint8_t *lds) {
+  if constexpr (ROWS == 16)
+    decode_part(c, layer, b, a, tiles, splits, steps, scope, w,
+                *reinterpret_cast<DecodeLds<D, 4> *>(lds));
   else
-    tile_part<D, 1, Suffix>(c, layer, b, a, p.tiles, p.splits, p.steps, s, blockIdx.x - p.prefix_grid, lds);
+    tile_part<D, 1, 2, S>(c, layer, b, a, tiles, splits, steps, scope, w, lds);
+}
+
+// What the kernel is called with.  It reads them where it takes its way, not at its
+// start, as it would by itself: both ways' arguments together pass the scalar registers.
+struct SharedArgs {
+  KvCache c;
+  int64_t layer;
+  KvBatch b;
+  KvAttention a;
+  Shared scope;
+  SharedPlan p;
+};
+
+template <int D, int PREFIX_ROWS, int ROWS>
+__global__ __launch_bounds__(256, 2) void shared_kernel(SharedArgs) {
+  constexpr int kTile = TileLds<D>::kBytes, kDecode = sizeof(DecodeLds<D, 4>);
+  static_assert(kTile >= kDecode, "the larger of the two");
+  __shared__ __align__(16) uint8_t lds[PREFIX_ROWS == 16 && ROWS == 16 ? kDecode : kTile];
+  const SharedArgs *args = (const SharedArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+  const uint32_t prefix_grid = args->p.prefix_grid;
+  if (blockIdx.x < prefix_grid) {
+    asm volatile("; a prefix");
+    const SharedArgs x = *args;
+    shared_part<D, PREFIX_ROWS>(x.c, x.layer, x.b, x.a, x.p.prefix_tiles, x.p.prefix_splits,
+                                x.p.prefix_steps, Prefix{x.scope}, blockIdx.x, lds);
+  } else {
+    asm volatile("; a suffix");
+    const SharedArgs x = *args;
+    shared_part<D, ROWS>(x.c, x.layer, x.b, x.a, x.p.tiles, x.p.splits, x.p.steps, Suffix{x.scope},
+                         blockIdx.x - prefix_grid, lds);
+  }
 }
 
 // Joins the parts of rows: 256 threads take four neighbouring values each of
@@ -1225,7 +1259,7 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   int n, len, end;
   b.sequence(seq, row0, n, len, end);
   const int rows = n < b.max_rows ? n : b.max_rows;
-  int64_t first;
+  int first;
   int shared = scope.g.shared_of(b, seq, &first);
   if (first_row_head >= (uint32_t)rows * a.heads) return;
   const uint32_t i = first_row_head + t / j.turns;
@@ -1360,12 +1394,28 @@ Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int si
 }
 
 // A group's rows may stand anywhere, so that some may see any of the shared keys.
-Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads) {
-  const int64_t longest = std::min<int64_t>(g.max_shared, b.max_len);
-  Plan p = plan_for(c, g.groups, g.max_rows, heads, [&](int keys, int) {
-    return std::max<int64_t>((longest + keys - 1) / keys, 1);
-  });
+Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window,
+                 bool few) {
+  const int64_t longest = std::min<int64_t>(g.max_shared, b.max_len), group = heads / c.kv_heads;
+  const int64_t rows = g.max_rows * group;
+  Plan p;
   p.teams = 1;
+  p.few = rows <= kFewRows && few;
+  p.width = p.few ? 16 : 64;
+  p.keys = p.few ? 32 : kTileKeys;
+  p.tiles = (rows + p.width - 1) / p.width;
+  p.items = g.groups * p.tiles * c.kv_heads;
+  const int64_t steps = std::max<int64_t>((longest + p.keys - 1) / p.keys, 1);
+  int64_t per;
+  if (p.few) {
+    per = kMinSteps;
+  } else {
+    const int64_t seen = window > 0 ? std::min<int64_t>(steps, window / p.keys + 2) : steps;
+    per = std::min<int64_t>(std::max<int64_t>(p.items * seen / (device_cu_count() / 2), 2), 16);
+  }
+  per = std::max<int64_t>(per, (steps + kMaxSplits - 1) / kMaxSplits);
+  p.splits = (steps + per - 1) / per;
+  p.split_steps = (int)((steps + p.splits - 1) / p.splits);  // as many each
   return p;
 }
 
@@ -1377,13 +1427,37 @@ Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
   if (g.max_shared < b.max_len) guess.max_len = b.max_len - g.max_shared;
   Plan p = make_plan(c, guess, heads, window, sinks);
   p.teams = 1;
+  if (p.few) return p;
+  const int64_t group = heads / c.kv_heads, rows = b.max_rows * group;
+  p.width = 64;
+  p.tiles = (rows + p.width - 1) / p.width;
+  p.items = b.seqs * p.tiles * c.kv_heads;
+  const int64_t steps =
+      most_steps(p.keys, guess, (int)((p.width - 1 + group) / group + 1), window, sinks);
+  int64_t per = std::min<int64_t>(std::max<int64_t>(p.items * steps / (device_cu_count() / 2), 4), 32);
+  per = std::max<int64_t>(per, (steps + kMaxSplits - 1) / kMaxSplits);
+  p.splits = (steps + per - 1) / per;
+  p.split_steps = (int)((steps + p.splits - 1) / p.splits);
   return p;
 }
 
-// Whether a call takes the shared keys apart: not where there are none, nor where a
-// sequence's own rows fill the tiles that its keys are read for.
-bool apart(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads) {
-  return g.max_shared > 0 && b.max_len > 0 && (int64_t)b.max_rows * (heads / c.kv_heads) <= kTileRows;
+// Whether a call takes the shared keys apart.  Without that, every tile of 16 rows reads
+// its own sequence's keys, which for shared ones mostly means from the caches, at some
+// 9.5 TB/s, and a short call is one launch of 6.5 us where taking them apart costs two, 12
+// us.  So it has to save reading kSavedBytes (a guess from the bounds): 53 sequences
+// over up to 397 shared tokens, 8 heads of 64 (22 MB): 8.2 us as one, 14.3 apart; 28 over
+// 776 (22 MB) 16.9 and 17.7; 8 over 14449, 4 heads of 128 (104 MB) 21.3 and 20.1; 32 over
+// a window of 2048, 8 heads of 128 (130 MB) 30.2 and 24.2.  A sequence whose own rows fill
+// a tile of 128 reads its keys once for them as it is.
+constexpr int64_t kSavedBytes = int64_t(64) << 20;
+
+bool apart(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window) {
+  const int64_t group = heads / c.kv_heads, own = b.max_rows * group;
+  if (own > kTileRows) return false;
+  int64_t keys = std::min(g.max_shared, b.max_len);
+  if (window > 0) keys = std::min<int64_t>(keys, window);
+  const int64_t tiles = b.seqs * ((own + 15) / 16) - g.groups * ((g.max_rows * group + 63) / 64);
+  return tiles > 0 && keys > kSavedBytes / (tiles * c.kv_heads * 2 * c.head_dim);
 }
 
 int64_t plan_floats(const Plan &p, int head_dim) {
@@ -1409,8 +1483,9 @@ size_t kv_attention_workspace_bytes(const KvCache &c, const KvBatch &b, int head
 
 size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, const KvGroups &g,
                                            int heads, int window, int sinks) {
-  if (!apart(c, b, g, heads)) return kv_attention_workspace_bytes(c, b, heads, window, sinks);
-  const Plan p = prefix_plan(c, b, g, heads), own = suffix_plan(c, b, g, heads, window, sinks);
+  if (!apart(c, b, g, heads, window)) return kv_attention_workspace_bytes(c, b, heads, window, sinks);
+  const Plan own = suffix_plan(c, b, g, heads, window, sinks);
+  const Plan p = prefix_plan(c, b, g, heads, window, own.few);
   return (size_t)((p.splits + own.splits) * b.rows * heads * (c.head_dim + 2)) * sizeof(float);
 }
 
@@ -1465,9 +1540,9 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
 
 hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvBatch &b,
                                       const KvGroups &g, const KvAttention &a, hipStream_t s) {
-  if (!apart(c, b, g, a.heads)) return launch_kv_attention(c, layer, b, a, s);
-  const Plan p = prefix_plan(c, b, g, a.heads);
+  if (!apart(c, b, g, a.heads, a.window)) return launch_kv_attention(c, layer, b, a, s);
   const Plan own = suffix_plan(c, b, g, a.heads, a.window, a.sinks);
+  const Plan p = prefix_plan(c, b, g, a.heads, a.window, own.few);
   const int turns = join_turns(c.head_dim, p.splits + own.splits);
   const int at_once = 256 / (c.head_dim / 4) / turns;
   const int64_t per_seq = ((int64_t)b.max_rows * a.heads + at_once - 1) / at_once;
@@ -1479,19 +1554,16 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
                         (int)p.splits, p.split_steps, (int)own.splits, own.split_steps};
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits + own.items * own.splits)), dim3(256),
-                       0, s, c, layer, b, a, scope, plan);
+                       0, s, SharedArgs{c, layer, b, a, scope, plan});
   };
-  if (c.head_dim == 128) {
-    if (p.few && own.few) go(shared_kernel<128, true, true>);
-    else if (own.few) go(shared_kernel<128, false, true>);
-    else if (p.few) go(shared_kernel<128, true, false>);
-    else go(shared_kernel<128, false, false>);
-  } else {
-    if (p.few && own.few) go(shared_kernel<64, true, true>);
-    else if (own.few) go(shared_kernel<64, false, true>);
-    else if (p.few) go(shared_kernel<64, true, false>);
-    else go(shared_kernel<64, false, false>);
-  }
+  auto pick = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (!own.few) go(shared_kernel<D, 64, 64>);
+    else if (p.few) go(shared_kernel<D, 16, 16>);
+    else go(shared_kernel<D, 64, 16>);
+  };
+  if (c.head_dim == 128) pick(std::integral_constant<int, 128>());
+  else pick(std::integral_constant<int, 64>());
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const SharedJoin j{p.split_steps * p.keys, own.width, own.keys, (int)own.splits, own.split_steps, turns,

@@ -66,24 +66,29 @@ struct KvBatch {
     const int64_t r = row_start ? row_start[s] : s;
     return r < 0 ? 0 : r > rows ? rows : r;
   }
-  // The position of a row of one of the sequences first .. past - 1 (of the last of them
-  // whose rows begin no later).
-  __device__ int position(int64_t row, int64_t first, int64_t past) const {
-    int64_t s = row;
-    if (row_start) {
-      // as many rows each, most often: then this is the one
-      const int64_t r0 = row_start[first], n = row_start[past] - r0;
-      int64_t guess = n > 0 && row >= r0 ? first + (row - r0) * (past - first) / n : first;
-      guess = guess < past ? guess : past - 1;
-      const int from = row_start[guess], to = row_start[guess + 1], len = kv_len[guess];
-      if (from <= row && row < to && from >= 0 && to <= rows)
-        return (len < 0 ? 0 : len > held_len ? held_len : len) - (to - from) + (int)(row - from);
-      s = first;
-      int64_t hi = past;
-      while (hi - s > 1) {
-        const int64_t mid = (s + hi) / 2;
-        (row_start[mid] <= row ? s : hi) = mid;
-      }
+  // The position of a row of one of the sequences first .. past - 1, in two steps, so that
+  // the loads of the first one are in flight beside others.  It takes the sequence
+  // that the row is in if all have as many rows; the second one searches if that is not it.
+  struct Guess {
+    int seq, from, to, len;
+  };
+  __device__ Guess guess(int64_t row, int first, int past, int64_t row0, int rows_of_all) const {
+    Guess g;
+    const int n = past - first, each = rows_of_all > n ? rows_of_all / n : 1;
+    g.seq = first + (int)(row - row0) / each;
+    g.seq = g.seq < past ? g.seq : past - 1;
+    g.from = row_start ? row_start[g.seq] : g.seq;
+    g.to = row_start ? row_start[g.seq + 1] : g.seq + 1;
+    g.len = kv_len[g.seq];
+    return g;
+  }
+  __device__ int position(const Guess &g, int64_t row, int first, int past) const {
+    if (g.from <= row && row < g.to && g.from >= 0 && g.to <= rows)
+      return (g.len < 0 ? 0 : g.len > held_len ? held_len : g.len) - (g.to - g.from) + (int)(row - g.from);
+    int s = first, hi = past;
+    while (row_start && hi - s > 1) {
+      const int mid = s + (hi - s) / 2;
+      (row_start[mid] <= row ? s : hi) = mid;
     }
     int64_t row0;
     int n, len, end;
@@ -94,16 +99,15 @@ struct KvBatch {
 
 // Sequences first[g] .. first[g + 1] - 1 begin with the same shared_len[g] tokens.
 struct KvGroups {
-  int64_t groups;
-  int max_rows, max_shared;
+  int groups, max_rows, max_shared;
   const int32_t *first, *shared_len;  // first null: one group of all
 
-  __device__ int64_t first_of(const KvBatch &b, int64_t g) const {
-    const int64_t s = first ? first[g] : g == 0 ? 0 : b.seqs;
-    return s < 0 ? 0 : s > b.seqs ? b.seqs : s;
+  __device__ int first_of(const KvBatch &b, int g) const {
+    const int n = (int)b.seqs, s = first ? first[g] : g == 0 ? 0 : n;
+    return s < 0 ? 0 : s > n ? n : s;
   }
   // Tokens that group g shares and the table has a place for.
-  __device__ int shared(const KvBatch &b, int64_t g) const { return held(b, shared_len[g]); }
+  __device__ int shared(const KvBatch &b, int g) const { return held(b, shared_len[g]); }
   __device__ int held(const KvBatch &b, int n) const {
     const int most = max_shared < b.max_len ? max_shared : b.max_len;
     return n < 0 ? 0 : n > most ? most : n;
@@ -111,20 +115,19 @@ struct KvGroups {
   // The same of the group that sequence s is in (0: in none), and that group's first
   // sequence.  The whole wave looks, a lane at every 64th place, so that up to 64 groups
   // take one trip to memory.
-  __device__ int shared_of(const KvBatch &b, int64_t s, int64_t *first_seq = nullptr) const {
+  __device__ int shared_of(const KvBatch &b, int s, int *first_seq = nullptr) const {
     const int lane = threadIdx.x & 63;
-    int64_t lo = 0, hi = groups;
+    int lo = 0, hi = groups;
     for (;;) {
-      const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
-      const int64_t here = at < hi ? at : hi - 1;
-      const int from = (int)first_of(b, here), to = (int)first_of(b, here + 1), len = shared_len[here];
+      const int step = (hi - lo + 63) / 64, at = lo + lane * step;
+      const int here = at < hi ? at : hi - 1;
+      const int from = first_of(b, here), to = first_of(b, here + 1), len = shared_len[here];
       const int in = __popcll(__ballot(at < hi && from <= s));  // ascending: the first ones
       if (in == 0) return 0;
       const int l = in - 1;
       if (step == 1) {
-        const int f = __builtin_amdgcn_readlane(from, l), past = __builtin_amdgcn_readlane(to, l);
-        if (first_seq) *first_seq = f;
-        return s < past ? held(b, __builtin_amdgcn_readlane(len, l)) : 0;
+        if (first_seq) *first_seq = __builtin_amdgcn_readlane(from, l);
+        return s < __builtin_amdgcn_readlane(to, l) ? held(b, __builtin_amdgcn_readlane(len, l)) : 0;
       }
       lo += l * step;
       hi = lo + step < hi ? lo + step : hi;

@@ -18,11 +18,23 @@ def side():
     return Side()
 
 
+SAVED = 64 << 20  # bytes of cache that taking the shared tokens apart has to save, by the bounds
+
+
 class Shared(Case):
     """A Case whose sequences first[g] .. first[g + 1] - 1 have the same first
-    prefix[g] tokens: whole pages shared, a page in part copied."""
+    prefix[g] tokens: whole pages shared, a page in part copied.  Its table has room for so
+    many tokens that the shared ones are taken apart (`apart`: whether they can be)."""
 
-    def __init__(self, side, seed, dim, page, heads, kv_heads, kv_len, count, first, prefix, **kw):
+    def __init__(self, side, seed, dim, page, heads, kv_heads, kv_len, count, first, prefix, roomy=True,
+                 **kw):
+        group = heads // kv_heads
+        of = [sum(count[a:b]) for a, b in zip(first, first[1:])]
+        self.most = max([1] + of)
+        tiles = len(kv_len) * -(-max(count) * group // 16) - len(prefix) * -(-self.most * group // 64)
+        self.tiles, self.apart = tiles, roomy and tiles > 0 and max(count) * group <= 128
+        if self.apart:
+            kw = {"stride_more": SAVED // (tiles * kv_heads * 2 * dim) // page + 2} | kw
         super().__init__(side, seed, dim, page, heads, kv_heads, kv_len, count, **kw)
         self.first, self.prefix = first, prefix
         for g, n in enumerate(prefix):
@@ -43,20 +55,31 @@ class Shared(Case):
             max_rows=None, max_prefix=None, groups=None, **kw):
         side, t = self.side, self.side.torch
         d = d or device_cache(side, self.c)
-        b = device_batch(side, self.table, self.kv_len, self.start, **kw)
-        g = groups or side.nf4.KVGroups(i32(side, self.prefix), i32(side, self.first), max_rows=max_rows,
+        b = device_batch(side, self.table, self.kv_len, self.start,
+                         **(({"max_len": 1 << 30} if self.apart else {}) | kw))
+        g = groups or side.nf4.KVGroups(i32(side, self.prefix), i32(side, self.first),
+                                        max_rows=self.most if max_rows is None else max_rows,
                                         max_prefix=max_prefix)
         q = rows_dev(side, self.q, pad, False)
         rows = self.q.shape[0]
         out = t.full((rows + 2, self.heads * self.dim), 7.0, dtype=t.bfloat16, device="cuda")
         z = t.full((rows + 2, self.heads), 7.0, dtype=t.float32, device="cuda") if lse else None
         n = side.nf4.nf4_kv_attention_shared_workspace_bytes(d, b, g, self.heads, window, sinks)
+        # a slot of every part holds the sums of all rows and heads
+        slots, rest = divmod(n, rows * self.heads * (self.dim + 2) * 4)
+        alone = side.nf4.nf4_kv_attention_workspace_bytes(d, b, self.heads, window, sinks)
+        seen = min(self.table.shape[1] * self.page, window or 1 << 30)
+        if max_prefix is None and max_rows is None and "max_len" not in kw:
+            if self.apart and seen > SAVED // (self.tiles * self.kv_heads * 2 * self.dim):
+                assert rest == 0 and slots >= 2 and n != alone, "not taken apart"
+            else:
+                assert n == alone
         ws = t.full((max(n, 16) + 64,), 0xAB, dtype=t.uint8, device="cuda")
         stream = stream or side.stream
         stream.wait_stream(t.cuda.current_stream())
         say(f"[kv shared] dim={self.dim} page={self.page} heads={self.heads}/{self.kv_heads} "
             f"len={self.kv_len[:6]} rows={self.count[:6]} first={self.first} prefix={self.prefix} "
-            f"window={window} sinks={sinks} ws={n}")
+            f"window={window} sinks={sinks} apart={self.apart} ws={n}")
         side.nf4.nf4_kv_attention_shared(d, self.c.layers - 1, b, g, q, q.stride(0), self.heads, scale,
                                          window, sinks, out, z, ws, n, stream=stream)
         stream.synchronize()
@@ -131,6 +154,29 @@ def test_windows(side, window, sinks, count):
         Shared(side, 7, dim, page, heads, kv_heads, [260, 230, 400, 201], count, [0, 3, 4], [200, 64]).run(window, sinks)
 
 
+@pytest.fixture(scope="module")
+def long(side):
+    """33 sequences of some 1400 tokens, all but one behind 1200 shared ones."""
+    rng = np.random.default_rng(20)
+    kv_len = [int(x) for x in 1201 + rng.integers(0, 250, 33)]
+    count = [1, 3, 2] * 11
+    c = Shared(side, 20, 128, 64, 16, 8, kv_len, count, [0, 32], [1200], stride_more=0)
+    assert c.apart and SAVED // (c.tiles * 8 * 2 * 128) < 1100
+    return c
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 31, 0), (1100, 0), (1103, 1), (1150, 64), (1200, 70), (1201, 1300),
+                                          (1300, 1199), (1400, 5)])
+def test_windows_over_what_is_taken_apart(long, window, sinks):
+    """Windows long enough for it, that begin in what is shared or before it."""
+    long.run(window, sinks)
+
+
+def test_bounds_as_they_are_taken_apart(long):
+    """The parts of a call whose bounds are the lengths themselves."""
+    long.run(max_len=max(long.kv_len), max_prefix=1200)
+
+
 @pytest.mark.parametrize("count", [1, 9])
 def test_long_prefix_in_parts(side, count):
     """A prefix over many parts, groups of few rows of a head and of many."""
@@ -195,12 +241,20 @@ def test_large_scores(side):
     c.run(scale=0.5)
 
 
-def test_many_rows_of_a_sequence(side):
-    """Sequences whose own rows fill tiles go as without sharing."""
-    c = Shared(side, 14, 64, 16, 4, 1, [140, 170], [33, 70], [0, 2], [100])
+@pytest.mark.parametrize("count,first,prefix", [([33, 70], [0, 2], [100]), ([1, 1], [0, 2], [100]),
+                                                ([1, 1], [0, 1, 2], [100, 100])])
+def test_as_without_sharing(side, count, first, prefix):
+    """Sequences whose own rows fill tiles, and what saves little, go as without sharing."""
+    c = Shared(side, 14, 64, 16, 4, 1, [140, 170], count, first, prefix, roomy=count[0] > 1)
     a, za = c.run()
     b, zb = Case.run(c)
-    assert np.array_equal(a, b) and np.array_equal(za, zb)
+    assert not c.apart and np.array_equal(a, b) and np.array_equal(za, zb)
+
+
+@pytest.mark.parametrize("dim,page,heads,kv_heads", SHAPES)
+def test_small_calls(side, dim, page, heads, kv_heads):
+    for kv_len, first, prefix in BATCHES:
+        Shared(side, 1, dim, page, heads, kv_heads, kv_len, [1] * len(kv_len), first, prefix, roomy=False).run()
 
 
 def test_bounds_of_the_host(side):
@@ -235,14 +289,16 @@ def test_in_a_replayed_graph(side):
     """Lengths, tables and what is shared change between replays; two graphs share a
     workspace, one after the other."""
     t, nf4 = side.torch, side.nf4
-    c = Shared(side, 18, 128, 16, 8, 2, [150, 140, 160, 155], [1] * 4, [0, 4], [128])
+    c = Shared(side, 18, 128, 16, 8, 2, [150, 140, 160, 155], [1] * 4, [0, 4], [128],
+               stride_more=SAVED // (2 * 2 * 2 * 128) // 16 + 2)
     d = device_cache(side, c.c)
     lens, table = i32(side, c.kv_len), i32(side, c.table)
     first, prefix = i32(side, [0, 4, 4]), i32(side, [128, 0])
-    b = nf4.KVBatch(lens, table, max_len=c.table.shape[1] * 16)
+    b = nf4.KVBatch(lens, table)
     g = nf4.KVGroups(prefix, first)
     q = side.to_dev(c.q).bfloat16()
     n = nf4.nf4_kv_attention_shared_workspace_bytes(d, b, g, 8)
+    assert n != nf4.nf4_kv_attention_workspace_bytes(d, b, 8), "not taken apart"
     ws = t.full((n,), 0xFF, dtype=t.uint8, device="cuda")
     outs = [t.zeros(4, 8 * 128, dtype=t.bfloat16, device="cuda") for _ in range(3)]
     zs = [t.zeros(4, 8, device="cuda") for _ in range(3)]
