@@ -194,7 +194,7 @@ struct Tile {
   int all;                   // rows of a group, max_rows or no
   uint32_t rows, r0, group;  // rows of a kv head of one sequence stay under 2^31
   int n, len, end, p_lo, p_hi;
-  __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, int64_t seq,
+  __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, const KvBatch::Raw &seq,
                   uint32_t tile, uint32_t width) {
     group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
     b.sequence(seq, row0, n, len, end);
@@ -274,6 +274,7 @@ struct Place {
   uint32_t index, width;
   int split, max_splits, split_steps;
   int first, past;  // sequences of the group
+  KvBatch::Raw raw;
   int shared;
   const int32_t *table;
 
@@ -287,6 +288,7 @@ struct Place {
       past = scope.g.first_of(b, seq + 1);
       shared = scope.g.shared(b, seq);
     }
+    if constexpr (!S::kPrefix) raw = b.raw(seq);
     if constexpr (S::kSuffix) shared = scope.g.shared_of(b, seq);
     // (a group without sequences has no rows: nothing of its table is read)
     table = b.table + (int64_t)(first < b.seqs ? first : 0) * b.table_stride;
@@ -297,30 +299,22 @@ struct Place {
   }
   __device__ Tile tile() const {
     if constexpr (S::kPrefix) return Tile(c, b, a, scope.g, first, past, shared, index, width);
-    return Tile(c, b, a, seq, index, width);
+    return Tile(c, b, a, raw, index, width);
   }
   // Without a window what a prefix's rows see does not wait for their positions.
   __device__ bool ahead() const { return S::kPrefix && a.window == 0; }
   __device__ Steps<N> steps(const Tile &tl, int p_hi) const {
-    if constexpr (S::kPrefix) {
-      const int low = split * split_steps;
-      const int64_t keys = (int64_t)(low + split_steps) * N;
-      const int last = (int)(keys < shared ? keys : shared) - 1;
-      return Steps<N>(low, tl.p_lo, ahead() ? last : min(p_hi, last), a.window, a.sinks);
-    }
+    if constexpr (S::kPrefix)
+      return Steps<N>(0, tl.p_lo, ahead() ? shared - 1 : min(p_hi, shared - 1), a.window, a.sinks);
     return Steps<N>(shared / N, tl.p_lo, tl.last_key(p_hi), a.window, a.sinks);
   }
-  // Whether the part is one of the prefix's, which are those of its length: each leaves
-  // its sums, also where its rows see none of its keys.
-  __device__ bool there() const {
-    if constexpr (S::kPrefix) return split < KvGroups::parts(shared, split_steps * N);
-    return true;
-  }
+  // The steps that the host has planned for a part, or more where it has made room for
+  // fewer parts; a prefix has all of its parts, some of them with nothing to do.
   __device__ Range range(const Steps<N> &s) const {
-    if constexpr (S::kPrefix) return Range{0, s.count, 1};
-    const int per = S::kSuffix ? suffix_steps(s.count, split_steps, max_splits) : split_steps;
+    const int per = S::kPrefix ? (s.count + max_splits - 1) / max_splits
+                    : S::kSuffix ? suffix_steps(s.count, split_steps, max_splits) : split_steps;
     return Range{split * per, min(s.count, (split + 1) * per),
-                 s.count <= per ? 1 : (s.count + per - 1) / per};
+                 S::kPrefix ? max_splits : s.count <= per ? 1 : (s.count + per - 1) / per};
   }
   // Whether a range holds all keys that the rows see.
   __device__ bool whole(const Range &r) const {
@@ -330,7 +324,6 @@ struct Place {
     if constexpr (S::kSuffix) return scope.prefix_slots + split;
     return split;
   }
-  // Steps of a suffix's parts: more where the host has made no room for as many parts.
   __device__ static int suffix_steps(int count, int split_steps, int max_splits) {
     return max(split_steps, (count + max_splits - 1) / max_splits);
   }
@@ -464,11 +457,11 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   // without a window, where the first page ids stand does not depend on the
   // lengths: they are read beside them (as far as the longest one may reach)
   int page_ahead = -1;
-  if (!S::kSuffix && a.window == 0) {
+  if (!S::kPrefix && !S::kSuffix && a.window == 0) {
     const int64_t t0 = (int64_t)(split * split_steps + wave + (lane >> 1) * W) * 32 + 16 * (lane & 1);
     page_ahead = table[min(t0, (int64_t)max(b.max_len - 1, 0)) >> c.page_shift];
   }
-  if (!place.there()) return;
+  if (S::kPrefix && place.shared == 0) return;
   Tile tl = place.tile();
   if (tl.empty()) return;
   int at[2];
@@ -476,7 +469,7 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
     tl.positions<16>(b, place.first, place.past, tl.guess<16>(b, place.first, place.past), at);
   const Steps<32> steps = place.steps(tl, tl.p_hi);
   const Range range = place.range(steps);
-  if (!S::kPrefix && split >= range.splits) return;
+  if (split >= range.splits) return;
   const int end = range.end;
 
   const bool mine = tl.r0 + col < tl.rows;
@@ -503,7 +496,8 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
     const int t0 = steps.key(i) + 16 * (lane & 1);
     page_l = -1;
     if (i < end && t0 < tl.end)
-      page_l = !S::kSuffix && a.window == 0 && i0 == first ? page_ahead : table[t0 >> c.page_shift];
+      page_l = !S::kPrefix && !S::kSuffix && a.window == 0 && i0 == first ? page_ahead
+                                                                          : table[t0 >> c.page_shift];
     if (page_l >= c.pages) page_l = -1;
     const int64_t block = block_of(page_l < 0 ? 0 : page_l, t0);
     kc_l = c.ks[block];
@@ -770,7 +764,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   const uint32_t seq = w % seqs;
   const uint32_t tile = tiles - 1 - w / seqs;
   const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows / H, split, max_splits, split_steps);
-  if (!place.there()) return;
+  if (S::kPrefix && place.shared == 0) return;
   Tile tl = place.tile();
   if (tl.empty()) return;
   int at[2];
@@ -791,7 +785,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   }
   const Steps<kTileKeys> steps = place.steps(tl, p_hi);
   const Range range = place.range(steps);
-  if (!S::kPrefix && split >= range.splits) return;
+  if (split >= range.splits) return;
   const int begin = range.begin + team, mine_steps = range.end - range.begin;
   const int turns = (mine_steps + G - 1) / G;
   const int n = (mine_steps - team + G - 1) / G;
@@ -1208,7 +1202,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
     }
   };
   load(turn);
-  const Tile tl(c, b, a, w / tiles, w % tiles, width);
+  const Tile tl(c, b, a, b.raw(w / tiles), w % tiles, width);
   if (tl.empty()) return;
   const Steps<N> steps(0, tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
   if (steps.count <= split_steps) return;  // written already
@@ -1239,7 +1233,6 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
 // suffix: a workgroup takes `256 / (D / 4) / turns` rows and heads of a sequence, which lie
 // side by side in every slot.
 struct SharedJoin {
-  int prefix_keys;                   // of a part
   int width, keys, splits, steps;    // the suffix's plan
   int turns;
   uint32_t per_seq;                  // workgroups of a sequence
@@ -1255,12 +1248,13 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   const int64_t seq = blockIdx.x / j.per_seq;
   const uint32_t first_row_head = (blockIdx.x % j.per_seq) * (256 / QUADS / j.turns);
   const uint32_t group_heads = (uint32_t)a.heads / (uint32_t)c.kv_heads;
+  const KvBatch::Raw raw = b.raw(seq);
+  int first = 0;
+  const int shared = scope.g.shared_of(b, seq, &first);
   int64_t row0;
   int n, len, end;
-  b.sequence(seq, row0, n, len, end);
+  b.sequence(raw, row0, n, len, end);
   const int rows = n < b.max_rows ? n : b.max_rows;
-  int first;
-  int shared = scope.g.shared_of(b, seq, &first);
   if (first_row_head >= (uint32_t)rows * a.heads) return;
   const uint32_t i = first_row_head + t / j.turns;
   const bool on = i < (uint32_t)rows * a.heads;
@@ -1273,7 +1267,7 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   const int per = Place<Suffix, N>::suffix_steps(steps.count, j.steps, j.splits);
   const int splits = steps.count <= per ? 1 : (steps.count + per - 1) / per;
   const bool written = shared == 0 && splits == 1;
-  int shared_parts = KvGroups::parts(shared, j.prefix_keys);
+  int shared_parts = shared > 0 ? scope.prefix_slots : 0;
   if (scope.g.max_rows < b.rows && shared > 0) {
     const int64_t at = row0 + tok - b.first_row(first);  // the row among its group's
     if (at < 0 || at >= scope.g.max_rows) shared_parts = 0;
@@ -1288,7 +1282,7 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       int s = min(s0 + u * j.turns, parts - 1);
-      s = s < shared_parts ? s : s - shared_parts + scope.prefix_slots;
+      if (s >= shared_parts) s += scope.prefix_slots - shared_parts;
       ml[u] = *scope.ml(a.ws, s, row_head, D);
       y[u] = *reinterpret_cast<const f32x4 *>(scope.sums(a.ws, s, row_head, D) + d);
     }
@@ -1393,32 +1387,6 @@ Plan make_plan(const KvCache &c, const KvBatch &b, int heads, int window, int si
   });
 }
 
-// A group's rows may stand anywhere, so that some may see any of the shared keys.
-Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window,
-                 bool few) {
-  const int64_t longest = std::min<int64_t>(g.max_shared, b.max_len), group = heads / c.kv_heads;
-  const int64_t rows = g.max_rows * group;
-  Plan p;
-  p.teams = 1;
-  p.few = rows <= kFewRows && few;
-  p.width = p.few ? 16 : 64;
-  p.keys = p.few ? 32 : kTileKeys;
-  p.tiles = (rows + p.width - 1) / p.width;
-  p.items = g.groups * p.tiles * c.kv_heads;
-  const int64_t steps = std::max<int64_t>((longest + p.keys - 1) / p.keys, 1);
-  int64_t per;
-  if (p.few) {
-    per = kMinSteps;
-  } else {
-    const int64_t seen = window > 0 ? std::min<int64_t>(steps, window / p.keys + 2) : steps;
-    per = std::min<int64_t>(std::max<int64_t>(p.items * seen / (device_cu_count() / 2), 2), 16);
-  }
-  per = std::max<int64_t>(per, (steps + kMaxSplits - 1) / kMaxSplits);
-  p.splits = (steps + per - 1) / per;
-  p.split_steps = (int)((steps + p.splits - 1) / p.splits);  // as many each
-  return p;
-}
-
 // The suffixes are as long as the bounds say if the longest sequence has the longest
 // prefix.  That is a guess: where it is not so, a part has more steps.
 Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window,
@@ -1438,6 +1406,47 @@ Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
   per = std::max<int64_t>(per, (steps + kMaxSplits - 1) / kMaxSplits);
   p.splits = (steps + per - 1) / per;
   p.split_steps = (int)((steps + p.splits - 1) / p.splits);
+  return p;
+}
+
+// The prefixes' part of a shared launch, beside suffixes by the plan `own`.  Tiles of 64
+// rows, or 16 where a group has no more than kFewRows; how many steps a workgroup takes
+// goes by the steps of all tiles: some 200 workgroups, of 2 to 12 steps (microseconds of
+// the whole call: 9 sequences of two rows over 4888 tokens, 32 heads over 8 of 128, in parts
+// of 6 steps 18.8, of 12 20.9; 62 over 4561, three groups, of 12 23.0, of 8 24.6; 8 over
+// 14449, of 4 18.7, of 7 19.7), and more, up to 24, where that is more workgroups than
+// run at a time, the suffixes' among them (23 sequences of three rows over 10477, two
+// groups, of 16 34.9, of 12 41.5; 64 of up to 2000 tokens past 4096, which are as many as
+// run at a time by themselves, of 24 46.0, of 16 48.2, of 12 53.9).
+// Tiles of 16 rows: 43 over 9451, 5 groups, 16 heads over 8 of 64, in parts of 24
+// steps 23.6, of 16 26.6.  A window's rows may stand anywhere: as many steps as it is long
+// are counted.
+Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window,
+                 const Plan &own) {
+  const int64_t longest = std::min<int64_t>(g.max_shared, b.max_len), group = heads / c.kv_heads;
+  const int64_t rows = g.max_rows * group, cus = device_cu_count();
+  Plan p;
+  p.teams = 1;
+  p.few = rows <= kFewRows && own.few;
+  p.width = p.few ? 16 : 64;
+  p.keys = p.few ? 32 : kTileKeys;
+  p.tiles = (rows + p.width - 1) / p.width;
+  p.items = g.groups * p.tiles * c.kv_heads;
+  int64_t steps = std::max<int64_t>((longest + p.keys - 1) / p.keys, 1);
+  if (window > 0) steps = std::min<int64_t>(steps, window / p.keys + 2);
+  int64_t per;
+  if (p.few) {
+    per = std::max<int64_t>(p.items * steps / (3 * cus), kMinSteps);
+  } else {
+    per = std::min<int64_t>(std::max<int64_t>(p.items * steps * 5 / (4 * cus), 2), 12);
+    const int64_t slots = (c.head_dim == 128 ? 2 : 3) * cus;
+    const int64_t taken = own.items * own.splits * std::min<int64_t>(own.split_steps * own.keys, 1024) / 1024;
+    const int64_t room = std::max<int64_t>((slots - taken) / p.items, 1);
+    per = std::max<int64_t>(per, std::min<int64_t>((steps + room - 1) / room, 24));
+  }
+  per = std::max<int64_t>(per, (steps + kMaxSplits - 1) / kMaxSplits);
+  p.splits = (steps + per - 1) / per;
+  p.split_steps = 0;  // as many as that leaves for each
   return p;
 }
 
@@ -1485,7 +1494,7 @@ size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, c
                                            int heads, int window, int sinks) {
   if (!apart(c, b, g, heads, window)) return kv_attention_workspace_bytes(c, b, heads, window, sinks);
   const Plan own = suffix_plan(c, b, g, heads, window, sinks);
-  const Plan p = prefix_plan(c, b, g, heads, window, own.few);
+  const Plan p = prefix_plan(c, b, g, heads, window, own);
   return (size_t)((p.splits + own.splits) * b.rows * heads * (c.head_dim + 2)) * sizeof(float);
 }
 
@@ -1542,7 +1551,7 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
                                       const KvGroups &g, const KvAttention &a, hipStream_t s) {
   if (!apart(c, b, g, a.heads, a.window)) return launch_kv_attention(c, layer, b, a, s);
   const Plan own = suffix_plan(c, b, g, a.heads, a.window, a.sinks);
-  const Plan p = prefix_plan(c, b, g, a.heads, a.window, own.few);
+  const Plan p = prefix_plan(c, b, g, a.heads, a.window, own);
   const int turns = join_turns(c.head_dim, p.splits + own.splits);
   const int at_once = 256 / (c.head_dim / 4) / turns;
   const int64_t per_seq = ((int64_t)b.max_rows * a.heads + at_once - 1) / at_once;
@@ -1566,7 +1575,7 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
   else pick(std::integral_constant<int, 64>());
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const SharedJoin j{p.split_steps * p.keys, own.width, own.keys, (int)own.splits, own.split_steps, turns,
+  const SharedJoin j{own.width, own.keys, (int)own.splits, own.split_steps, turns,
                      (uint32_t)per_seq};
   auto join = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(b.seqs * per_seq)), dim3(256), 0, s, c, b, a, scope, j);

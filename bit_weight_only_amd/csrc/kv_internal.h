@@ -48,17 +48,28 @@ struct KvBatch {
   // rows' positions come from the former: a sequence that has outgrown its
   // table must not find its new tokens on the places of older ones.
   __device__ void sequence(int64_t s, int64_t &row0, int &n, int &len, int &end) const {
-    int64_t r0 = s, r1 = s + 1;
+    sequence(raw(s), row0, n, len, end);
+  }
+  // The same in two steps, so that other loads can go out beside these.
+  struct Raw {
+    int64_t r0, r1;
+    int len;
+  };
+  __device__ Raw raw(int64_t s) const {
+    Raw x{s, s + 1, 0};
     if (row_start) {
-      r0 = row_start[s];
-      r1 = row_start[s + 1];
+      x.r0 = row_start[s];
+      x.r1 = row_start[s + 1];
     }
-    r0 = r0 < 0 ? 0 : r0 > rows ? rows : r0;
-    r1 = r1 < r0 ? r0 : r1 > rows ? rows : r1;
+    x.len = kv_len[s];
+    return x;
+  }
+  __device__ void sequence(const Raw &x, int64_t &row0, int &n, int &len, int &end) const {
+    const int64_t r0 = x.r0 < 0 ? 0 : x.r0 > rows ? rows : x.r0;
+    const int64_t r1 = x.r1 < r0 ? r0 : x.r1 > rows ? rows : x.r1;
     row0 = r0;
     n = (int)(r1 - r0);
-    const int l = kv_len[s];
-    len = l < 0 ? 0 : l > held_len ? held_len : l;
+    len = x.len < 0 ? 0 : x.len > held_len ? held_len : x.len;
     end = len > max_len ? max_len : len;
   }
   // The first row of sequence s, s = seqs: past the last one's.
@@ -132,10 +143,6 @@ struct KvGroups {
       lo += l * step;
       hi = lo + step < hi ? lo + step : hi;
     }
-  }
-  // Parts of so many shared tokens.
-  __device__ static int parts(int shared, int keys) {
-    return (int)(((int64_t)shared + keys - 1) / keys);
   }
 };
 
