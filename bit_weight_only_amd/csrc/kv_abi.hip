@@ -96,7 +96,7 @@ bool type_ok(int type) { return type == NF4_KV_BF16 || type == NF4_KV_F32; }
 
 // Rows of `width` values: a stride that holds them, in whole 16-byte pieces.
 nf4_status check_rows(const void *p, int64_t stride, int64_t width, nf4_kv_type type) {
-  if (stride < width || stride > kMaxElems) return NF4_ERR_SHAPE;
+  if (stride < width || stride > nf4::kKvWidestRows) return NF4_ERR_SHAPE;
   return aligned(p, 16) && stride % (type == NF4_KV_F32 ? 4 : 8) == 0 ? NF4_OK : NF4_ERR_ALIGN;
 }
 

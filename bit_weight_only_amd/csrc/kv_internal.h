@@ -17,6 +17,10 @@ constexpr int kKvExpMax = 100;  // attention folds them into exponents of its we
 // key, and positions less windows stay in 32 bits.
 constexpr int kKvLongest = (1 << 30) + (1 << 23);
 
+// Values that the rows of queries, keys and the like may lie apart: offsets inside a block
+// of 16 rows stay in 31 bits.
+constexpr int64_t kKvWidestRows = int64_t(1) << 24;
+
 // The cache as a kernel sees it.  A page of one layer is kv_heads runs of
 // page_tokens * D bytes (k and v alike) and kv_heads * page_tokens / 16 scales.
 struct KvCache {

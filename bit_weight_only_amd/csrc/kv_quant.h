@@ -9,9 +9,11 @@ namespace nf4 {
 
 constexpr int kWave = 64;
 
+// The largest of LANES neighbouring lanes' values.
+template <int LANES = 64>
 __device__ inline uint32_t wave_max(uint32_t v) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
+  for (int o = LANES / 2; o > 0; o >>= 1) {
     const uint32_t w = __shfl_xor(v, o);
     v = w > v ? w : v;
   }
@@ -66,18 +68,22 @@ struct Block {
 // 1: values) into its page: val holds them as above, top is the lane's largest
 // finite magnitude of them, as bits.  Tokens before `first` are the sequence's
 // own earlier ones; what lies past `last` is left as it is.
-template <bool F32, int D, int VEC, int PER>
+// SUB: as many heads are taken by as many parts of the wave (head < 0: none).
+template <bool F32, int D, int SUB = 1, int VEC, int PER>
 __device__ inline void store_block(const KvCache &c, int64_t layer, int64_t page, int head, int kv,
                                    int t0, int first, int last, const float (&val)[PER][4][VEC],
                                    uint32_t top) {
   constexpr int CHUNKS = Block<F32, D>::CHUNKS, TASKS = Block<F32, D>::TASKS;
-  const int lane = threadIdx.x & 63;
+  constexpr int LANES = 64 / SUB;
+  const int lane = threadIdx.x & (LANES - 1);
+  const uint32_t top_of_all = wave_max<LANES>(top);
+  if (SUB > 1 && head < 0) return;
   const int64_t block = ((layer * c.pages + page) * c.kv_heads + head) *
                             (int64_t)(1 << (c.page_shift - 4)) +
                         ((t0 & (c.page_tokens() - 1)) >> 4);
   uint8_t *codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
   float *scale = (kv ? c.vs : c.ks) + block;
-  int e = block_exponent(wave_max(top));
+  int e = block_exponent(top_of_all);
   const bool has_old = first > t0;
   int e_old = e;
   if (has_old) {
