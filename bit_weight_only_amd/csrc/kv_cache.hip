@@ -79,7 +79,8 @@ __global__ __launch_bounds__(256) void append_kernel(KvCache c, int64_t layer, K
   }
   // the rows are on their way before the page is known
   if (page < 0 || page >= c.pages) return;
-  store_block<F32, D>(c, layer, page, head, kv, t0, first, last, val, top);
+  const OldBlock<F32, D> was(c, layer, page, head, kv, t0, first, last);
+  store_block<F32, D>(was, head, kv, t0, first, last, val, top);
 }
 
 struct ReadRows {

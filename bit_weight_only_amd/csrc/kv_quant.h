@@ -9,15 +9,20 @@ namespace nf4 {
 
 constexpr int kWave = 64;
 
-// The largest of LANES neighbouring lanes' values.
+// The largest of 64 (or each 32) neighbouring lanes' values.
 template <int LANES = 64>
 __device__ inline uint32_t wave_max(uint32_t v) {
+  auto max_with = [&](uint32_t w) { v = w > v ? w : v; };
+  max_with(__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  max_with(__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  max_with(__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));  // 7 - lane of 8
+  max_with(__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // 15 - lane of 16
+  uint32_t row[4];
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    const uint32_t w = __shfl_xor(v, o);
-    v = w > v ? w : v;
-  }
-  return v;
+  for (int i = 0; i < 4; ++i) row[i] = (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * i);
+  const uint32_t low = row[0] > row[1] ? row[0] : row[1], high = row[2] > row[3] ? row[2] : row[3];
+  if (LANES == 32) return threadIdx.x & 32 ? high : low;
+  return low > high ? low : high;
 }
 
 // Exponent of the block scale for the bits of a magnitude a = m 2^E, 1 <= m <
@@ -64,30 +69,60 @@ struct Block {
   static constexpr int PER = (TASKS + kWave - 1) / kWave;
 };
 
+// What a block that is new in part held before, read ahead of the new values' way
+// through the kernel: its scale, and the values' quads that have old or no tokens in them.
+template <bool F32, int D, int SUB = 1>
+struct OldBlock {
+  using B = Block<F32, D>;
+  uint8_t *codes;
+  float *scale;
+  float old_scale;
+  uint32_t had[B::PER][B::VEC];
+
+  // The block that starts at t0 of keys (kv 0) or values (1), of which the tokens first ..
+  // last - 1 are new.  SUB: as many heads are taken by as many parts of the wave.
+  __device__ OldBlock(const KvCache &c, int64_t layer, int64_t page, int head, int kv, int t0,
+                      int first, int last) {
+    const int lane = threadIdx.x & (64 / SUB - 1);
+    const int64_t block = ((layer * c.pages + page) * c.kv_heads + head) *
+                              (int64_t)(1 << (c.page_shift - 4)) +
+                          ((t0 & (c.page_tokens() - 1)) >> 4);
+    codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
+    scale = (kv ? c.vs : c.ks) + block;
+    old_scale = 0.0f;
+    if (head < 0) return;
+    if (first > t0) old_scale = *scale;
+#pragma unroll
+    for (int i = 0; i < B::PER; ++i) {
+      const int task = lane + i * kWave, quad = task / B::CHUNKS, piece = task % B::CHUNKS;
+      const int q0 = t0 + 4 * quad;
+      if (kv && task < B::TASKS && q0 < last && (q0 < first || q0 + 4 > last))
+        __builtin_memcpy(had[i], __builtin_assume_aligned(codes + (quad * D + piece * B::VEC) * 4, 16),
+                         sizeof(had[i]));
+    }
+  }
+};
+
 // Writes the tokens first .. last - 1 of the block that starts at t0 (kv 0: keys,
 // 1: values) into its page: val holds them as above, top is the lane's largest
 // finite magnitude of them, as bits.  Tokens before `first` are the sequence's
-// own earlier ones; what lies past `last` is left as it is.
-// SUB: as many heads are taken by as many parts of the wave (head < 0: none).
+// own earlier ones; what lies past `last` is left as it is.  head < 0: a part of the wave
+// that has none.
 template <bool F32, int D, int SUB = 1, int VEC, int PER>
-__device__ inline void store_block(const KvCache &c, int64_t layer, int64_t page, int head, int kv,
-                                   int t0, int first, int last, const float (&val)[PER][4][VEC],
+__device__ inline void store_block(const OldBlock<F32, D, SUB> &was, int head, int kv, int t0,
+                                   int first, int last, const float (&val)[PER][4][VEC],
                                    uint32_t top) {
   constexpr int CHUNKS = Block<F32, D>::CHUNKS, TASKS = Block<F32, D>::TASKS;
   constexpr int LANES = 64 / SUB;
   const int lane = threadIdx.x & (LANES - 1);
   const uint32_t top_of_all = wave_max<LANES>(top);
   if (SUB > 1 && head < 0) return;
-  const int64_t block = ((layer * c.pages + page) * c.kv_heads + head) *
-                            (int64_t)(1 << (c.page_shift - 4)) +
-                        ((t0 & (c.page_tokens() - 1)) >> 4);
-  uint8_t *codes = (kv ? c.v : c.k) + block * (kKvBlock * D);
-  float *scale = (kv ? c.vs : c.ks) + block;
+  uint8_t *const codes = was.codes;
   int e = block_exponent(top_of_all);
   const bool has_old = first > t0;
   int e_old = e;
   if (has_old) {
-    e_old = scale_exponent(*scale);
+    e_old = scale_exponent(was.old_scale);
     e = e_old > e ? e_old : e;
   }
   const float inv = pow2(-e), factor = pow2(e_old - e < -126 ? -126 : e_old - e);
@@ -123,20 +158,22 @@ __device__ inline void store_block(const KvCache &c, int64_t layer, int64_t page
         if (q0 + t < first || q0 + t >= last) keep |= 0xFFu << (8 * t);
         if (q0 + t < first) old |= 0xFFu << (8 * t);
       }
+      uint32_t out[VEC];
 #pragma unroll
       for (int d = 0; d < VEC; ++d) {
         uint32_t y = codes4(val[i][0][d] * inv, val[i][1][d] * inv, val[i][2][d] * inv,
                             val[i][3][d] * inv);
         if (keep) {
-          const uint32_t had = p[d];
+          const uint32_t had = was.had[i][d];
           const uint32_t kept = grew ? (rescale4(had, factor) & old) | (had & ~old) : had;
           y = (y & ~keep) | (kept & keep);
         }
-        p[d] = y;
+        out[d] = y;
       }
+      __builtin_memcpy(__builtin_assume_aligned(p, 16), out, sizeof(out));
     }
   }
-  if (lane == 0) *scale = pow2(e);
+  if (lane == 0) *was.scale = pow2(e);
 }
 
 }  // namespace nf4

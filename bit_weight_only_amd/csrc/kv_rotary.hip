@@ -53,15 +53,17 @@ __device__ inline Turn turned(uint32_t u, double gain) {
   return Turn{(quarter + 1) & 2 ? -co : co, quarter & 2 ? -si : si};
 }
 
-// What the workgroup's waves share: cosines and sines of 16 tokens, (cos, sin) in fp32
-// and, where something is worked out in 64 bits (T double), what that leaves of them, and
-// for each wave some rows of heads, where lanes find the other values of their pairs.
-// Rows are padded by 16 bytes, so that neighbouring ones start at other banks.
+// What the workgroup's waves share: what turns the values of 16 tokens, in fp32 and, where
+// something is worked out in 64 bits (T double), what that leaves of it, and for each
+// wave some rows of heads, where lanes find the other values of their pairs.  In pairs entry
+// i holds (cos, sin) of pair i; in halves every value has its own, (cos, -sin) for the
+// first one of a pair and (cos, sin) for the second.  Rows are padded by 16 bytes,
+// so that neighbouring ones start at other banks.
 template <class T, int D>
 struct alignas(16) TurnLds {
   static constexpr bool LOW = sizeof(T) == 8;
-  float2 cs[kKvBlock][D / 2 + 2];
-  float2 low[LOW ? kKvBlock : 1][D / 2 + 2];
+  float2 cs[kKvBlock][D + 2];
+  float2 low[LOW ? kKvBlock : 1][D + 2];
   // 64 lanes of up to 8 values, and what a read of a last row may pass it by
   T rows[kThreads / 64][512 / D * (D + 16 / sizeof(T)) + 8];
 };
@@ -71,9 +73,9 @@ constexpr int kRow = D + 16 / (int)sizeof(T);
 
 // The table for tokens r of 16, lo <= r < hi, at the positions `position(r)`.  A thread
 // has one pair in all of its turns.
-template <class T, int D, class Position>
-__device__ inline void fill_table(TurnLds<T, D> &lds, const KvRotary &rot, uint64_t turns, int lo,
-                                  int hi, Position position) {
+template <class T, int D, class Lds, class Position>
+__device__ inline void fill_table(Lds &lds, const KvRotary &rot, uint64_t turns, int lo, int hi,
+                                  Position position) {
   constexpr int PAIRS = D / 2;
   const int p = threadIdx.x % PAIRS;
   if (2 * p >= rot.dims) return;
@@ -81,9 +83,13 @@ __device__ inline void fill_table(TurnLds<T, D> &lds, const KvRotary &rot, uint6
     if (r < lo) continue;
     const Turn t = turned((uint32_t)(((uint64_t)position(r) * turns) >> 32), rot.gain);
     const float2 cs = make_float2((float)t.c, (float)t.s);
-    lds.cs[r][p] = cs;
-    if constexpr (TurnLds<T, D>::LOW)
-      lds.low[r][p] = make_float2((float)(t.c - cs.x), (float)(t.s - cs.y));
+    const float2 low = make_float2((float)(t.c - cs.x), (float)(t.s - cs.y));
+    auto set = [&](int at, float sign) {
+      lds.cs[r][at] = make_float2(cs.x, sign * cs.y);
+      if constexpr (sizeof(T) == 8) lds.low[r][at] = make_float2(low.x, sign * low.y);
+    };
+    set(p, rot.pairs ? 1.0f : -1.0f);
+    if (!rot.pairs) set(p + rot.dims / 2, 1.0f);
   }
 }
 
@@ -153,13 +159,38 @@ __device__ inline void norm_row(const float (&w)[VEC], double eps, float (&v)[VE
   for (int e = 0; e < VEC; ++e) v[e] *= inv * w[e];
 }
 
-__device__ inline float turn_a(float a, float b, float2 cs, float2) { return fmaf(a, cs.x, -(b * cs.y)); }
-__device__ inline float turn_b(float a, float b, float2 cs, float2) { return fmaf(b, cs.x, a * cs.y); }
-__device__ inline double turn_a(double a, double b, float2 cs, float2 low) {
-  return fma(a, (double)cs.x + low.x, -(b * ((double)cs.y + low.y)));
+// What one lane's value is to the lane that holds the other half of its row, CHUNKS / 2 lanes
+// away from it.
+template <int CHUNKS>
+__device__ inline uint32_t across(uint32_t v) {
+  if constexpr (CHUNKS == 8) {  // lane ^ 4: 7 - lane of 8, then 3 - lane of 4
+    const int m = __builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);
+  } else if constexpr (CHUNKS == 16) {  // rotated by 8 in 16
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true);
+  } else {
+    // rows of 16 lanes: [0] has the even ones twice, [1] the odd ones
+    const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return threadIdx.x & 16 ? x[0] : x[1];
+  }
 }
-__device__ inline double turn_b(double a, double b, float2 cs, float2 low) {
-  return fma(b, (double)cs.x + low.x, a * ((double)cs.y + low.y));
+template <int CHUNKS>
+__device__ inline float across(float v) {
+  return __uint_as_float(across<CHUNKS>(__float_as_uint(v)));
+}
+template <int CHUNKS>
+__device__ inline double across(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)across<CHUNKS>((uint32_t)(u >> 32)) << 32 |
+                                        across<CHUNKS>((uint32_t)u));
+}
+
+// A value turned, by what the table holds for it and the other value of its pair.
+__device__ inline float turn(float x, float other, float2 cs, float2) {
+  return fmaf(x, cs.x, other * cs.y);
+}
+__device__ inline double turn(double x, double other, float2 cs, float2 low) {
+  return fma(x, (double)cs.x + low.x, other * ((double)cs.y + low.y));
 }
 
 // N values at p, which is aligned to `ALIGN` bytes.
@@ -183,52 +214,47 @@ __device__ inline void turn_row(const Lds &lds, T *row, const KvRotary &rot,
   const int e0 = piece * VEC;
   if (rot.dims > 0 && rot.pairs) {
     float2 cs[VEC / 2], low[VEC / 2] = {};
-    load_n<VEC * 4 < 16 ? 8 : 16>(cs, &lds.cs[r][piece * (VEC / 2)]);
-    if (LOW) load_n<VEC * 4 < 16 ? 8 : 16>(low, &lds.low[LOW ? r : 0][piece * (VEC / 2)]);
+    load_n<16>(cs, &lds.cs[r][piece * (VEC / 2)]);
+    if (LOW) load_n<16>(low, &lds.low[LOW ? r : 0][piece * (VEC / 2)]);
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
       const T a = x[2 * j], b = x[2 * j + 1];
       const bool on = e0 + 2 * j < rot.dims;
-      x[2 * j] = on ? turn_a(a, b, cs[j], low[j]) : a;
-      x[2 * j + 1] = on ? turn_b(a, b, cs[j], low[j]) : b;
+      x[2 * j] = on ? turn(a, b, make_float2(cs[j].x, -cs[j].y), make_float2(low[j].x, -low[j].y)) : a;
+      x[2 * j + 1] = on ? turn(b, a, cs[j], low[j]) : b;
     }
   } else if (rot.dims > 0) {
     const int half = rot.dims / 2;
-    __builtin_memcpy(__builtin_assume_aligned(row + e0, 16), x, sizeof(x));
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     T other[VEC];
-    float2 cs[VEC], low[VEC] = {};
-    if (half % VEC == 0) {  // the other values of a lane's pairs are one piece
-      const bool on = e0 < rot.dims, first = e0 < half;
-      const int p = first || !on ? e0 % (D / 2) : e0 - half;
-      load_n<16>(other, row + (!on ? e0 : first ? e0 + half : e0 - half));
-      load_n<16>(cs, &lds.cs[r][p]);
-      if (LOW) load_n<16>(low, &lds.low[LOW ? r : 0][p]);
+    if (rot.dims == D) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const T y = first ? turn_a(x[e], other[e], cs[e], low[e]) : turn_b(other[e], x[e], cs[e], low[e]);
-        x[e] = on ? y : x[e];
-      }
+      for (int e = 0; e < VEC; ++e) other[e] = across<D / VEC>(x[e]);
     } else {
-      // they start anywhere, and a lane may have first and second values of pairs: it reads
-      // the others of both kinds (of a kind that it has none of, anything of the row)
-      const int up = min(e0 + half, D - 1), down = e0 + VEC > half ? e0 - half : 0;
-      T below[VEC];
-      load_n<sizeof(T)>(other, row + up);
-      load_n<sizeof(T)>(below, row + down);
+      __builtin_memcpy(__builtin_assume_aligned(row + e0, 16), x, sizeof(x));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (half % VEC == 0) {  // the other values of a lane's pairs are one piece
+        load_n<16>(other, row + (e0 >= rot.dims ? e0 : e0 < half ? e0 + half : e0 - half));
+      } else {
+        // they start anywhere, and a lane may have first and second values of pairs: it reads
+        // the others of both kinds (of a kind that it has none of, anything of the row)
+        T below[VEC];
+        load_n<sizeof(T)>(other, row + min(e0 + half, D - 1));
+        load_n<sizeof(T)>(below, row + (e0 + VEC > half ? e0 - half : 0));
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int at = e0 + e;
-        const bool on = at < rot.dims, first = at < half;
-        const int p = !on ? 0 : first ? at : at - half;
-        const float2 t = lds.cs[r][p], l = LOW ? lds.low[LOW ? r : 0][p] : float2{};
-        const T y = first ? turn_a(x[e], other[e], t, l) : turn_b(below[e], x[e], t, l);
-        x[e] = on ? y : x[e];
+        for (int e = 0; e < VEC; ++e) other[e] = e0 + e < half ? other[e] : below[e];
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    float2 cs[VEC], low[VEC] = {};
+    load_n<16>(cs, &lds.cs[r][e0]);
+    if (LOW) load_n<16>(low, &lds.low[LOW ? r : 0][e0]);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const T y = turn(x[e], other[e], cs[e], low[e]);
+      x[e] = e0 + e < rot.dims ? y : x[e];
+    }
   }
 #pragma unroll
   for (int e = 0; e < VEC; ++e) v[e] = (float)x[e];
@@ -313,10 +339,12 @@ struct Heads : Block<F32, D> {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int r = 4 * quad(i) + t;
+        const bool mine = head >= 0 && r >= lo && r < hi;
+        if (!__any(mine)) continue;
         float val[B::VEC];
         values(i, t, val);
         turn<T>(lds, rot, w, norm, eps, i, t, val);
-        if (head >= 0 && r >= lo && r < hi) store_values<Y32>(dst + (uint32_t)(r * stride + at), val);
+        if (mine) store_values<Y32>(dst + (uint32_t)(r * stride + at), val);
       }
   }
 };
@@ -364,124 +392,157 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(KvRotary rot, RotateAr
   }
 }
 
-// What append_rotated_kernel is called with.  It reads them where it wants them, not at its
-// start, as it would by itself: all together pass the scalar registers.
+// What append_rotated_kernel is called with.  Its two ways read them where they begin, not
+// at the kernel's start, as it would by itself: all together pass the scalar registers.
 struct AppendArgs {
+  uint32_t blocks_per_seq;
+  int q_slices, q_per, kv_slices, kv_per;  // workgroups of a block, units of each
+  KvBatch b;
+  KvTurned a;
   KvCache c;
   int64_t layer;
-  KvBatch b;
   KvRotary rot;
-  KvTurned a;
-  uint32_t blocks_per_seq, slices;
-  int per;
 };
 
-// New tokens: a workgroup takes `per` units of one block of 16 positions of a sequence, a
-// wave one at a time.  A unit is SUB heads of queries, keys or values, in this order.
-template <bool F32, int D>
-__global__ __launch_bounds__(kThreads) void append_rotated_kernel(AppendArgs) {
-  using H = Heads<F32, D>;
-  constexpr int SUB = H::SUB, WAVES = kThreads / 64;
-  __shared__ TurnLds<double, D> lds;
-  const AppendArgs *args = (const AppendArgs *)__builtin_amdgcn_kernarg_segment_ptr();
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint64_t turns = args->rot.turns[threadIdx.x % (D / 2)];
-  const uint32_t slices = args->slices, blocks_per_seq = args->blocks_per_seq;
-  uint32_t w = blockIdx.x;
-  const int slice = w % slices;
-  w /= slices;
-  const int64_t seq = w / blocks_per_seq;
+// The rows of a workgroup: those of a sequence at the 16 positions of a block.
+struct NewRows {
+  int64_t row;      // of the block's first position, which may be an earlier sequence's
+  int t0, lo, hi;   // the block's first position; rows lo .. hi - 1 of the block are new
+  int kv_hi;        // those up to here have a place in the table
+  int none;         // rows that are no tokens, from row0 on, where the block is the first
   int64_t row0;
-  int n, len, end;
-  const int max_rows = args->b.max_rows, heads = args->a.heads, kv_heads = args->c.kv_heads;
-  args->b.sequence(seq, row0, n, len, end);
-  const int begin = len - n;                // position of row 0, may be negative
-  const int first = begin < 0 ? 0 : begin;  // first new token
-  const int past = begin + (n < max_rows ? n : max_rows);  // past the last row's position
-  const int last = past < end ? past : end;                // past the last token with a place
-  const int blk = first / kKvBlock + (int)(w % blocks_per_seq);
-  const int t0 = blk * kKvBlock;
-  const int q_units = (heads + SUB - 1) / SUB, kv_units = (kv_heads + SUB - 1) / SUB;
-  const int from = slice * args->per, to = min(q_units + 2 * kv_units, from + args->per);
-  const int q_to = min(to, q_units);
-  if (begin < 0 && w % blocks_per_seq == 0) {
-    // rows that are no tokens: zeros
-    const int none = min(-begin, min(n, max_rows));
-    const int h0 = from * SUB, pieces = (min(to * SUB, heads) - h0) * (D / 8);
-    for (int64_t i = threadIdx.x; pieces > 0 && i < (int64_t)none * pieces; i += kThreads)
-      reinterpret_cast<uint4 *>(args->a.q_out + ((row0 + i / pieces) * heads + h0) * D)[i % pieces] =
+  __device__ NewRows(const KvBatch &b, int64_t seq, uint32_t block) {
+    int n, len, end;
+    b.sequence(seq, row0, n, len, end);
+    const int begin = len - n;                // position of row 0, may be negative
+    const int first = begin < 0 ? 0 : begin;  // first new token
+    const int rows = n < b.max_rows ? n : b.max_rows;
+    const int past = begin + rows;            // past the last row's position
+    t0 = (first / kKvBlock + (int)block) * kKvBlock;
+    row = row0 + (t0 - begin);
+    lo = first > t0 ? first - t0 : 0;
+    hi = past - t0 < kKvBlock ? past - t0 : kKvBlock;
+    kv_hi = min(hi, min(past, end) - t0);
+    none = begin < 0 && block == 0 ? min(-begin, rows) : 0;
+  }
+};
+
+// Queries: a workgroup takes `q_per` units of one block, a wave one at a time, the next one's
+// values on their way.  A unit is SUB heads.
+template <bool F32, int D>
+__device__ inline void append_queries(const AppendArgs &x, int64_t seq, uint32_t block, int slice,
+                                      TurnLds<double, D> &lds) {
+  using H = Heads<F32, D>;
+  constexpr int WAVES = kThreads / 64;
+  const KvTurned a = x.a;  // all at once
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), heads = a.heads;
+  const uint64_t turns = x.rot.turns[threadIdx.x % (D / 2)];
+  const NewRows r(x.b, seq, block);
+  int first = (slice * x.q_per + wave) * H::SUB;
+  const int end = min(heads, (slice + 1) * x.q_per * H::SUB);
+  if (r.none > 0) {  // zeros
+    const int h0 = slice * x.q_per * H::SUB, pieces = (end - h0) * (D / 8);
+    for (int64_t i = threadIdx.x; pieces > 0 && i < (int64_t)r.none * pieces; i += kThreads)
+      reinterpret_cast<uint4 *>(a.q_out + ((r.row0 + i / pieces) * heads + h0) * D)[i % pieces] =
           make_uint4(0, 0, 0, 0);
   }
-  if (first >= past || t0 >= past) return;
-  int page = -1;
-  if (to > q_units && t0 < last)
-    page = args->b.table[seq * args->b.table_stride + (t0 >> args->c.page_shift)];
-  const int lo = first > t0 ? first - t0 : 0, hi = past - t0 < kKvBlock ? past - t0 : kKvBlock;
-  const int64_t row = row0 + (t0 - begin);  // of token t0, which may be an earlier sequence's
-  KvRotary rot;
-  rot.dims = args->rot.dims;
-  rot.pairs = args->rot.pairs;
-  rot.gain = args->rot.gain;
-  const double eps = args->a.eps;
-
-  const uint8_t *src = args->a.q + row * args->a.q_stride;
-  const uint32_t stride = (uint32_t)args->a.q_stride;
-  auto head = [&](int unit, int end, int heads) {
-    const int h = unit * SUB + H::sub();
-    return unit < end && h < heads ? h : -1;
-  };
+  if (r.lo >= r.hi) return;
+  const uint8_t *src = a.q + r.row * a.q_stride;
+  uint8_t *dst = reinterpret_cast<uint8_t *>(a.q_out + r.row * heads * D);
+  auto head = [&](int first) { return first + H::sub() < end ? first + H::sub() : -1; };
+  float w[H::VEC];
+  H::weights(a.q_weight, w);
   H now, next;
-  if (from < q_units) now.load(src, stride, head(from + wave, q_to, heads), lo, hi);
-  if (from < q_units + kv_units) {
-    fill_table<double, D>(lds, rot, turns, lo, hi, [&](int r) { return (int64_t)(t0 + r); });
+  now.load(src, (uint32_t)a.q_stride, head(first), r.lo, r.hi);
+  fill_table<float, D>(lds, x.rot, turns, r.lo, r.hi, [&](int i) { return (int64_t)(r.t0 + i); });
+  __syncthreads();
+  for (; first < end; first += WAVES * H::SUB) {
+    next.load(src, (uint32_t)a.q_stride, head(first + WAVES * H::SUB), r.lo, r.hi);
+    now.template turn_and_store<float, false>(lds, x.rot, w, a.q_weight != nullptr, a.eps, dst,
+                                              (uint32_t)(heads * D * 2), head(first), r.lo, r.hi);
+    now = next;
+  }
+}
+
+// Keys, then values: units as above.  What a block that is new in part held before is read
+// beside the new values.
+template <bool F32, int D>
+__device__ inline void append_block(const AppendArgs &x, int64_t seq, uint32_t block, int slice,
+                                    TurnLds<double, D> &lds) {
+  using H = Heads<F32, D>;
+  constexpr int SUB = H::SUB, WAVES = kThreads / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const KvTurned a = x.a;  // all at once
+  const KvCache c = x.c;
+  const uint64_t turns = x.rot.turns[threadIdx.x % (D / 2)];
+  const NewRows r(x.b, seq, block);
+  if (r.lo >= r.kv_hi) return;  // no place
+  const int page = x.b.table[seq * x.b.table_stride + (r.t0 >> c.page_shift)];
+  const int units = (c.kv_heads + SUB - 1) / SUB, end = min(2 * units, (slice + 1) * x.kv_per);
+  int unit = slice * x.kv_per + wave;
+  const bool turned = slice * x.kv_per < units;
+  H now;
+  auto load = [&] {
+    const int value = unit >= units, h = (unit - (value ? units : 0)) * SUB + H::sub();
+    const int64_t stride = value ? a.v_stride : a.k_stride;
+    now.load((value ? a.v : a.k) + r.row * stride, (uint32_t)stride,
+             unit < end && h < c.kv_heads ? h : -1, r.lo, r.kv_hi);
+  };
+  load();
+  if (turned) {
+    fill_table<double, D>(lds, x.rot, turns, r.lo, r.kv_hi, [&](int i) { return (int64_t)(r.t0 + i); });
     __syncthreads();
   }
-  if (from < q_units) {
-    const float *weight = args->a.q_weight;
-    float qw[H::VEC];
-    H::weights(weight, qw);
-    uint8_t *dst = reinterpret_cast<uint8_t *>(args->a.q_out + row * heads * D);
-    for (int unit = from + wave; unit < q_to; unit += WAVES) {
-      next.load(src, stride, head(unit + WAVES, q_to, heads), lo, hi);
-      now.template turn_and_store<float, false>(lds, rot, qw, weight != nullptr, eps, dst,
-                                                (uint32_t)(heads * D * 2), head(unit, q_to, heads), lo, hi);
-      now = next;
-    }
-  }
-  const int kv_hi = min(hi, last - t0);
-  if (to <= q_units || lo >= kv_hi || page < 0) return;  // no place for keys and values
-  KvCache c = args->c;
-  if (page >= c.pages) return;
-  const float *weight = args->a.k_weight;
-  // the wave's first unit past the queries
-  int unit = from + wave;
-  if (unit < q_units) unit += (q_units - unit + WAVES - 1) / WAVES * WAVES;
-  for (; unit < to; unit += WAVES) {
-    const bool value = unit >= q_units + kv_units;
-    const int h = head(unit - q_units - (value ? kv_units : 0), kv_units, kv_heads);
-    const int64_t stride = value ? args->a.v_stride : args->a.k_stride;
-    now.load((value ? args->a.v : args->a.k) + row * stride, (uint32_t)stride, h, lo, kv_hi);
-    float kw[H::VEC], val[H::PER][4][H::VEC];
-    H::weights(value ? nullptr : weight, kw);
+  if (page < 0 || page >= c.pages) return;
+  for (; unit < end; unit += WAVES) {
+    const int value = unit >= units, at = (unit - (value ? units : 0)) * SUB + H::sub();
+    const int h = at < c.kv_heads ? at : -1;
+    const OldBlock<F32, D, SUB> was(c, x.layer, page, h, value, r.t0, r.t0 + r.lo, r.t0 + r.kv_hi);
+    float w[H::VEC], val[H::PER][4][H::VEC];
+    const bool norm = a.k_weight != nullptr;
+    H::weights(value ? nullptr : a.k_weight, w);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < H::PER; ++i)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
+        const int row = 4 * H::quad(i) + t;
+        const bool mine = row >= r.lo && row < r.kv_hi;
         now.values(i, t, val[i][t]);
-        if (!value) H::template turn<double>(lds, rot, kw, weight != nullptr, eps, i, t, val[i][t]);
-        const int r = 4 * H::quad(i) + t;
+        if (!__any(mine)) continue;
+        if (!value) H::template turn<double>(lds, x.rot, w, norm, a.eps, i, t, val[i][t]);
 #pragma unroll
         for (int e = 0; e < H::VEC; ++e) {
           const uint32_t mag = __float_as_uint(val[i][t][e]) & 0x7FFFFFFFu;
-          if (r >= lo && r < kv_hi && mag < 0x7F800000u && mag > top) top = mag;
+          if (mine && mag < 0x7F800000u && mag > top) top = mag;
         }
       }
-    store_block<F32, D, SUB>(c, args->layer, page, h, value, t0, t0 + lo, t0 + kv_hi, val, top);
+    store_block<F32, D>(was, h, value, r.t0, r.t0 + r.lo, r.t0 + r.kv_hi, val, top);
+    if (unit + WAVES < end) {
+      unit += WAVES;
+      load();
+      unit -= WAVES;
+    }
   }
 }
 
-// Heads of a workgroup: one unit for each wave, as long as that makes no more workgroups
+template <bool F32, int D>
+__global__ __launch_bounds__(kThreads) void append_rotated_kernel(AppendArgs) {
+  __shared__ TurnLds<double, D> lds;
+  const AppendArgs *args = (const AppendArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+  const uint32_t slices = args->q_slices + args->kv_slices, blocks = args->blocks_per_seq;
+  const int slice = blockIdx.x % slices;
+  const uint32_t w = blockIdx.x / slices;
+  if (slice < args->q_slices) {
+    asm volatile("; queries");
+    append_queries<F32, D>(*args, w / blocks, w % blocks, slice, lds);
+  } else {
+    asm volatile("; keys and values");
+    append_block<F32, D>(*args, w / blocks, w % blocks, slice - args->q_slices, lds);
+  }
+}
+
+// Units of a workgroup: one for each wave, as long as that makes no more workgroups
 // than the card takes at a time, else three, which share a table.
 int units_each(int64_t blocks, int64_t units) {
   const int64_t waves = kThreads / 64;
@@ -528,13 +589,14 @@ hipError_t launch_kv_append_rotated(const KvCache &c, int64_t layer, const KvBat
   // n consecutive tokens touch at most (n + 30) / 16 blocks
   const int64_t blocks = ((int64_t)b.max_rows + 2 * kKvBlock - 2) / kKvBlock;
   const int sub = f32 ? sub_of<true>(c.head_dim) : sub_of<false>(c.head_dim);
-  const int units = (a.heads + sub - 1) / sub + 2 * ((c.kv_heads + sub - 1) / sub);
-  const int per = units_each(b.seqs * blocks, units);
-  const int64_t slices = (units + per - 1) / per, grid = b.seqs * blocks * slices;
+  const int q_units = (a.heads + sub - 1) / sub, kv_units = 2 * ((c.kv_heads + sub - 1) / sub);
+  const int per = units_each(b.seqs * blocks, q_units + kv_units);
+  const int q_slices = (q_units + per - 1) / per, kv_slices = (kv_units + per - 1) / per;
+  const int64_t grid = b.seqs * blocks * (q_slices + kv_slices);
   if (grid > 0x7FFFFFFF / kThreads) return hipErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
-                       AppendArgs{c, layer, b, rot, a, (uint32_t)blocks, (uint32_t)slices, per});
+                       AppendArgs{(uint32_t)blocks, q_slices, per, kv_slices, per, b, a, c, layer, rot});
   };
   if (f32) {
     if (c.head_dim == 128) go(append_rotated_kernel<true, 128>);

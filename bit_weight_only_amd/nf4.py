@@ -380,15 +380,22 @@ def nf4_kv_append(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, 
                                type, _stream(stream)), "nf4_kv_append")
 
 
+_kinds = None  # the tensors' types, by NF4_KV_*
+
+
 def _operands(where: str, gpu: int, type: int, *tensors) -> None:
     """Tensors (None and addresses are left out) lie on that GPU and hold what `type`
     says: the kernels take them as they are told to."""
+    global _kinds
+    if _kinds is None:
+        import torch
+        _kinds = {NF4_KV_BF16: torch.bfloat16, NF4_KV_F32: torch.float32}
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
             continue
-        if not t.is_cuda or t.device.index != gpu:
+        if t.get_device() != gpu:
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on one GPU")
-        if t.element_size() != (4 if type == NF4_KV_F32 else 2) or not t.is_floating_point():
+        if t.dtype is not _kinds.get(type):
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: a tensor of another type")
 
 
@@ -422,14 +429,14 @@ def nf4_rotary_init(struct, dims: int, layout: int, frequency, gain: float = 1.0
 def nf4_rotate(rotary, x, x_stride: int, x_type: int, positions, rows: int, heads: int,
                head_dim: int, weight, eps: float, y, y_stride: int, y_type: int,
                stream=None) -> None:
-    if not isinstance(x, int) and x is not None:
-        gpu = _gpu(x)
+    if x.__class__ is not int and x is not None:
+        gpu = x.get_device()
         _on_gpu("nf4_rotate", gpu)
         _operands("nf4_rotate", gpu, x_type, x)
         _operands("nf4_rotate", gpu, y_type, y)
         _operands("nf4_rotate", gpu, NF4_KV_F32, weight)
-        if not isinstance(positions, int) and positions is not None:
-            _on_gpu("nf4_rotate", gpu, _gpu(_int32(positions)))
+        if positions.__class__ is not int and positions is not None:
+            _on_gpu("nf4_rotate", gpu, _int32(positions).get_device())
     _check(lib().nf4_rotate(rotary.arg, _ptr(x), x_stride, x_type, _ptr(positions), rows, heads,
                             head_dim, _ptr(weight), eps, _ptr(y), y_stride, y_type,
                             _stream(stream)), "nf4_rotate")

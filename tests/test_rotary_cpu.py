@@ -183,7 +183,9 @@ def groups(**kw):
 
 def test_shared_attention_refusals():
     f, size = nf4.lib().nf4_kv_attention_shared, nf4.lib().nf4_kv_attention_shared_workspace_bytes
-    ok = [cache(), 0, batch(), groups(), A, 1024, 8, 0.1, 0, 0, A, None, A, 1 << 30, None]
+    # 64 sequences that share so much that it is taken apart, through the workspace
+    big = dict(seqs=64, rows=64, max_rows=1, max_len=1 << 20, table_stride=1 << 15)
+    ok = [cache(), 0, batch(**big), groups(max_prefix=4096), A, 1024, 8, 0.1, 0, 0, A, None, A, 1 << 30, None]
 
     def status(*changes):
         a = list(ok)
@@ -193,23 +195,24 @@ def test_shared_attention_refusals():
     for i in (0, 2, 3, 4, 10):
         assert status((i, None)) == nf4.NF4_ERR_NULL
     assert status((3, groups(prefix_len=None))) == nf4.NF4_ERR_NULL
-    for bad in (dict(groups=0), dict(groups=3), dict(groups=-1), dict(first=None), dict(max_rows=-1),
+    for bad in (dict(groups=0), dict(groups=65), dict(groups=-1), dict(first=None), dict(max_rows=-1),
                 dict(max_prefix=-1), dict(max_prefix=(1 << 30) + 1)):
         assert status((3, groups(**bad))) == nf4.NF4_ERR_SHAPE, bad
-        assert size(cache(), batch(), groups(**bad), 8, 0, 0) == 0
+        assert size(cache(), batch(**big), groups(**bad), 8, 0, 0) == 0
     for bad in (dict(first=A + 2), dict(prefix_len=A + 1)):
         assert status((3, groups(**bad))) == nf4.NF4_ERR_ALIGN
     for bad, want in BAD_BATCHES:
         assert status((2, batch(**bad))) == want
     for bad in BAD_SHAPES:
         assert status((0, cache(**bad))) == nf4.NF4_ERR_SHAPE
-        assert size(cache(**bad), batch(), groups(), 8, 0, 0) == 0
+        assert size(cache(**bad), batch(**big), groups(), 8, 0, 0) == 0
     for i, v in ((1, 2), (5, 1016), (6, 0), (6, 6), (7, 0.0), (7, math.nan), (8, -1), (9, -1)):
         assert status((i, v)) == nf4.NF4_ERR_SHAPE, (i, v)
     for i, v in ((4, A + 8), (5, 1028), (10, A + 4), (11, A + 2)):
         assert status((i, v)) == nf4.NF4_ERR_ALIGN, (i, v)
-    need = size(cache(), batch(), groups(), 8, 0, 0)
-    assert need > 0 and need % 16 == 0
+    need = size(cache(), batch(**big), groups(max_prefix=4096), 8, 0, 0)
+    # slots of every row and head's sums
+    assert need > 0 and need % (64 * 8 * (128 + 2) * 4) == 0
     assert status((12, None)) == nf4.NF4_ERR_NULL
     assert status((13, need - 1)) == nf4.NF4_ERR_WORKSPACE
     assert status((12, A + 8)) == nf4.NF4_ERR_ALIGN
