@@ -64,12 +64,8 @@ struct alignas(16) TurnLds {
   static constexpr bool LOW = sizeof(T) == 8;
   float2 cs[kKvBlock][D + 2];
   float2 low[LOW ? kKvBlock : 1][D + 2];
-  // 64 lanes of up to 8 values, and what a read of a last row may pass it by
-  T rows[kThreads / 64][512 / D * (D + 16 / sizeof(T)) + 8];
+  T rows[kThreads / 64][512 / D][D + D / 8 + 4];  // 64 lanes of up to 8 values
 };
-// Values of a row in LDS.
-template <class T, int D>
-constexpr int kRow = D + 16 / (int)sizeof(T);
 
 // The table for tokens r of 16, lo <= r < hi, at the positions `position(r)`.  A thread
 // has one pair in all of its turns.
@@ -199,6 +195,12 @@ __device__ inline void load_n(T (&x)[N], const T *p) {
   __builtin_memcpy(x, __builtin_assume_aligned(p, ALIGN), sizeof(x));
 }
 
+// What a wave's lanes have written to LDS before this, any of them reads after it.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Norms (weight w) and turns one token's values of one row: `v` are the lane's, from
 // value VEC * piece on; `r` the token's row of the table; `row` the row in LDS for this
 // lane's token.  All lanes of the wave come here together.
@@ -230,30 +232,38 @@ __device__ inline void turn_row(const Lds &lds, T *row, const KvRotary &rot,
 #pragma unroll
       for (int e = 0; e < VEC; ++e) other[e] = across<D / VEC>(x[e]);
     } else {
-      __builtin_memcpy(__builtin_assume_aligned(row + e0, 16), x, sizeof(x));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
       if (half % VEC == 0) {  // the other values of a lane's pairs are one piece
+        __builtin_memcpy(__builtin_assume_aligned(row + e0, 16), x, sizeof(x));
+        wave_sync();
         load_n<16>(other, row + (e0 >= rot.dims ? e0 : e0 < half ? e0 + half : e0 - half));
       } else {
-        // they start anywhere, and a lane may have first and second values of pairs: it reads
-        // the others of both kinds (of a kind that it has none of, anything of the row)
-        T below[VEC];
-        load_n<sizeof(T)>(other, row + min(e0 + half, D - 1));
-        load_n<sizeof(T)>(below, row + (e0 + VEC > half ? e0 - half : 0));
+        // they start anywhere: one at a time, a place left free after every eight values, so
+        // that lanes find theirs in different banks
+        auto place = [](int at) { return at + at / 8; };
+        int from = e0;
+        asm volatile("" : "+v"(from));  // places are worked out here, not kept from row to row
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) other[e] = e0 + e < half ? other[e] : below[e];
+        for (int e = 0; e < VEC; ++e) row[place(from) + e] = x[e];
+        wave_sync();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int at = from + e;
+          other[e] = row[place(at >= rot.dims ? at : at < half ? at + half : at - half)];
+        }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
-    float2 cs[VEC], low[VEC] = {};
-    load_n<16>(cs, &lds.cs[r][e0]);
-    if (LOW) load_n<16>(low, &lds.low[LOW ? r : 0][e0]);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const T y = turn(x[e], other[e], cs[e], low[e]);
-      x[e] = e0 + e < rot.dims ? y : x[e];
+    for (int c = 0; c < VEC; c += 4) {
+      float2 cs[4], low[4] = {};
+      load_n<16>(cs, &lds.cs[r][e0 + c]);
+      if (LOW) load_n<16>(low, &lds.low[LOW ? r : 0][e0 + c]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const T y = turn(x[c + e], other[c + e], cs[e], low[e]);
+        x[c + e] = e0 + c + e < rot.dims ? y : x[c + e];
+      }
+      if (LOW) __builtin_amdgcn_sched_barrier(0);  // registers
     }
   }
 #pragma unroll
@@ -323,7 +333,7 @@ struct Heads : Block<F32, D> {
   template <class T, class Lds>
   __device__ static void turn(Lds &lds, const KvRotary &rot, const float (&w)[B::VEC], bool norm,
                               double eps, int i, int t, float (&val)[B::VEC]) {
-    T *row = reinterpret_cast<T *>(lds.rows[threadIdx.x >> 6]) + (threadIdx.x & 63) / B::CHUNKS * kRow<T, D>;
+    T *row = lds.rows[threadIdx.x >> 6][(threadIdx.x & 63) / B::CHUNKS];
     turn_row<T, D, B::VEC>(lds, row, rot, w, norm, eps, 4 * quad(i) + t, piece(), val);
     __builtin_amdgcn_sched_barrier(0);  // one at a time: registers
   }
@@ -431,7 +441,7 @@ struct NewRows {
 // values on their way.  A unit is SUB heads.
 template <bool F32, int D>
 __device__ inline void append_queries(const AppendArgs &x, int64_t seq, uint32_t block, int slice,
-                                      TurnLds<double, D> &lds) {
+                                      TurnLds<float, D> &lds) {
   using H = Heads<F32, D>;
   constexpr int WAVES = kThreads / 64;
   const KvTurned a = x.a;  // all at once
@@ -528,25 +538,30 @@ __device__ inline void append_block(const AppendArgs &x, int64_t seq, uint32_t b
 
 template <bool F32, int D>
 __global__ __launch_bounds__(kThreads) void append_rotated_kernel(AppendArgs) {
-  __shared__ TurnLds<double, D> lds;
+  __shared__ union {
+    TurnLds<float, D> queries;
+    TurnLds<double, D> keys;
+  } lds;
   const AppendArgs *args = (const AppendArgs *)__builtin_amdgcn_kernarg_segment_ptr();
   const uint32_t slices = args->q_slices + args->kv_slices, blocks = args->blocks_per_seq;
   const int slice = blockIdx.x % slices;
   const uint32_t w = blockIdx.x / slices;
   if (slice < args->q_slices) {
     asm volatile("; queries");
-    append_queries<F32, D>(*args, w / blocks, w % blocks, slice, lds);
+    append_queries<F32, D>(*args, w / blocks, w % blocks, slice, lds.queries);
   } else {
     asm volatile("; keys and values");
-    append_block<F32, D>(*args, w / blocks, w % blocks, slice - args->q_slices, lds);
+    append_block<F32, D>(*args, w / blocks, w % blocks, slice - args->q_slices, lds.keys);
   }
 }
 
 // Units of a workgroup: one for each wave, as long as that makes no more workgroups
-// than the card takes at a time, else three, which share a table.
+// than the card takes at a time, else two, which share a table (14449 rows of 32 heads:
+// one 56.9 us, two 50.2, three 51.8; 300 rows one 17.5, two 17.6, three 19.2, with some 12
+// of a replayed graph each).
 int units_each(int64_t blocks, int64_t units) {
   const int64_t waves = kThreads / 64;
-  const int64_t per = blocks * ((units + waves - 1) / waves) <= 4 * (int64_t)device_cu_count() ? waves : 3 * waves;
+  const int64_t per = blocks * ((units + waves - 1) / waves) <= 4 * (int64_t)device_cu_count() ? waves : 2 * waves;
   return (int)(per < units ? per : units);
 }
 
@@ -592,11 +607,12 @@ hipError_t launch_kv_append_rotated(const KvCache &c, int64_t layer, const KvBat
   const int q_units = (a.heads + sub - 1) / sub, kv_units = 2 * ((c.kv_heads + sub - 1) / sub);
   const int per = units_each(b.seqs * blocks, q_units + kv_units);
   const int q_slices = (q_units + per - 1) / per, kv_slices = (kv_units + per - 1) / per;
+  const int q_per = (q_units + q_slices - 1) / q_slices, kv_per = (kv_units + kv_slices - 1) / kv_slices;
   const int64_t grid = b.seqs * blocks * (q_slices + kv_slices);
   if (grid > 0x7FFFFFFF / kThreads) return hipErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
-                       AppendArgs{(uint32_t)blocks, q_slices, per, kv_slices, per, b, a, c, layer, rot});
+                       AppendArgs{(uint32_t)blocks, q_slices, q_per, kv_slices, kv_per, b, a, c, layer, rot});
   };
   if (f32) {
     if (c.head_dim == 128) go(append_rotated_kernel<true, 128>);
