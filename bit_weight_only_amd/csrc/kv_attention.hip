@@ -736,6 +736,79 @@ struct TileLds {
   static constexpr int kCopies = 2 * (D / 64) + 2;      // per wave and stage
 };
 
+// The end of a tile of 64 rows (tile_part with H = 2): the waves that share rows add their
+// sums, through LDS that nobody copies into any more, and the rows go through it once
+// more, so that whole ones are stored side by side (a lane's own values are 16 bytes
+// of every one of its pieces: 1.7 us to store them as they lie).
+template <int D, class S, int DT>
+__device__ inline void store_halves(const KvCache &c, const KvAttention &a, const S &scope, bool whole,
+                                    int slot, const Tile &tl, int head, int sub, int half,
+                                    f32x16 (&o)[DT], float m, float sum, uint8_t *lds) {
+  constexpr int PITCH = D + 4, QUADS = D / 4;
+  static_assert(64 * (PITCH * 4 + 8) <= TileLds<D>::kBytes && 2 * 64 * (64 * DT + 8) <= TileLds<D>::kBytes,
+                "both have room in the stages");
+  const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+  f32x4 *own = reinterpret_cast<f32x4 *>(lds) + sub * (4 * DT * 64) + lane;
+  float2 *own_ml = reinterpret_cast<float2 *>(lds + 2 * 4 * DT * 64 * 16) + sub * 64 + lane;
+  float *rows = reinterpret_cast<float *>(lds);
+  float2 *rows_ml = reinterpret_cast<float2 *>(rows + 64 * PITCH);
+  __syncthreads();
+  if (half == 1) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        own[64 * (4 * t + i)] = f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+    *own_ml = make_float2(m, sum);
+  }
+  __syncthreads();
+  if (half == 0) {
+    const float2 other = *own_ml;
+    const float top = fmaxf(m, other.x);
+    const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+    const float f1 = other.x == -INFINITY ? 0.0f : exp2_fast(other.x - top);
+    m = top;
+    sum = sum * f0 + other.y * f1;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 x = own[64 * (4 * t + i)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][4 * i + e] = o[t][4 * i + e] * f0 + x[e] * f1;
+      }
+  }
+  __syncthreads();
+  if (half == 0) {
+    // element 4a + e of tile t is value DT (8a + 4h + e) + t
+    float *to = rows + (32 * sub + col) * PITCH + h * 4 * DT;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < DT; ++x) {
+        f32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = o[(4 * x + e) % DT][4 * i + (4 * x + e) / DT];
+        *reinterpret_cast<f32x4 *>(to + i * 8 * DT + 4 * x) = y;
+      }
+    if (h == 0) rows_ml[32 * sub + col] = make_float2(m, sum);
+  }
+  __syncthreads();
+  const int count = (int)min(64u, tl.rows - tl.r0);
+  for (int u = threadIdx.x; u < count * QUADS; u += 256) {
+    const int cc = u / QUADS, d = u % QUADS * 4;
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(rows + cc * PITCH + d);
+    const float2 ml = rows_ml[cc];
+    const int64_t at = tl.row_head(a, head, tl.r0 + cc);
+    if (whole) {
+      store_sums(c, a, at, d, x, ml.x, ml.y);
+    } else {
+      *reinterpret_cast<f32x4 *>(scope.sums(a.ws, slot, at, D) + d) = x;
+      if (d == 0) *scope.ml(a.ws, slot, at, D) = ml;
+    }
+  }
+}
+
 // H = 2: tiles of 64 rows, two waves for each 32 of them, which take the first and the
 // last 32 keys of every step and meet in LDS at the end.
 template <int D, int G, int H, class S>
@@ -1029,11 +1102,14 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
 
   float sum = l[0] + l[1];
   sum += __shfl_xor(sum, 32);
-  if (G > 1 || H > 1) {  // the teams' or halves' sums, through LDS that nobody copies into any more
-    const int second = G > 1 ? team : half;
+  if constexpr (H == 2) {
+    store_halves<D>(c, a, scope, place.whole(range), place.slot(), tl, head, sub, half, o, m, sum, all_lds);
+    return;
+  }
+  if (G > 1) {  // the teams' sums, through LDS that nobody copies into any more
     __syncthreads();
     float *of = reinterpret_cast<float *>(all_lds) + sub * (64 * (16 * DT + 2)) + lane;
-    if (second == 1) {
+    if (team == 1) {
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -1042,7 +1118,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
       of[64 * (16 * DT + 1)] = sum;
     }
     __syncthreads();
-    if (second == 1) return;
+    if (team == 1) return;
     const float m1 = of[64 * 16 * DT], sum1 = of[64 * (16 * DT + 1)];
     const float top = fmaxf(m, m1);
     const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
@@ -1081,19 +1157,9 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     if (a.lse && my_h == 0) a.lse[at] = log_sum(m, sum);
     return;
   }
-  float *x_to;
-  float2 *ml_to;
-  if constexpr (S::kPrefix || S::kSuffix) {
-    const int64_t at = tl.row_head(a, head, r0 + my_col);
-    x_to = scope.sums(a.ws, place.slot(), at, D);
-    ml_to = scope.ml(a.ws, place.slot(), at, D);
-  } else {
-    const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
-    float *part = static_cast<float *>(a.ws) + (item * max_splits + split) * part_floats(kTileRows, D);
-    const int row = 32 * sub + my_col;
-    x_to = part + row * D;
-    ml_to = reinterpret_cast<float2 *>(part + kTileRows * D) + row;
-  }
+  const int64_t item = ((int64_t)seq * tiles + tile) * c.kv_heads + head;
+  float *part = static_cast<float *>(a.ws) + (item * max_splits + split) * part_floats(kTileRows, D);
+  const int row = 32 * sub + my_col;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1101,9 +1167,9 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
       f32x4 y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = o[(4 * x + e) % DT][4 * i + (4 * x + e) / DT];
-      *reinterpret_cast<f32x4 *>(x_to + i * 8 * DT + my_h * 4 * DT + 4 * x) = y;
+      *reinterpret_cast<f32x4 *>(part + row * D + i * 8 * DT + my_h * 4 * DT + 4 * x) = y;
     }
-  if (my_h == 0) *ml_to = make_float2(m, sum);
+  if (my_h == 0) *reinterpret_cast<float2 *>(part + kTileRows * D + 2 * row) = make_float2(m, sum);
 }
 
 template <int D, int G>
@@ -1233,7 +1299,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
 // suffix: a workgroup takes `256 / (D / 4) / turns` rows and heads of a sequence, which lie
 // side by side in every slot.
 struct SharedJoin {
-  int width, keys, splits, steps;    // the suffix's plan
+  int splits, steps;  // the suffix's plan
   int turns;
   uint32_t per_seq;                  // workgroups of a sequence
 };
@@ -1247,7 +1313,6 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   const int d = (threadIdx.x % QUADS) * 4, t = threadIdx.x / QUADS, turn = t % j.turns;
   const int64_t seq = blockIdx.x / j.per_seq;
   const uint32_t first_row_head = (blockIdx.x % j.per_seq) * (256 / QUADS / j.turns);
-  const uint32_t group_heads = (uint32_t)a.heads / (uint32_t)c.kv_heads;
   const KvBatch::Raw raw = b.raw(seq);
   int first = 0;
   const int shared = scope.g.shared_of(b, seq, &first);
@@ -1258,14 +1323,19 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   if (first_row_head >= (uint32_t)rows * a.heads) return;
   const uint32_t i = first_row_head + t / j.turns;
   const bool on = i < (uint32_t)rows * a.heads;
-  const int tok = on ? (int)(i / a.heads) : 0;
-  // the steps of the tile that the row is in
-  const uint32_t r = tok * group_heads + (i % a.heads) % group_heads, r0 = r / j.width * j.width;
-  const uint32_t r1 = min(r0 + j.width, (uint32_t)rows * group_heads) - 1;
-  const int begin = len - n, p_lo = begin + (int)(r0 / group_heads), p_hi = begin + (int)(r1 / group_heads);
-  const Steps<N> steps(shared / N, p_lo, min(p_hi, end - 1), a.window, a.sinks);
-  const int per = Place<Suffix, N>::suffix_steps(steps.count, j.steps, j.splits);
-  const int splits = steps.count <= per ? 1 : (steps.count + per - 1) / per;
+  const int tok = on && b.max_rows > 1 ? (int)(i / a.heads) : 0;
+  int splits = 1;
+  if (j.splits > 1) {
+    // the steps of the tile that the row is in
+    constexpr int WIDTH = N == 32 ? 16 : 64;
+    const uint32_t group_heads = (uint32_t)a.heads / (uint32_t)c.kv_heads;
+    const uint32_t r = tok * group_heads + (i % a.heads) % group_heads, r0 = r / WIDTH * WIDTH;
+    const uint32_t r1 = min(r0 + WIDTH, (uint32_t)rows * group_heads) - 1;
+    const int begin = len - n, p_lo = begin + (int)(r0 / group_heads), p_hi = begin + (int)(r1 / group_heads);
+    const Steps<N> steps(shared / N, p_lo, min(p_hi, end - 1), a.window, a.sinks);
+    const int per = Place<Suffix, N>::suffix_steps(steps.count, j.steps, j.splits);
+    if (steps.count > per) splits = (steps.count + per - 1) / per;
+  }
   const bool written = shared == 0 && splits == 1;
   int shared_parts = shared > 0 ? scope.prefix_slots : 0;
   if (scope.g.max_rows < b.rows && shared > 0) {
@@ -1291,14 +1361,26 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
       if (s0 + u * j.turns < parts) join(mm, ll, x, ml[u].x, ml[u].y, y[u]);
   }
   if (j.turns > 1) {
-    xs[threadIdx.x] = x;
+    // every turn scales its own sums to the largest m, then they are added
     mls[threadIdx.x] = make_float2(mm, ll);
     __syncthreads();
-    if (turn == 0)
+    const int first_turn = threadIdx.x - turn * QUADS;
+    float top = mm;
+    for (int u = 0; u < j.turns; ++u) top = fmaxf(top, mls[first_turn + u * QUADS].x);
+    const float f = mm == -INFINITY ? 0.0f : exp2_fast(mm - top);
+    x = mm == -INFINITY ? f32x4{0, 0, 0, 0} : x * f;
+    xs[threadIdx.x] = x;
+    __syncthreads();
+    if (turn == 0) {
+      ll = ll * f;
       for (int u = 1; u < j.turns; ++u) {
         const float2 other = mls[threadIdx.x + u * QUADS];
-        join(mm, ll, x, other.x, other.y, xs[threadIdx.x + u * QUADS]);
+        if (other.x == -INFINITY) continue;
+        ll += other.y * exp2_fast(other.x - top);
+        x += xs[threadIdx.x + u * QUADS];
       }
+      mm = top;
+    }
   }
   if (parts > 0 && turn == 0) store_sums(c, a, row_head, d, x, mm, ll);
 }
@@ -1575,7 +1657,7 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
   else pick(std::integral_constant<int, 64>());
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const SharedJoin j{own.width, own.keys, (int)own.splits, own.split_steps, turns,
+  const SharedJoin j{(int)own.splits, own.split_steps, turns,
                      (uint32_t)per_seq};
   auto join = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(b.seqs * per_seq)), dim3(256), 0, s, c, b, a, scope, j);
