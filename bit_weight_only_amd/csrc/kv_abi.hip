@@ -348,6 +348,7 @@ nf4_status nf4_kv_read(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_ba
   const int64_t width = (int64_t)c.kv_heads * c.head_dim;
   if ((st = check_rows(k, k_stride, width, type)) != NF4_OK) return st;
   if ((st = check_rows(v, v_stride, width, type)) != NF4_OK) return st;
+  if (k == v) return NF4_ERR_SHAPE;
   const bool f32 = type == NF4_KV_F32;
   return from_hip(nf4::launch_kv_read(c, layer, b, {k, k_stride, f32}, {v, v_stride, f32}, stream));
 }

@@ -1541,14 +1541,30 @@ Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
 // a window of 2048, 8 heads of 128 (130 MB) 30.2 and 24.2.  A sequence whose own rows fill
 // a tile of 128 reads its keys once for them as it is.
 constexpr int64_t kSavedBytes = int64_t(64) << 20;
+// Nor where the parts would take more room than this: 400000 rows times heads of 128 in
+// ten parts, whose queries alone are 100 MB.
+constexpr int64_t kMostPartBytes = int64_t(2) << 30;
 
-bool apart(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window) {
-  const int64_t group = heads / c.kv_heads, own = b.max_rows * group;
-  if (own > kTileRows) return false;
+struct SharedPlans {
+  bool apart;
+  Plan prefix, own;
+  int64_t bytes;  // of the workspace
+};
+
+SharedPlans shared_plans(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads,
+                         int window, int sinks) {
+  SharedPlans p{};
+  const int64_t group = heads / c.kv_heads, rows = b.max_rows * group;
   int64_t keys = std::min(g.max_shared, b.max_len);
   if (window > 0) keys = std::min<int64_t>(keys, window);
-  const int64_t tiles = b.seqs * ((own + 15) / 16) - g.groups * ((g.max_rows * group + 63) / 64);
-  return tiles > 0 && keys > kSavedBytes / (tiles * c.kv_heads * 2 * c.head_dim);
+  const int64_t tiles = b.seqs * ((rows + 15) / 16) - g.groups * ((g.max_rows * group + 63) / 64);
+  if (rows > kTileRows || tiles <= 0 || keys <= kSavedBytes / (tiles * c.kv_heads * 2 * c.head_dim))
+    return p;
+  p.own = suffix_plan(c, b, g, heads, window, sinks);
+  p.prefix = prefix_plan(c, b, g, heads, window, p.own);
+  p.bytes = (p.prefix.splits + p.own.splits) * b.rows * heads * (c.head_dim + 2) * (int64_t)sizeof(float);
+  p.apart = p.bytes <= kMostPartBytes;
+  return p;
 }
 
 int64_t plan_floats(const Plan &p, int head_dim) {
@@ -1574,10 +1590,8 @@ size_t kv_attention_workspace_bytes(const KvCache &c, const KvBatch &b, int head
 
 size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, const KvGroups &g,
                                            int heads, int window, int sinks) {
-  if (!apart(c, b, g, heads, window)) return kv_attention_workspace_bytes(c, b, heads, window, sinks);
-  const Plan own = suffix_plan(c, b, g, heads, window, sinks);
-  const Plan p = prefix_plan(c, b, g, heads, window, own);
-  return (size_t)((p.splits + own.splits) * b.rows * heads * (c.head_dim + 2)) * sizeof(float);
+  const SharedPlans p = shared_plans(c, b, g, heads, window, sinks);
+  return p.apart ? (size_t)p.bytes : kv_attention_workspace_bytes(c, b, heads, window, sinks);
 }
 
 namespace {
@@ -1631,9 +1645,9 @@ hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b
 
 hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvBatch &b,
                                       const KvGroups &g, const KvAttention &a, hipStream_t s) {
-  if (!apart(c, b, g, a.heads, a.window)) return launch_kv_attention(c, layer, b, a, s);
-  const Plan own = suffix_plan(c, b, g, a.heads, a.window, a.sinks);
-  const Plan p = prefix_plan(c, b, g, a.heads, a.window, own);
+  const SharedPlans plans = shared_plans(c, b, g, a.heads, a.window, a.sinks);
+  if (!plans.apart) return launch_kv_attention(c, layer, b, a, s);
+  const Plan &p = plans.prefix, &own = plans.own;
   const int turns = join_turns(c.head_dim, p.splits + own.splits);
   const int at_once = 256 / (c.head_dim / 4) / turns;
   const int64_t per_seq = ((int64_t)b.max_rows * a.heads + at_once - 1) / at_once;

@@ -399,12 +399,24 @@ def _operands(where: str, gpu: int, type: int, *tensors) -> None:
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: a tensor of another type")
 
 
+def _stream_on(where: str, gpu: int, stream) -> int | None:
+    """The stream's handle.  The current one, and a Stream object, have to be of the
+    tensors' GPU: a launch on another GPU's would take their addresses as its own."""
+    if stream is None:
+        import torch
+        if torch.cuda.current_device() != gpu:
+            raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on the current GPU")
+    elif stream.__class__ is not int and stream.device.index != gpu:
+        raise NF4Error(NF4_ERR_SHAPE, f"{where}: a stream of another GPU")
+    return _stream(stream)
+
+
 def nf4_kv_read(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, type: int,
                 stream=None) -> None:
     _on_gpu("nf4_kv_read", cache.gpu, batch.gpu)
     _operands("nf4_kv_read", cache.gpu, type, k, v)
     _check(lib().nf4_kv_read(cache.arg, layer, batch.arg, _ptr(k), k_stride, _ptr(v), v_stride,
-                             type, _stream(stream)), "nf4_kv_read")
+                             type, _stream_on("nf4_kv_read", cache.gpu, stream)), "nf4_kv_read")
 
 
 def nf4_rotary_frequencies(dims: int, base: float, scaling: int = NF4_SCALING_PLAIN,
@@ -429,7 +441,9 @@ def nf4_rotary_init(struct, dims: int, layout: int, frequency, gain: float = 1.0
 def nf4_rotate(rotary, x, x_stride: int, x_type: int, positions, rows: int, heads: int,
                head_dim: int, weight, eps: float, y, y_stride: int, y_type: int,
                stream=None) -> None:
-    if x.__class__ is not int and x is not None:
+    if x.__class__ is int or x is None:
+        stream = _stream(stream)
+    else:
         gpu = x.get_device()
         _on_gpu("nf4_rotate", gpu)
         _operands("nf4_rotate", gpu, x_type, x)
@@ -437,9 +451,10 @@ def nf4_rotate(rotary, x, x_stride: int, x_type: int, positions, rows: int, head
         _operands("nf4_rotate", gpu, NF4_KV_F32, weight)
         if positions.__class__ is not int and positions is not None:
             _on_gpu("nf4_rotate", gpu, _int32(positions).get_device())
+        stream = _stream_on("nf4_rotate", gpu, stream)
     _check(lib().nf4_rotate(rotary.arg, _ptr(x), x_stride, x_type, _ptr(positions), rows, heads,
-                            head_dim, _ptr(weight), eps, _ptr(y), y_stride, y_type,
-                            _stream(stream)), "nf4_rotate")
+                            head_dim, _ptr(weight), eps, _ptr(y), y_stride, y_type, stream),
+           "nf4_rotate")
 
 
 def nf4_kv_append_rotated(cache, layer: int, batch, rotary, q, q_stride: int, heads: int, q_weight,
@@ -452,7 +467,8 @@ def nf4_kv_append_rotated(cache, layer: int, batch, rotary, q, q_stride: int, he
     _check(lib().nf4_kv_append_rotated(cache.arg, layer, batch.arg, rotary.arg, _ptr(q), q_stride,
                                        heads, _ptr(q_weight), _ptr(k), k_stride, _ptr(k_weight),
                                        _ptr(v), v_stride, type, eps, _ptr(q_out),
-                                       _stream(stream)), "nf4_kv_append_rotated")
+                                       _stream_on("nf4_kv_append_rotated", cache.gpu, stream)),
+           "nf4_kv_append_rotated")
 
 
 def nf4_kv_attention_workspace_bytes(cache, batch, heads: int, window: int = 0,
@@ -485,7 +501,8 @@ def nf4_kv_attention_shared(cache, layer: int, batch, groups, q, q_stride: int, 
     _operands(where, cache.gpu, NF4_KV_F32, lse)
     _check(lib().nf4_kv_attention_shared(cache.arg, layer, batch.arg, groups.arg, _ptr(q), q_stride,
                                          heads, scale, window, sinks, _ptr(out), _ptr(lse),
-                                         _ptr(workspace), ws_bytes, _stream(stream)), where)
+                                         _ptr(workspace), ws_bytes,
+                                         _stream_on(where, cache.gpu, stream)), where)
 
 
 def nf4_kv_copy_pages(cache, src, dst, n: int, stream=None) -> None:

@@ -462,7 +462,8 @@ nf4_status nf4_kv_append(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_
  * bfloat16 and fp32 hold exactly (NaN codes as NaN).  Rows that are no tokens, and
  * tokens in holes or past the table, read as zeros; rows of no sequence and rows past
  * max_rows are left as they are.  k, v: kv_heads * head_dim values a row, k_stride and
- * v_stride of them apart (a multiple of 16 bytes), which must not overlap each other.
+ * v_stride of them apart (a multiple of 16 bytes, at most 2^24 values), which must not
+ * overlap each other (NF4_ERR_SHAPE if they begin at one address).
  * Errors: as nf4_kv_append. */
 nf4_status nf4_kv_read(const nf4_kv_cache *cache, int64_t layer, const nf4_kv_batch *batch, void *k,
                        int64_t k_stride, void *v, int64_t v_stride, nf4_kv_type type,
@@ -521,13 +522,16 @@ nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout l
 
 /* Turns the heads of rows.  x: heads * head_dim values a row, bfloat16 or fp32,
  * x_stride of them apart; y the same, of its own type and stride (both multiples of 16
- * bytes, so that slices of a fused projection's rows are taken as they are).
+ * bytes and at most 2^24 values, so that slices of a fused projection's rows are taken
+ * as they are).
  * positions: device int32[rows], any values (a negative one turns back, so
  * that -p undoes p).  weight: device fp32[head_dim], 16-byte aligned, of the norm, or NULL
  * for none; eps: at least 2^-100, not looked at without a norm.  y may be x with
- * the same type and stride; else they must not overlap.  Sines, cosines and the norm's
- * sum are worked out in 64 bits, the rest in fp32, and the result rounded once to y's
- * type.  head_dim: 64 or 128; rows <= 2^23.
+ * the same type and stride (NF4_ERR_SHAPE with others); else they must not overlap.
+ * Sines and cosines are worked out in 64 bits, and so is all of an fp32 result, which
+ * is rounded once; a bfloat16 result is worked out in fp32 from them (the norm's sum in
+ * 64 bits where a mean square passes 2^100).  head_dim: 64 or 128; rows <= 2^23.
+ * Bitwise reproducible.
  * Errors: NF4_ERR_NULL, NF4_ERR_SHAPE, NF4_ERR_ALIGN. */
 nf4_status nf4_rotate(const nf4_rotary *rotary, const void *x, int64_t x_stride,
                       nf4_kv_type x_type, const int32_t *positions, int64_t rows, int64_t heads,
@@ -538,9 +542,10 @@ nf4_status nf4_rotate(const nf4_rotary *rotary, const void *x, int64_t x_stride,
  * queries and keys are normed (q_weight, k_weight: as in nf4_rotate, NULL for no norm)
  * and turned by the rows' positions; the queries go to q_out, bfloat16
  * [rows][heads * head_dim], as nf4_kv_attention takes them, and the keys and values
- * into their pages as by nf4_kv_append, the keys straight from fp32.  One launch.
- * q, k, v: rows of one type, each with its stride (a multiple of 16 bytes); heads a
- * multiple of kv_heads.  q_out may be q where that is bfloat16 with q_stride = heads *
+ * into their pages: the queries and the cache are what nf4_rotate (the keys to fp32)
+ * and then nf4_kv_append leave, bit for bit.  One launch.  q, k, v: rows of one type,
+ * each with its stride (a multiple of 16 bytes, at most 2^24 values); heads a multiple of
+ * kv_heads.  q_out may be q where that is bfloat16 with q_stride = heads *
  * head_dim; else it must not overlap q, k or v.  q_out gets zeros for rows that are no
  * tokens; rows of no sequence and rows past max_rows are left as they are.
  * Errors: NF4_ERR_NULL, NF4_ERR_SHAPE, NF4_ERR_ALIGN. */
@@ -591,8 +596,10 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_
  * int32[groups]; less than 1: none), in the same pages or in copies.  Sequences of no
  * group share nothing.  first NULL: one group of all sequences (groups == 1).
  * max_rows bounds the rows of a group together, as the host knows it (0: the
- * batch's rows): rows of a group past it do not see what is shared.  max_prefix, 0 ..
- * 2^30, bounds the lengths: longer ones count as max_prefix. */
+ * batch's rows): rows of a group past it may miss what is shared.  max_prefix, 0 ..
+ * 2^30, bounds the lengths: what a longer one has past it is read as not shared.  How
+ * the work is divided follows from both, so they cost time where they are far above
+ * what is there. */
 typedef struct nf4_kv_groups {
   int64_t groups;     /* 1 .. seqs */
   int64_t max_rows, max_prefix;
@@ -610,8 +617,8 @@ size_t nf4_kv_attention_shared_workspace_bytes(const nf4_kv_cache *cache,
  * computes, with the keys and values of a group's shared tokens read once for all of the
  * group's rows, through the table of its first sequence (or, where each sequence's own rows
  * are many, each through its own), and the tokens past them sequence by sequence;
- * the two meet through the workspace.  Rows may stand anywhere, among the shared
- * tokens too.  The weights of shared tokens are rounded to bf16 (groups of up to 32 rows
+ * the two meet through the workspace.  Calls that this would save little run as
+ * nf4_kv_attention does.  Rows may stand anywhere, among the shared tokens too.  The weights of shared tokens are rounded to bf16 (groups of up to 32 rows
  * of a kv head: to two bf16 terms).  Bitwise reproducible run to run for a given
  * device.  Other arguments and errors as nf4_kv_attention; NF4_ERR_NULL for a missing
  * structure or prefix_len, NF4_ERR_SHAPE for its sizes. */

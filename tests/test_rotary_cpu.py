@@ -126,6 +126,8 @@ def test_rotate_refusals():
     assert status((0, rotary(dims=66)), (7, 64), (6, 16)) == nf4.NF4_ERR_SHAPE  # more than the head
     for i, v in ((1, A + 8), (2, 1028), (4, A + 2), (8, A + 4), (10, 2 * A + 8), (11, 1028)):
         assert status((i, v)) == nf4.NF4_ERR_ALIGN, (i, v)
+    wide = (1 << 24) + 8  # rows further apart than the kernels go
+    assert status((2, wide)) == status((11, wide)) == nf4.NF4_ERR_SHAPE
     # in place with another type or stride
     assert status((10, A), (12, 1)) == status((10, A), (11, 1032)) == nf4.NF4_ERR_SHAPE
 
@@ -154,11 +156,13 @@ def test_append_rotated_refusals():
                  (12, 513), (15, A + 2)):
         assert status((i, v)) == nf4.NF4_ERR_ALIGN, (i, v)
     assert status((15, A), (13, 1)) == status((15, A), (5, 1032)) == nf4.NF4_ERR_SHAPE
+    wide = (1 << 24) + 8  # rows further apart than the kernels go
+    assert status((5, wide)) == status((9, wide)) == status((12, wide)) == nf4.NF4_ERR_SHAPE
 
 
 def test_read_refusals():
     f = nf4.lib().nf4_kv_read
-    ok = [cache(), 0, batch(), A, 512, A, 512, 0, None]
+    ok = [cache(), 0, batch(), A, 512, 2 * A, 512, 0, None]
 
     def status(i, v):
         a = list(ok)
@@ -170,7 +174,8 @@ def test_read_refusals():
         assert status(0, cache(**bad)) == nf4.NF4_ERR_SHAPE
     for bad, want in BAD_BATCHES:
         assert status(2, batch(**bad)) == want
-    for i, v in ((1, -1), (1, 2), (4, 504), (6, 511), (7, 2), (7, -1)):
+    wide = (1 << 24) + 8  # rows further apart than the kernels go
+    for i, v in ((1, -1), (1, 2), (4, 504), (6, 511), (7, 2), (7, -1), (5, A), (4, wide), (6, wide)):
         assert status(i, v) == nf4.NF4_ERR_SHAPE, (i, v)
     for i, v in ((3, A + 8), (5, A + 2), (4, 516), (6, 513)):
         assert status(i, v) == nf4.NF4_ERR_ALIGN, (i, v)
@@ -256,3 +261,30 @@ def test_tensors_on_the_host_are_refused():
     for call in calls[:2]:
         with pytest.raises(nf4.NF4Error, match="not on one GPU"):
             call()
+
+
+def test_streams_of_another_gpu_are_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        def __init__(self, index):
+            self.device, self.cuda_stream = torch.device(f"cuda:{index}"), 0x50 + index
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(nf4, "_stream",
+                        lambda s: 0x77 if s is None else s if isinstance(s, int) else s.cuda_stream)
+    assert nf4._stream_on("f", 1, None) == 0x77
+    assert nf4._stream_on("f", 0, 0x60) == 0x60
+    assert nf4._stream_on("f", 2, Stream(2)) == 0x52
+    for gpu, stream in ((0, None), (0, Stream(1)), (1, Stream(0))):
+        with pytest.raises(nf4.NF4Error) as e:
+            nf4._stream_on("f", gpu, stream)
+        assert e.value.status == nf4.NF4_ERR_SHAPE
+
+
+def test_parts_that_take_too_much_room_are_not_taken_apart():
+    shared = nf4.lib().nf4_kv_attention_shared_workspace_bytes
+    plain = nf4.lib().nf4_kv_attention_workspace_bytes
+    for rows, apart in ((1000, True), (1 << 20, False)):
+        b = batch(seqs=rows, rows=rows, max_rows=1, max_len=20000, table_stride=400)
+        need = shared(cache(), b, groups(groups=1, max_prefix=16000), 8, 0, 0)
+        assert (need != plain(cache(), b, 8, 0, 0)) == apart and need <= 2 << 30
