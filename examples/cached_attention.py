@@ -5,7 +5,8 @@
 Two prompts go in as one ragged batch, the first one branches into two
 continuations that share its pages, and all of them decode token by token
 under a sliding window with a few first tokens that stay visible, one captured
-graph per step.  Then the prompt's own row is released and the pool compacted.
+graph per step.  Queries and keys are turned by their positions as they are
+appended, and attention knows which tokens the continuations share.  Then the prompt's own row is released and the pool compacted.
 The last hidden states are compared with the same computation in fp32 without
 a cache: the difference is the cache's (keys and values in 8 bits).
 """
@@ -20,10 +21,11 @@ from bit_weight_only_amd import nf4  # noqa: E402
 HIDDEN, HEADS, KV, DIM, LAYERS = 512, 8, 2, 64, 2
 PAGE, PAGES, WINDOW, SINKS = 32, 40, 48, 4
 SCALE = DIM ** -0.5
+ROTARY = nf4.Rotary(DIM)
 
 
 def rotate(x, at):
-    """Rotary position embedding of rows x [rows][heads * DIM] at positions at."""
+    """What ROTARY does to rows x [rows][heads * DIM] at positions at, in fp32."""
     x = x.reshape(len(x), -1, 2, DIM // 2)
     angle = at[:, None] * 10000.0 ** (-torch.arange(DIM // 2, device=x.device) / (DIM // 2))
     c, s = angle.cos()[:, None], angle.sin()[:, None]
@@ -56,19 +58,23 @@ class Layers:
         return y
 
 
-def forward(net, cache, batch, x, at, window):
-    """One step of rows x (fp32 hidden states at positions `at`) through the layers."""
-    n = nf4.nf4_kv_attention_workspace_bytes(cache, batch, HEADS, window, SINKS)
+def forward(net, cache, batch, x, window, groups=None):
+    """One step of rows x (fp32 hidden states) through the layers."""
+    shared = () if groups is None else (groups,)
+    size, attention = ((nf4.nf4_kv_attention_workspace_bytes, nf4.nf4_kv_attention) if groups is None
+                       else (nf4.nf4_kv_attention_shared_workspace_bytes, nf4.nf4_kv_attention_shared))
+    n = size(cache, batch, *shared, HEADS, window, SINKS)
     ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
     for layer, (qkv, wo) in enumerate(net.packed):
         y = net.linear(x.bfloat16(), qkv)
-        q = rotate(y[:, :HEADS * DIM], at).bfloat16()
-        k = rotate(y[:, HEADS * DIM:(HEADS + KV) * DIM], at)
-        v = y[:, (HEADS + KV) * DIM:]  # as the projection left it, fp32 and strided
-        nf4.nf4_kv_append(cache, layer, batch, k, k.stride(0), v, v.stride(0), nf4.NF4_KV_F32)
+        # slices of the rows as the projection left them, fp32 and strided
+        k, v = y[:, HEADS * DIM:], y[:, (HEADS + KV) * DIM:]
+        q = torch.empty(len(y), HEADS * DIM, dtype=torch.bfloat16, device="cuda")
+        nf4.nf4_kv_append_rotated(cache, layer, batch, ROTARY, y, y.stride(0), HEADS, None, k,
+                                  k.stride(0), None, v, v.stride(0), nf4.NF4_KV_F32, 0.0, q)
         out = torch.empty_like(q)
-        nf4.nf4_kv_attention(cache, layer, batch, q, q.stride(0), HEADS, SCALE, window, SINKS, out,
-                             None, ws, n)
+        attention(cache, layer, batch, *shared, q, q.stride(0), HEADS, SCALE, window, SINKS, out,
+                  None, ws, n)
         x = x + net.linear(out, wo)
     return x
 
@@ -110,20 +116,21 @@ def main(tokens=20):
     nf4.nf4_kv_reserve(cache, pool, i32(*lengths, 0, 0))
     batch = nf4.KVBatch(pool.length[:2], pool.table[:2], row_start=i32(0, 150, 220), rows=220,
                         max_rows=150, max_len=150)
-    at = torch.cat([torch.arange(n, device="cuda") for n in lengths])
-    forward(net, cache, batch, torch.cat(prompts), at, 0)
+    forward(net, cache, batch, torch.cat(prompts), 0)
 
     # row 0 continues as rows 2 and 3; rows 1 to 3 go on, a token at a time
     nf4.nf4_kv_fork(cache, pool, i32(0, 0), i32(2, 3), 2)
     nf4.nf4_kv_release(cache, pool, i32(0), 1)
     new = torch.randn(tokens, 3, HIDDEN, device="cuda")
     batch = nf4.KVBatch(pool.length[1:], pool.table[1:], max_len=width * PAGE)
+    # the last two of the batch share the prompt
+    groups = nf4.KVGroups(i32(lengths[0]), i32(1, 3), max_rows=2, max_prefix=lengths[0])
     one, x, missing = i32(0, 1, 1, 1), torch.empty(3, HIDDEN, device="cuda"), i32(0)
 
     def step():
         nf4.nf4_kv_reserve(cache, pool, one)
         missing.add_(pool.missing)
-        return forward(net, cache, batch, x, pool.length[1:] - 1, WINDOW)
+        return forward(net, cache, batch, x, WINDOW, groups)
 
     x.copy_(new[0])
     last = step()  # eager once, then captured: lengths and pages live on the device
