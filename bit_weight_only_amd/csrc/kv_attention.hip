@@ -1187,7 +1187,7 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 // unit, the latter by memory.
 struct SharedPlan {
   uint32_t prefix_grid, prefix_tiles, tiles;
-  int prefix_splits, prefix_steps, splits, steps;
+  int prefix_splits, splits, steps;  // steps of a suffix's part
 };
 
 // A workgroup's tile of ROWS rows: 16 or 64.
@@ -1223,8 +1223,8 @@ __global__ __launch_bounds__(256, 2) void shared_kernel(SharedArgs) {
   if (blockIdx.x < prefix_grid) {
     asm volatile("; a prefix");
     const SharedArgs x = *args;
-    shared_part<D, PREFIX_ROWS>(x.c, x.layer, x.b, x.a, x.p.prefix_tiles, x.p.prefix_splits,
-                                x.p.prefix_steps, Prefix{x.scope}, blockIdx.x, lds);
+    shared_part<D, PREFIX_ROWS>(x.c, x.layer, x.b, x.a, x.p.prefix_tiles, x.p.prefix_splits, 0,
+                                Prefix{x.scope}, blockIdx.x, lds);
   } else {
     asm volatile("; a suffix");
     const SharedArgs x = *args;
@@ -1301,7 +1301,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
 struct SharedJoin {
   int splits, steps;  // the suffix's plan
   int turns;
-  uint32_t per_seq;                  // workgroups of a sequence
+  uint32_t per_seq;   // workgroups of a sequence
 };
 
 template <int D, int N>
@@ -1545,10 +1545,23 @@ constexpr int64_t kSavedBytes = int64_t(64) << 20;
 // ten parts, whose queries alone are 100 MB.
 constexpr int64_t kMostPartBytes = int64_t(2) << 30;
 
+// Up to 2^31 threads a launch.
+bool fits(const Plan &p) { return p.items * p.splits <= 0x7FFFFFFF / (256 * p.teams); }
+
+// Rows of a tile side by side in a workgroup of the join, and turns over the parts: as
+// many turns as there are four parts for each, the rest of the threads on other rows.
+int join_turns(int head_dim, int64_t parts) {
+  int turns = 256 / (head_dim / 4);
+  while (turns > 1 && parts <= 2 * turns) turns /= 2;
+  return turns;
+}
+
 struct SharedPlans {
   bool apart;
   Plan prefix, own;
-  int64_t bytes;  // of the workspace
+  int turns;        // of the join, and its workgroups of a sequence
+  int64_t per_seq;
+  int64_t bytes;    // of the workspace
 };
 
 SharedPlans shared_plans(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads,
@@ -1563,20 +1576,18 @@ SharedPlans shared_plans(const KvCache &c, const KvBatch &b, const KvGroups &g, 
   p.own = suffix_plan(c, b, g, heads, window, sinks);
   p.prefix = prefix_plan(c, b, g, heads, window, p.own);
   p.bytes = (p.prefix.splits + p.own.splits) * b.rows * heads * (c.head_dim + 2) * (int64_t)sizeof(float);
-  p.apart = p.bytes <= kMostPartBytes;
+  p.turns = join_turns(c.head_dim, p.prefix.splits + p.own.splits);
+  const int64_t at_once = 256 / (c.head_dim / 4) / p.turns;
+  p.per_seq = (b.max_rows * (int64_t)heads + at_once - 1) / at_once;
+  Plan both = p.own;  // one launch
+  both.items = p.prefix.items * p.prefix.splits + p.own.items * p.own.splits;
+  both.splits = 1;
+  p.apart = p.bytes <= kMostPartBytes && fits(both) && b.seqs * p.per_seq <= 0x7FFFFFFF / 256;
   return p;
 }
 
 int64_t plan_floats(const Plan &p, int head_dim) {
   return p.items * p.splits * part_floats(p.width, head_dim);
-}
-
-// Rows of a tile side by side in a workgroup of the join, and turns over the parts: as
-// many turns as there are four parts for each, the rest of the threads on other rows.
-int join_turns(int head_dim, int64_t parts) {
-  int turns = 256 / (head_dim / 4);
-  while (turns > 1 && parts <= 2 * turns) turns /= 2;
-  return turns;
 }
 
 }  // namespace
@@ -1593,13 +1604,6 @@ size_t kv_attention_shared_workspace_bytes(const KvCache &c, const KvBatch &b, c
   const SharedPlans p = shared_plans(c, b, g, heads, window, sinks);
   return p.apart ? (size_t)p.bytes : kv_attention_workspace_bytes(c, b, heads, window, sinks);
 }
-
-namespace {
-
-// Up to 2^31 threads a launch.
-bool fits(const Plan &p) { return p.items * p.splits <= 0x7FFFFFFF / (256 * p.teams); }
-
-}  // namespace
 
 hipError_t launch_kv_attention(const KvCache &c, int64_t layer, const KvBatch &b,
                                const KvAttention &a, hipStream_t s) {
@@ -1648,15 +1652,9 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
   const SharedPlans plans = shared_plans(c, b, g, a.heads, a.window, a.sinks);
   if (!plans.apart) return launch_kv_attention(c, layer, b, a, s);
   const Plan &p = plans.prefix, &own = plans.own;
-  const int turns = join_turns(c.head_dim, p.splits + own.splits);
-  const int at_once = 256 / (c.head_dim / 4) / turns;
-  const int64_t per_seq = ((int64_t)b.max_rows * a.heads + at_once - 1) / at_once;
-  if (!fits(p) || !fits(own) || b.seqs * per_seq > 0x7FFFFFFF / 256 ||
-      p.items * p.splits + own.items * own.splits > 0x7FFFFFFF / 256)
-    return hipErrorInvalidConfiguration;
   const Shared scope{g, b.rows * a.heads, (int)p.splits, (int)(p.splits + own.splits)};
   const SharedPlan plan{(uint32_t)(p.items * p.splits), (uint32_t)p.tiles, (uint32_t)own.tiles,
-                        (int)p.splits, p.split_steps, (int)own.splits, own.split_steps};
+                        (int)p.splits, (int)own.splits, own.split_steps};
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits + own.items * own.splits)), dim3(256),
                        0, s, SharedArgs{c, layer, b, a, scope, plan});
@@ -1671,10 +1669,9 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
   else pick(std::integral_constant<int, 64>());
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const SharedJoin j{(int)own.splits, own.split_steps, turns,
-                     (uint32_t)per_seq};
+  const SharedJoin j{(int)own.splits, own.split_steps, plans.turns, (uint32_t)plans.per_seq};
   auto join = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(b.seqs * per_seq)), dim3(256), 0, s, c, b, a, scope, j);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(b.seqs * plans.per_seq)), dim3(256), 0, s, c, b, a, scope, j);
   };
   if (own.few) {
     if (c.head_dim == 128) join(join_shared_kernel<128, 32>);

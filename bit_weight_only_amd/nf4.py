@@ -451,6 +451,8 @@ def nf4_rotate(rotary, x, x_stride: int, x_type: int, positions, rows: int, head
         _operands("nf4_rotate", gpu, NF4_KV_F32, weight)
         if positions.__class__ is not int and positions is not None:
             _on_gpu("nf4_rotate", gpu, _int32(positions).get_device())
+            if positions.numel() < rows:
+                raise NF4Error(NF4_ERR_SHAPE, "nf4_rotate: fewer positions than rows")
         stream = _stream_on("nf4_rotate", gpu, stream)
     _check(lib().nf4_rotate(rotary.arg, _ptr(x), x_stride, x_type, _ptr(positions), rows, heads,
                             head_dim, _ptr(weight), eps, _ptr(y), y_stride, y_type, stream),

@@ -593,8 +593,10 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_
 /* Sequences of a batch that begin with the same tokens, as nf4_kv_fork leaves them:
  * sequences first[g] .. first[g + 1] - 1 (device int32[groups + 1], ascending) all
  * have the same keys and values in their first prefix_len[g] tokens (device
- * int32[groups]; less than 1: none), in the same pages or in copies.  Sequences of no
- * group share nothing.  first NULL: one group of all sequences (groups == 1).
+ * int32[groups]; less than 1: none), in the same pages or in copies.  A sequence may
+ * have fewer tokens than that, but the first one of a group not fewer of the shared
+ * ones than any other: they are read from its pages.  Sequences of no group share
+ * nothing.  first NULL: one group of all sequences (groups == 1).
  * max_rows bounds the rows of a group together, as the host knows it (0: the
  * batch's rows): rows of a group past it may miss what is shared.  max_prefix, 0 ..
  * 2^30, bounds the lengths: what a longer one has past it is read as not shared.  How

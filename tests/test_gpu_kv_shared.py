@@ -43,11 +43,11 @@ class Shared(Case):
                 own = min(n, self.kv_len[s], self.kv_len[a])  # what both have
                 whole = own // page
                 self.table[s, :whole] = self.table[a, :whole]
-                for b in range(whole * page, own, kv.BLOCK):  # the rest in copies, whole blocks
+                for b in range(whole * page, own):  # the rest in copies, with their scales
                     p, q = self.table[a, b // page], self.table[s, b // page]
                     u = b % page
-                    self.c.k[:, q, :, u:u + 16] = self.c.k[:, p, :, u:u + 16]
-                    self.c.v[:, q, :, u // 4:u // 4 + 4] = self.c.v[:, p, :, u // 4:u // 4 + 4]
+                    self.c.k[:, q, :, u] = self.c.k[:, p, :, u]
+                    self.c.v[:, q, :, u // 4, :, u % 4] = self.c.v[:, p, :, u // 4, :, u % 4]
                     for x in (self.c.ks, self.c.vs):
                         x[:, q, :, u // 16] = x[:, p, :, u // 16]
 
@@ -94,7 +94,7 @@ class Shared(Case):
 # (lengths, groups' first sequences, shared tokens)
 BATCHES = [([20, 21], [0, 2], [16]), ([40, 33, 64], [0, 3], [33]), ([1, 2, 3, 4], [0, 4], [1]),
            ([70, 130, 65, 64, 200, 90], [0, 2, 3, 6], [64, 10, 50]),
-           ([300, 301, 280, 5, 290], [1, 3, 5], [250, 300])]
+           ([300, 301, 280, 290, 5], [1, 3, 5], [250, 300])]
 
 
 @pytest.mark.parametrize("dim,page,heads,kv_heads", SHAPES)
