@@ -103,25 +103,52 @@ __device__ inline int lanes_min(int v) {
   return __builtin_amdgcn_readfirstlane(v);
 }
 
+// A number that the host knows and workgroups divide by: n / value for n under 2^31, as
+// n factor / 2^shift with factor = 2^shift / value rounded up, shift = 31 + log2 value
+// rounded up, so that what rounding adds stays under one part.  (A division by a number that
+// is not known beforehand takes some 30 instructions that wait for one another.)
+struct Divisor {
+  uint32_t value, factor, shift;
+  static Divisor of(int64_t value) {
+    uint32_t s = 0;
+    while ((int64_t(1) << s) < value) ++s;
+    return Divisor{(uint32_t)value, (uint32_t)(((uint64_t(1) << (31 + s)) + value - 1) / value), 31 + s};
+  }
+  __device__ operator uint32_t() const { return value; }
+  friend __device__ uint32_t operator/(uint32_t n, const Divisor &d) {
+    return (uint32_t)((uint64_t)n * d.factor >> d.shift);
+  }
+  friend __device__ uint32_t operator%(uint32_t n, const Divisor &d) { return n - n / d * d.value; }
+};
+
 // What a workgroup takes of the keys: all that its rows see, or, where sequences share
 // their first tokens, those of the shared ones (rows of a whole group at once, its
 // keys split at fixed places) or those past them.  The parts of the latter two meet in
 // the workspace: slot i holds the i-th part's sums of every row and head, [rows][heads][D],
-// the prefix's parts before the suffix's; behind all slots (m, l) of each.
+// the prefix's parts before the suffix's; behind all slots (m, l) of each.  All of it is
+// less than 2^32 bytes (kMostPartBytes), so that places are 32 bits past one address.
 struct Shared {
+  using Number = Divisor;
   KvGroups g;
-  int64_t row_heads;
+  uint32_t row_heads;
   int prefix_slots, slots;
-  __device__ float *sums(void *ws, int slot, int64_t row_head, int dim) const {
-    return static_cast<float *>(ws) + (slot * row_heads + row_head) * dim;
+  Divisor kv_heads, heads_each;  // heads of keys, and of queries to each
+  __device__ Divisor heads(const KvCache &) const { return kv_heads; }
+  __device__ Divisor group(const KvCache &, const KvAttention &) const { return heads_each; }
+  __device__ f32x4 *sums(void *ws, uint32_t slot, uint32_t row_head, int dim, int d) const {
+    return reinterpret_cast<f32x4 *>(static_cast<uint8_t *>(ws) + ((slot * row_heads + row_head) * dim + d) * 4);
   }
-  __device__ float2 *ml(void *ws, int slot, int64_t row_head, int dim) const {
-    return reinterpret_cast<float2 *>(static_cast<float *>(ws) + slots * row_heads * dim) +
-           (slot * row_heads + row_head);
+  __device__ float2 *ml(void *ws, uint32_t slot, uint32_t row_head, int dim) const {
+    return reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + (slots * row_heads * dim * 4 + (slot * row_heads + row_head) * 8));
   }
 };
 struct Whole {
   static constexpr bool kPrefix = false, kSuffix = false;
+  using Number = uint32_t;
+  __device__ static uint32_t heads(const KvCache &c) { return (uint32_t)c.kv_heads; }
+  __device__ static uint32_t group(const KvCache &c, const KvAttention &a) {
+    return (uint32_t)a.heads / (uint32_t)c.kv_heads;
+  }
 };
 struct Prefix : Shared {
   static constexpr bool kPrefix = true, kSuffix = false;
@@ -189,14 +216,15 @@ int64_t most_steps(int N, const KvBatch &b, int tile_rows, int window, int sinks
 
 // Rows of a sequence's tile: query row r of a kv head is token r / group and
 // head r % group of its group.
-struct Tile {
+template <class Number>
+struct TileOf {
   int64_t row0;
-  int all;                   // rows of a group, max_rows or no
-  uint32_t rows, r0, group;  // rows of a kv head of one sequence stay under 2^31
+  int all;            // rows of a group, max_rows or no
+  Number group;
+  uint32_t rows, r0;  // rows of a kv head of one sequence stay under 2^31
   int n, len, end, p_lo, p_hi;
-  __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, const KvBatch::Raw &seq,
-                  uint32_t tile, uint32_t width) {
-    group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
+  __device__ TileOf(Number group, const KvBatch &b, const KvBatch::Raw &seq, uint32_t tile, uint32_t width)
+      : group(group) {
     b.sequence(seq, row0, n, len, end);
     rows = (uint32_t)(n < b.max_rows ? n : b.max_rows) * group;
     r0 = tile * width;
@@ -213,9 +241,9 @@ struct Tile {
   __device__ int last_key(int p) const { return min(p, end - 1); }
 
   // A tile of all rows of a group of sequences over the tokens that they share.
-  __device__ Tile(const KvCache &c, const KvBatch &b, const KvAttention &a, const KvGroups &g,
-                  int first, int past, int shared, uint32_t tile, uint32_t width) {
-    group = (uint32_t)a.heads / (uint32_t)c.kv_heads;
+  __device__ TileOf(Number group, const KvBatch &b, const KvGroups &g, int first, int past, int shared,
+                    uint32_t tile, uint32_t width)
+      : group(group) {
     row0 = b.first_row(first);
     const int64_t many = first < past ? b.first_row(past) - row0 : 0;
     all = (int)(many < 0 ? 0 : many);
@@ -257,29 +285,34 @@ struct Tile {
     return t < 64 ? x : y;
   }
 };
+using Tile = TileOf<uint32_t>;
 
 // Where a workgroup works: the tile `index` of sequence (or group) `seq`, part `split` of
 // its keys.
 struct Range {
-  int begin, end, splits;  // of the list of steps; parts that the list has
+  int begin, end;  // of the list of steps
+  bool one, none;  // the only part of the list; one past its last part
 };
 
 template <class S, int N>
 struct Place {
+  using Number = typename S::Number;
   const KvCache &c;
   const KvBatch &b;
   const KvAttention &a;
   const S &scope;
   int seq;
   uint32_t index, width;
-  int split, max_splits, split_steps;
+  int split;
+  Number max_splits;
+  int split_steps;
   int first, past;  // sequences of the group
   KvBatch::Raw raw;
   int shared;
   const int32_t *table;
 
   __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const S &scope,
-                   int seq, uint32_t index, uint32_t width, int split, int max_splits,
+                   int seq, uint32_t index, uint32_t width, int split, Number max_splits,
                    int split_steps)
       : c(c), b(b), a(a), scope(scope), seq(seq), index(index), width(width), split(split),
         max_splits(max_splits), split_steps(split_steps), first(seq), past(seq + 1), shared(0) {
@@ -293,13 +326,10 @@ struct Place {
     // (a group without sequences has no rows: nothing of its table is read)
     table = b.table + (int64_t)(first < b.seqs ? first : 0) * b.table_stride;
   }
-  __device__ static uint32_t count(const KvBatch &b, const S &scope) {
-    if constexpr (S::kPrefix) return (uint32_t)scope.g.groups;
-    return (uint32_t)b.seqs;
-  }
+  using Tile = TileOf<typename S::Number>;
   __device__ Tile tile() const {
-    if constexpr (S::kPrefix) return Tile(c, b, a, scope.g, first, past, shared, index, width);
-    return Tile(c, b, a, raw, index, width);
+    if constexpr (S::kPrefix) return Tile(scope.group(c, a), b, scope.g, first, past, shared, index, width);
+    else return Tile(scope.group(c, a), b, raw, index, width);
   }
   // Without a window what a prefix's rows see does not wait for their positions.
   __device__ bool ahead() const { return S::kPrefix && a.window == 0; }
@@ -311,21 +341,22 @@ struct Place {
   // The steps that the host has planned for a part, or more where it has made room for
   // fewer parts; a prefix has all of its parts, some of them with nothing to do.
   __device__ Range range(const Steps<N> &s) const {
-    const int per = S::kPrefix ? (s.count + max_splits - 1) / max_splits
+    const int per = S::kPrefix ? in_parts(s.count, max_splits)
                     : S::kSuffix ? suffix_steps(s.count, split_steps, max_splits) : split_steps;
-    return Range{split * per, min(s.count, (split + 1) * per),
-                 S::kPrefix ? max_splits : s.count <= per ? 1 : (s.count + per - 1) / per};
+    return Range{split * per, min(s.count, (split + 1) * per), !S::kPrefix && s.count <= per,
+                 !S::kPrefix && split > 0 && split * per >= s.count};
   }
   // Whether a range holds all keys that the rows see.
-  __device__ bool whole(const Range &r) const {
-    return !S::kPrefix && r.splits == 1 && shared == 0;
-  }
+  __device__ bool whole(const Range &r) const { return r.one && shared == 0; }
   __device__ int slot() const {
     if constexpr (S::kSuffix) return scope.prefix_slots + split;
     return split;
   }
-  __device__ static int suffix_steps(int count, int split_steps, int max_splits) {
-    return max(split_steps, (count + max_splits - 1) / max_splits);
+  __device__ static int in_parts(int count, Number parts) {
+    return (int)(((uint32_t)count + parts - 1) / parts);
+  }
+  __device__ static int suffix_steps(int count, int split_steps, Number max_splits) {
+    return max(split_steps, in_parts(count, max_splits));
   }
 };
 
@@ -370,7 +401,8 @@ __device__ inline void store_sums(const KvCache &c, const KvAttention &a, int64_
   if (a.lse && d == 0) a.lse[at] = log_sum(m, l);
 }
 // The same of row `cc` of a tile.
-__device__ inline void store_row(const KvCache &c, const KvAttention &a, const Tile &tl, int head,
+template <class T>
+__device__ inline void store_row(const KvCache &c, const KvAttention &a, const T &tl, int head,
                                  int cc, int d, f32x4 x, float m, float l) {
   store_sums(c, a, tl.row_head(a, head, tl.r0 + cc), d, x, m, l);
 }
@@ -434,9 +466,10 @@ struct DecodeLds {
 
 template <int D, int W, class S>
 __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatch &b,
-                                   const KvAttention &a, uint32_t tiles, int max_splits,
-                                   int split_steps, const S &scope, uint32_t w,
-                                   DecodeLds<D, W> &lds) {
+                                   const KvAttention &a, typename S::Number tiles,
+                                   typename S::Number max_splits, int split_steps, const S &scope,
+                                   uint32_t w, DecodeLds<D, W> &lds) {
+  using Tile = TileOf<typename S::Number>;
   constexpr int KS = D / 32;   // k-steps of the first product
   constexpr int DT = D / 16;   // tiles of 16 values of the second
   constexpr int PITCH = DecodeLds<D, W>::kPitch;
@@ -447,10 +480,10 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   // neighbouring workgroups take the heads of one page, so that what is read
   // at a time lies side by side (64 sequences of up to 16384 tokens: 256 us
   // with the parts of a head side by side instead, 217 us this way)
-  const int head = w % (uint32_t)c.kv_heads;
-  w /= (uint32_t)c.kv_heads;
-  const int split = w % (uint32_t)max_splits;
-  w /= (uint32_t)max_splits;
+  const int head = w % scope.heads(c);
+  w = w / scope.heads(c);
+  const int split = w % max_splits;
+  w = w / max_splits;
   const uint32_t item = w * (uint32_t)c.kv_heads + head;
   const Place<S, 32> place(c, b, a, scope, w / tiles, w % tiles, 16, split, max_splits, split_steps);
   const int32_t *table = place.table;
@@ -466,10 +499,10 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   if (tl.empty()) return;
   int at[2];
   if (S::kPrefix && !place.ahead())
-    tl.positions<16>(b, place.first, place.past, tl.guess<16>(b, place.first, place.past), at);
+    tl.template positions<16>(b, place.first, place.past, tl.template guess<16>(b, place.first, place.past), at);
   const Steps<32> steps = place.steps(tl, tl.p_hi);
   const Range range = place.range(steps);
-  if (split >= range.splits) return;
+  if (range.none) return;
   const int end = range.end;
 
   const bool mine = tl.r0 + col < tl.rows;
@@ -529,15 +562,15 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   };
 
   look(first);
-  Tile::Guesses guesses = {};
-  if (S::kPrefix && place.ahead()) guesses = tl.guess<16>(b, place.first, place.past);
+  typename Tile::Guesses guesses = {};
+  if (S::kPrefix && place.ahead()) guesses = tl.template guess<16>(b, place.first, place.past);
 
   bf16x8 q[KS];
   const uint16_t *qp = a.q + (tl.row0 + tok) * a.q_stride + (int64_t)qh * D + g * 16;
 #pragma unroll
   for (int j = 0; j < KS; ++j)
     q[j] = *reinterpret_cast<const bf16x8 *>(qp + 64 * (j / 2) + 8 * (j % 2));
-  if (S::kPrefix && place.ahead()) tl.positions<16>(b, place.first, place.past, guesses, at);
+  if (S::kPrefix && place.ahead()) tl.template positions<16>(b, place.first, place.past, guesses, at);
   const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
   const int pos = mine ? row_pos : -1;
 
@@ -688,8 +721,8 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
     if (place.whole(range)) {
       store_row(c, a, tl, head, cc, d, x, mm, ll);
     } else if constexpr (S::kPrefix || S::kSuffix) {
-      const int64_t at = tl.row_head(a, head, tl.r0 + cc);
-      *reinterpret_cast<f32x4 *>(scope.sums(a.ws, place.slot(), at, D) + d) = x;
+      const uint32_t at = (uint32_t)tl.row_head(a, head, tl.r0 + cc);
+      *scope.sums(a.ws, place.slot(), at, D, d) = x;
       if (d == 0) *scope.ml(a.ws, place.slot(), at, D) = make_float2(mm, ll);
     } else {
       *reinterpret_cast<f32x4 *>(part + cc * D + d) = x;
@@ -736,74 +769,99 @@ struct TileLds {
   static constexpr int kCopies = 2 * (D / 64) + 2;      // per wave and stage
 };
 
-// The end of a tile of 64 rows (tile_part with H = 2): the waves that share rows add their
-// sums, through LDS that nobody copies into any more, and the rows go through it once
-// more, so that whole ones are stored side by side (a lane's own values are 16 bytes
-// of every one of its pieces: 1.7 us to store them as they lie).
+// The end of a tile of 64 rows (tile_part with H = 2), through LDS that nobody copies into
+// any more: the two waves that share rows add their sums, each wave half of
+// them, and the rows go through LDS once more, so that whole ones are stored side by
+// side (a lane's own values are 16 bytes of every one of its pieces: 1.7 us to store
+// them as they lie).
 template <int D, class S, int DT>
 __device__ inline void store_halves(const KvCache &c, const KvAttention &a, const S &scope, bool whole,
-                                    int slot, const Tile &tl, int head, int sub, int half,
+                                    int slot, const TileOf<typename S::Number> &tl, int head, int sub, int half,
                                     f32x16 (&o)[DT], float m, float sum, uint8_t *lds) {
-  constexpr int PITCH = D + 4, QUADS = D / 4;
-  static_assert(64 * (PITCH * 4 + 8) <= TileLds<D>::kBytes && 2 * 64 * (64 * DT + 8) <= TileLds<D>::kBytes,
+  constexpr int PITCH = D + 4, QUADS = D / 4, AT_ONCE = 256 / QUADS;
+  static_assert(64 * (PITCH * 4 + 8) <= TileLds<D>::kBytes && 4 * 64 * (32 * DT + 8) <= TileLds<D>::kBytes,
                 "both have room in the stages");
   const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
-  f32x4 *own = reinterpret_cast<f32x4 *>(lds) + sub * (4 * DT * 64) + lane;
-  float2 *own_ml = reinterpret_cast<float2 *>(lds + 2 * 4 * DT * 64 * 16) + sub * 64 + lane;
+  // what a wave gives to the other one, [wave][..][lane]
+  f32x4 *given = reinterpret_cast<f32x4 *>(lds) + lane;
+  float2 *given_ml = reinterpret_cast<float2 *>(lds + 4 * 2 * DT * 64 * 16) + lane;
   float *rows = reinterpret_cast<float *>(lds);
   float2 *rows_ml = reinterpret_cast<float2 *>(rows + 64 * PITCH);
+  const int mine = 2 * half + sub, its = 2 * (1 - half) + sub;
   __syncthreads();
-  if (half == 1) {
+  // elements 8 half .. 8 half + 7 of every tile are the wave's own
+  auto give = [&](auto from) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        own[64 * (4 * t + i)] = f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-    *own_ml = make_float2(m, sum);
-  }
+      for (int i = 0; i < 2; ++i) {
+        constexpr int E = decltype(from)::value;
+        given[((mine * DT + t) * 2 + i) * 64] =
+            f32x4{o[t][E + 4 * i], o[t][E + 4 * i + 1], o[t][E + 4 * i + 2], o[t][E + 4 * i + 3]};
+      }
+  };
+  if (half) give(std::integral_constant<int, 0>());
+  else give(std::integral_constant<int, 8>());
+  given_ml[mine * 64] = make_float2(m, sum);
   __syncthreads();
-  if (half == 0) {
-    const float2 other = *own_ml;
-    const float top = fmaxf(m, other.x);
-    const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
-    const float f1 = other.x == -INFINITY ? 0.0f : exp2_fast(other.x - top);
-    m = top;
-    sum = sum * f0 + other.y * f1;
+  const float2 other = given_ml[its * 64];
+  const float top = fmaxf(m, other.x);
+  const float f0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+  const float f1 = other.x == -INFINITY ? 0.0f : exp2_fast(other.x - top);
+  sum = sum * f0 + other.y * f1;
+  float y[DT][8];
+  auto add = [&](auto from) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 x = own[64 * (4 * t + i)];
+      for (int i = 0; i < 2; ++i) {
+        const f32x4 x = given[((its * DT + t) * 2 + i) * 64];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][4 * i + e] = o[t][4 * i + e] * f0 + x[e] * f1;
+        for (int e = 0; e < 4; ++e)
+          y[t][4 * i + e] = o[t][decltype(from)::value + 4 * i + e] * f0 + x[e] * f1;
       }
-  }
+  };
+  if (half) add(std::integral_constant<int, 8>());
+  else add(std::integral_constant<int, 0>());
   __syncthreads();
-  if (half == 0) {
-    // element 4a + e of tile t is value DT (8a + 4h + e) + t
-    float *to = rows + (32 * sub + col) * PITCH + h * 4 * DT;
+  // element 4a + e of tile t is value DT (8a + 4h + e) + t
+  float *to = rows + (32 * sub + col) * PITCH + (16 * half + 4 * h) * DT;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int x = 0; x < DT; ++x) {
-        f32x4 y;
+    for (int x = 0; x < DT; ++x) {
+      f32x4 z;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = o[(4 * x + e) % DT][4 * i + (4 * x + e) / DT];
-        *reinterpret_cast<f32x4 *>(to + i * 8 * DT + 4 * x) = y;
-      }
-    if (h == 0) rows_ml[32 * sub + col] = make_float2(m, sum);
-  }
+      for (int e = 0; e < 4; ++e) z[e] = y[(4 * x + e) % DT][4 * i + (4 * x + e) / DT];
+      *reinterpret_cast<f32x4 *>(to + i * 8 * DT + 4 * x) = z;
+    }
+  if (half == 0 && h == 0) rows_ml[32 * sub + col] = make_float2(top, sum);
   __syncthreads();
-  const int count = (int)min(64u, tl.rows - tl.r0);
-  for (int u = threadIdx.x; u < count * QUADS; u += 256) {
-    const int cc = u / QUADS, d = u % QUADS * 4;
+  const int count = (int)min(64u, tl.rows - tl.r0), d = threadIdx.x % QUADS * 4;
+  // row r0 + cc among all rows and heads: its token, counted from the tile's first one, by a
+  // product that is exact for r under 2^21
+  const uint32_t from = tl.r0 % tl.group;
+  const uint32_t first = (uint32_t)((tl.row0 + tl.r0 / tl.group) * a.heads) + head * tl.group;
+  const float inverse = 1.0f / (float)tl.group;
+  auto place_of = [&](int cc) {
+    const uint32_t r = from + cc, tok = (uint32_t)(((float)r + 0.5f) * inverse);
+    return first + tok * ((uint32_t)a.heads - tl.group) + r;
+  };
+  if (whole) {
+    for (int cc = threadIdx.x / QUADS; cc < count; cc += AT_ONCE) {
+      const float2 ml = rows_ml[cc];
+      store_sums(c, a, place_of(cc), d, *reinterpret_cast<const f32x4 *>(rows + cc * PITCH + d), ml.x, ml.y);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 64 / AT_ONCE; ++i) {
+    const int cc = i * AT_ONCE + threadIdx.x / QUADS;
     const f32x4 x = *reinterpret_cast<const f32x4 *>(rows + cc * PITCH + d);
     const float2 ml = rows_ml[cc];
-    const int64_t at = tl.row_head(a, head, tl.r0 + cc);
-    if (whole) {
-      store_sums(c, a, at, d, x, ml.x, ml.y);
-    } else {
-      *reinterpret_cast<f32x4 *>(scope.sums(a.ws, slot, at, D) + d) = x;
+    const uint32_t at = place_of(cc);
+    if (cc < count) {
+      *scope.sums(a.ws, slot, at, D, d) = x;
       if (d == 0) *scope.ml(a.ws, slot, at, D) = ml;
     }
   }
@@ -813,9 +871,10 @@ __device__ inline void store_halves(const KvCache &c, const KvAttention &a, cons
 // last 32 keys of every step and meet in LDS at the end.
 template <int D, int G, int H, class S>
 __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch &b,
-                                 const KvAttention &a, uint32_t tiles, int max_splits,
-                                 int split_steps, const S &scope, uint32_t w,
-                                 uint8_t *all_lds) {
+                                 const KvAttention &a, typename S::Number seqs, uint32_t tiles,
+                                 typename S::Number max_splits, int split_steps, const S &scope,
+                                 uint32_t w, uint8_t *all_lds) {
+  using Tile = TileOf<typename S::Number>;
   using L = TileLds<D>;
   constexpr int DT = D / 32;   // tiles of 32 values
   constexpr int CH = D / 16;   // 16-byte pieces of a key
@@ -829,11 +888,10 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   const int col = lane & 31, h = lane >> 5;
   // heads first: a kv head's workgroups run on the same dies and find its keys
   // in their cache; the last rows, which see most, start first
-  const int head = w % (uint32_t)c.kv_heads;
-  w /= (uint32_t)c.kv_heads;
-  const int split = w % (uint32_t)max_splits;
-  w /= (uint32_t)max_splits;
-  const uint32_t seqs = Place<S, kTileKeys>::count(b, scope);
+  const int head = w % scope.heads(c);
+  w = w / scope.heads(c);
+  const int split = w % max_splits;
+  w = w / max_splits;
   const uint32_t seq = w % seqs;
   const uint32_t tile = tiles - 1 - w / seqs;
   const Place<S, kTileKeys> place(c, b, a, scope, seq, tile, kTileRows / H, split, max_splits, split_steps);
@@ -842,7 +900,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   if (tl.empty()) return;
   int at[2];
   if (S::kPrefix && !place.ahead())
-    tl.positions<kTileRows / H>(b, place.first, place.past, tl.guess<kTileRows / H>(b, place.first, place.past), at);
+    tl.template positions<kTileRows / H>(b, place.first, place.past, tl.template guess<kTileRows / H>(b, place.first, place.past), at);
   // the wave's rows: with two teams, waves w and w + 4 share a SIMD and hold
   // different halves of the tile
   const int sub = H == 2 ? wave & 1 : team == 0 ? wave : wave ^ 2;
@@ -858,7 +916,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   }
   const Steps<kTileKeys> steps = place.steps(tl, p_hi);
   const Range range = place.range(steps);
-  if (split >= range.splits) return;
+  if (range.none) return;
   const int begin = range.begin + team, mine_steps = range.end - range.begin;
   const int turns = (mine_steps + G - 1) / G;
   const int n = (mine_steps - team + G - 1) / G;
@@ -930,8 +988,8 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     to = to == lds0 + (kStages - 1) * L::kStage ? lds0 : to + L::kStage;
   };
 
-  Tile::Guesses guesses = {};
-  if (S::kPrefix && place.ahead()) guesses = tl.guess<kTileRows / H>(b, place.first, place.past);
+  typename Tile::Guesses guesses = {};
+  if (S::kPrefix && place.ahead()) guesses = tl.template guess<kTileRows / H>(b, place.first, place.past);
 
   // the element of key piece 2m + h that step 2m + e of the first product takes
   // is value 32m + 16h + 8e
@@ -1076,7 +1134,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   }
   if constexpr (S::kPrefix) {
     // (all of these loads are in flight together)
-    if (place.ahead()) tl.positions<kTileRows / H>(b, place.first, place.past, guesses, at);
+    if (place.ahead()) tl.template positions<kTileRows / H>(b, place.first, place.past, guesses, at);
     const int row_pos = Tile::position(at, tok - (int)(tl.r0 / tl.group));
     pos = mine ? row_pos : -1;
     w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
@@ -1179,27 +1237,30 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
                                                                       int max_splits,
                                                                       int split_steps) {
   __shared__ __align__(16) uint8_t lds[G * TileLds<D>::kBytes];
-  tile_part<D, G, 1, Whole>(c, layer, b, a, tiles, max_splits, split_steps, Whole{}, blockIdx.x, lds);
+  tile_part<D, G, 1, Whole>(c, layer, b, a, (uint32_t)b.seqs, tiles, max_splits, split_steps, Whole{}, blockIdx.x, lds);
 }
 
 // Shared first tokens: the first workgroups take the prefixes of all groups, the others
 // the suffixes of all sequences, in one launch: the former are bound by the vector
 // unit, the latter by memory.
 struct SharedPlan {
-  uint32_t prefix_grid, prefix_tiles, tiles;
-  int prefix_splits, splits, steps;  // steps of a suffix's part
+  uint32_t prefix_grid;
+  Divisor groups, prefix_tiles, prefix_splits;
+  Divisor seqs, tiles, splits;
+  int steps;  // of a suffix's part
 };
 
 // A workgroup's tile of ROWS rows: 16 or 64.
 template <int D, int ROWS, class S>
 __device__ inline void shared_part(const KvCache &c, int64_t layer, const KvBatch &b,
-                                   const KvAttention &a, uint32_t tiles, int splits, int steps,
-                                   const S &scope, uint32_t w, uint8_t *lds) {
+                                   const KvAttention &a, const Divisor &seqs, const Divisor &tiles,
+                                   const Divisor &splits, int steps, const S &scope, uint32_t w,
+                                   uint8_t *lds) {
   if constexpr (ROWS == 16)
     decode_part(c, layer, b, a, tiles, splits, steps, scope, w,
                 *reinterpret_cast<DecodeLds<D, 4> *>(lds));
   else
-    tile_part<D, 1, 2, S>(c, layer, b, a, tiles, splits, steps, scope, w, lds);
+    tile_part<D, 1, 2, S>(c, layer, b, a, seqs, tiles, splits, steps, scope, w, lds);
 }
 
 // What the kernel is called with.  It reads them where it takes its way, not at its
@@ -1223,13 +1284,14 @@ __global__ __launch_bounds__(256, 2) void shared_kernel(SharedArgs) {
   if (blockIdx.x < prefix_grid) {
     asm volatile("; a prefix");
     const SharedArgs x = *args;
-    shared_part<D, PREFIX_ROWS>(x.c, x.layer, x.b, x.a, x.p.prefix_tiles, x.p.prefix_splits, 0,
+    shared_part<D, PREFIX_ROWS>(x.c, x.layer, x.b, x.a, x.p.groups, x.p.prefix_tiles,
+                                x.p.prefix_splits, 0,
                                 Prefix{x.scope}, blockIdx.x, lds);
   } else {
     asm volatile("; a suffix");
     const SharedArgs x = *args;
-    shared_part<D, ROWS>(x.c, x.layer, x.b, x.a, x.p.tiles, x.p.splits, x.p.steps, Suffix{x.scope},
-                         blockIdx.x - prefix_grid, lds);
+    shared_part<D, ROWS>(x.c, x.layer, x.b, x.a, x.p.seqs, x.p.tiles, x.p.splits, x.p.steps,
+                         Suffix{x.scope}, blockIdx.x - prefix_grid, lds);
   }
 }
 
@@ -1268,7 +1330,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
     }
   };
   load(turn);
-  const Tile tl(c, b, a, b.raw(w / tiles), w % tiles, width);
+  const Tile tl(Whole::group(c, a), b, b.raw(w / tiles), w % tiles, width);
   if (tl.empty()) return;
   const Steps<N> steps(0, tl.p_lo, tl.last_key(tl.p_hi), a.window, a.sinks);
   if (steps.count <= split_steps) return;  // written already
@@ -1299,9 +1361,11 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
 // suffix: a workgroup takes `256 / (D / 4) / turns` rows and heads of a sequence, which lie
 // side by side in every slot.
 struct SharedJoin {
-  int splits, steps;  // the suffix's plan
-  int turns;
-  uint32_t per_seq;   // workgroups of a sequence
+  Divisor splits;     // the suffix's plan
+  int steps;
+  int turns;          // a power of two
+  Divisor per_seq;    // workgroups of a sequence
+  Divisor heads;
 };
 
 template <int D, int N>
@@ -1310,9 +1374,10 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   constexpr int QUADS = D / 4;
   __shared__ f32x4 xs[256];
   __shared__ float2 mls[256];
-  const int d = (threadIdx.x % QUADS) * 4, t = threadIdx.x / QUADS, turn = t % j.turns;
+  const int d = (threadIdx.x % QUADS) * 4, t = threadIdx.x / QUADS, turn = t & (j.turns - 1);
+  const int turn_bits = __builtin_ctz(j.turns), row = t >> turn_bits;
   const int64_t seq = blockIdx.x / j.per_seq;
-  const uint32_t first_row_head = (blockIdx.x % j.per_seq) * (256 / QUADS / j.turns);
+  const uint32_t first_row_head = (blockIdx.x % j.per_seq) * (256 / QUADS >> turn_bits);
   const KvBatch::Raw raw = b.raw(seq);
   int first = 0;
   const int shared = scope.g.shared_of(b, seq, &first);
@@ -1321,15 +1386,15 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
   b.sequence(raw, row0, n, len, end);
   const int rows = n < b.max_rows ? n : b.max_rows;
   if (first_row_head >= (uint32_t)rows * a.heads) return;
-  const uint32_t i = first_row_head + t / j.turns;
+  const uint32_t i = first_row_head + row;
   const bool on = i < (uint32_t)rows * a.heads;
-  const int tok = on && b.max_rows > 1 ? (int)(i / a.heads) : 0;
+  const int tok = on && b.max_rows > 1 ? (int)(i / j.heads) : 0;
   int splits = 1;
   if (j.splits > 1) {
     // the steps of the tile that the row is in
     constexpr int WIDTH = N == 32 ? 16 : 64;
-    const uint32_t group_heads = (uint32_t)a.heads / (uint32_t)c.kv_heads;
-    const uint32_t r = tok * group_heads + (i % a.heads) % group_heads, r0 = r / WIDTH * WIDTH;
+    const Divisor &group_heads = scope.heads_each;
+    const uint32_t r = tok * group_heads + (i % j.heads) % group_heads, r0 = r / WIDTH * WIDTH;
     const uint32_t r1 = min(r0 + WIDTH, (uint32_t)rows * group_heads) - 1;
     const int begin = len - n, p_lo = begin + (int)(r0 / group_heads), p_hi = begin + (int)(r1 / group_heads);
     const Steps<N> steps(shared / N, p_lo, min(p_hi, end - 1), a.window, a.sinks);
@@ -1342,7 +1407,7 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
     const int64_t at = row0 + tok - b.first_row(first);  // the row among its group's
     if (at < 0 || at >= scope.g.max_rows) shared_parts = 0;
   }
-  const int64_t row_head = row0 * a.heads + (on ? i : 0);
+  const uint32_t row_head = (uint32_t)row0 * a.heads + (on ? i : 0);
   const int parts = on && !written ? shared_parts + splits : 0;
   float mm = -INFINITY, ll = 0.0f;
   f32x4 x = {0, 0, 0, 0};
@@ -1354,11 +1419,23 @@ __global__ __launch_bounds__(256) void join_shared_kernel(KvCache c, KvBatch b, 
       int s = min(s0 + u * j.turns, parts - 1);
       if (s >= shared_parts) s += scope.prefix_slots - shared_parts;
       ml[u] = *scope.ml(a.ws, s, row_head, D);
-      y[u] = *reinterpret_cast<const f32x4 *>(scope.sums(a.ws, s, row_head, D) + d);
+      y[u] = *scope.sums(a.ws, s, row_head, D, d);
     }
+    // all eight to the largest m of theirs and of those before
+    float top = mm;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, ml[u].x);  // (past the last part: the last one)
+    const float f = mm == -INFINITY ? 0.0f : exp2_fast(mm - top);
+    ll *= f;
+    x *= f;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (s0 + u * j.turns < parts) join(mm, ll, x, ml[u].x, ml[u].y, y[u]);
+      if (s0 + u * j.turns < parts && ml[u].x != -INFINITY) {
+        const float g = exp2_fast(ml[u].x - top);
+        ll += ml[u].y * g;
+        x += y[u] * g;
+      }
+    mm = top;
   }
   if (j.turns > 1) {
     // every turn scales its own sums to the largest m, then they are added
@@ -1652,9 +1729,11 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
   const SharedPlans plans = shared_plans(c, b, g, a.heads, a.window, a.sinks);
   if (!plans.apart) return launch_kv_attention(c, layer, b, a, s);
   const Plan &p = plans.prefix, &own = plans.own;
-  const Shared scope{g, b.rows * a.heads, (int)p.splits, (int)(p.splits + own.splits)};
-  const SharedPlan plan{(uint32_t)(p.items * p.splits), (uint32_t)p.tiles, (uint32_t)own.tiles,
-                        (int)p.splits, (int)own.splits, own.split_steps};
+  const Shared scope{g, (uint32_t)(b.rows * a.heads), (int)p.splits, (int)(p.splits + own.splits),
+                     Divisor::of(c.kv_heads), Divisor::of(a.heads / c.kv_heads)};
+  const SharedPlan plan{(uint32_t)(p.items * p.splits), Divisor::of(g.groups), Divisor::of(p.tiles),
+                        Divisor::of(p.splits), Divisor::of(b.seqs), Divisor::of(own.tiles),
+                        Divisor::of(own.splits), own.split_steps};
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.items * p.splits + own.items * own.splits)), dim3(256),
                        0, s, SharedArgs{c, layer, b, a, scope, plan});
@@ -1669,7 +1748,8 @@ hipError_t launch_kv_attention_shared(const KvCache &c, int64_t layer, const KvB
   else pick(std::integral_constant<int, 64>());
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const SharedJoin j{(int)own.splits, own.split_steps, plans.turns, (uint32_t)plans.per_seq};
+  const SharedJoin j{Divisor::of(own.splits), own.split_steps, plans.turns, Divisor::of(plans.per_seq),
+                     Divisor::of(a.heads)};
   auto join = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(b.seqs * plans.per_seq)), dim3(256), 0, s, c, b, a, scope, j);
   };
