@@ -381,21 +381,37 @@ def nf4_kv_append(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, 
 
 
 _kinds = None  # the tensors' types, by NF4_KV_*
+_int32_kind = None
+
+
+def _bind_torch() -> None:
+    """What the entries below ask torch for in every call, looked up once: of a call of
+    some 6 us each lookup is 0.1 us."""
+    global _kinds, _int32_kind, _current_device, _raw_stream
+    import torch
+    _current_device = torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream_of
+    _int32_kind = torch.int32
+    _kinds = {NF4_KV_BF16: torch.bfloat16, NF4_KV_F32: torch.float32}
+
+
+def _stream_of(gpu: int) -> int:
+    import torch
+    return torch.cuda.current_stream(gpu).cuda_stream
 
 
 def _operands(where: str, gpu: int, type: int, *tensors) -> None:
     """Tensors (None and addresses are left out) lie on that GPU and hold what `type`
     says: the kernels take them as they are told to."""
-    global _kinds
     if _kinds is None:
-        import torch
-        _kinds = {NF4_KV_BF16: torch.bfloat16, NF4_KV_F32: torch.float32}
+        _bind_torch()
+    kind = _kinds.get(type)
     for t in tensors:
         if t is None or t.__class__ is int:
             continue
         if t.get_device() != gpu:
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on one GPU")
-        if t.dtype is not _kinds.get(type):
+        if t.dtype is not kind:
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: a tensor of another type")
 
 
@@ -403,12 +419,16 @@ def _stream_on(where: str, gpu: int, stream) -> int | None:
     """The stream's handle.  The current one, and a Stream object, have to be of the
     tensors' GPU: a launch on another GPU's would take their addresses as its own."""
     if stream is None:
-        import torch
-        if torch.cuda.current_device() != gpu:
+        if _kinds is None:
+            _bind_torch()
+        if _current_device() != gpu:
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on the current GPU")
-    elif stream.__class__ is not int and stream.device.index != gpu:
+        return _raw_stream(gpu)
+    if stream.__class__ is int:
+        return stream
+    if stream.device.index != gpu:
         raise NF4Error(NF4_ERR_SHAPE, f"{where}: a stream of another GPU")
-    return _stream(stream)
+    return stream.cuda_stream
 
 
 def nf4_kv_read(cache, layer: int, batch, k, k_stride: int, v, v_stride: int, type: int,
@@ -445,15 +465,19 @@ def nf4_rotate(rotary, x, x_stride: int, x_type: int, positions, rows: int, head
         stream = _stream(stream)
     else:
         gpu = x.get_device()
-        _on_gpu("nf4_rotate", gpu)
+        if gpu < 0:
+            raise NF4Error(NF4_ERR_SHAPE, "nf4_rotate: tensors that are not on one GPU")
         _operands("nf4_rotate", gpu, x_type, x)
         _operands("nf4_rotate", gpu, y_type, y)
-        _operands("nf4_rotate", gpu, NF4_KV_F32, weight)
-        if positions.__class__ is not int and positions is not None:
-            _on_gpu("nf4_rotate", gpu, _int32(positions).get_device())
-            if positions.numel() < rows:
-                raise NF4Error(NF4_ERR_SHAPE, "nf4_rotate: fewer positions than rows")
+        if weight is not None:
+            _operands("nf4_rotate", gpu, NF4_KV_F32, weight)
         stream = _stream_on("nf4_rotate", gpu, stream)
+        if positions.__class__ is not int and positions is not None:
+            if positions.get_device() != gpu:
+                raise NF4Error(NF4_ERR_SHAPE, "nf4_rotate: tensors that are not on one GPU")
+            if positions.dtype is not _int32_kind or not positions.is_contiguous() or \
+                    positions.numel() < rows:
+                raise NF4Error(NF4_ERR_SHAPE, "nf4_rotate: positions are int32, one for each row")
     _check(lib().nf4_rotate(rotary.arg, _ptr(x), x_stride, x_type, _ptr(positions), rows, heads,
                             head_dim, _ptr(weight), eps, _ptr(y), y_stride, y_type, stream),
            "nf4_rotate")

@@ -440,6 +440,6 @@ def test_read_gives_back_what_was_appended(side):
 def test_rotate_refuses_fewer_positions_than_rows(side):
     t, nf4 = side.torch, side.nf4
     x, r = t.zeros(5, 128, device="cuda"), nf4.Rotary(64)
-    with pytest.raises(nf4.NF4Error, match="fewer positions"):
+    with pytest.raises(nf4.NF4Error, match="one for each row"):
         nf4.nf4_rotate(r, x, 128, nf4.NF4_KV_F32, i32(side, range(4)), 5, 2, 64, None, 0.0, x, 128,
                        nf4.NF4_KV_F32)

@@ -269,9 +269,9 @@ def test_streams_of_another_gpu_are_refused(monkeypatch):
     class Stream:
         def __init__(self, index):
             self.device, self.cuda_stream = torch.device(f"cuda:{index}"), 0x50 + index
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    monkeypatch.setattr(nf4, "_stream",
-                        lambda s: 0x77 if s is None else s if isinstance(s, int) else s.cuda_stream)
+    monkeypatch.setattr(nf4, "_kinds", {})
+    monkeypatch.setattr(nf4, "_current_device", lambda: 1, raising=False)
+    monkeypatch.setattr(nf4, "_raw_stream", lambda gpu: 0x76 + gpu, raising=False)
     assert nf4._stream_on("f", 1, None) == 0x77
     assert nf4._stream_on("f", 0, 0x60) == 0x60
     assert nf4._stream_on("f", 2, Stream(2)) == 0x52
