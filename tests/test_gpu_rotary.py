@@ -443,3 +443,29 @@ def test_rotate_refuses_fewer_positions_than_rows(side):
     with pytest.raises(nf4.NF4Error, match="one for each row"):
         nf4.nf4_rotate(r, x, 128, nf4.NF4_KV_F32, i32(side, range(4)), 5, 2, 64, None, 0.0, x, 128,
                        nf4.NF4_KV_F32)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_large_rows_leave_their_neighbours_alone(side, dim):
+    """A row whose squares pass 32 bits is normed in 64; the rows beside it are not."""
+    t, nf4 = side.torch, side.nf4
+    rng = np.random.default_rng(41)
+    heads, rows = 5, 19
+    x = side.to_dev(rng.normal(size=(rows, heads * dim)).astype(np.float32))
+    y = x.clone()
+    y[3, dim:2 * dim] *= 2.0 ** 90
+    y[12] *= 2.0 ** 70
+    w = side.to_dev((1 + 0.3 * rng.normal(size=dim)).astype(np.float32))
+    out = []
+    for z in (x, y):
+        out.append(t.zeros(rows, heads * dim, dtype=t.bfloat16, device="cuda"))
+        nf4.nf4_rotate(nf4.Rotary(dim), z, heads * dim, nf4.NF4_KV_F32, i32(side, range(rows)), rows, heads, dim,
+                       w, EPS, out[-1], heads * dim, nf4.NF4_KV_BF16)
+    t.cuda.synchronize()
+    same = (out[0] == out[1]).reshape(rows, heads, dim).all(-1)
+    for r in range(rows):
+        for h in range(heads):
+            if not (r == 12 or (r == 3 and h == 1)):
+                assert bool(same[r, h]), (r, h)
+    # scaled by a power of two, and eps far below both: the same up to the roundings
+    assert float((out[0].float() - out[1].float()).abs().max()) <= float(out[0].float().abs().max()) * 2.0 ** -7
