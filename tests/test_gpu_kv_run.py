@@ -153,3 +153,84 @@ def test_prompt_branches_and_steps(side, dim, dims, layout, heads, kvh, branches
                     off = np.abs(got[b, head].astype(np.float64) - w[b, head])
                     assert (off <= np.abs(w[b, head]) * 2.0 ** -4 + half).all()
     assert int(missing) == 0
+
+
+def branches_of(side, cache, pages, seqs, width, n, seed):
+    """`seqs` sequences over the same n tokens in the given pages, one more token in a page
+    of its own each: the batch, its groups and what one step appends."""
+    t, nf4 = side.torch, side.nf4
+    page, kvh, dim = cache.struct.page_tokens, cache.struct.kv_heads, cache.struct.head_dim
+    table = np.full((seqs, width), -1, np.int32)
+    table[:, :n // page] = pages[:n // page]
+    table[:, n // page] = pages[n // page:n // page + seqs]
+    g = t.Generator(device="cuda").manual_seed(seed)
+    rows = lambda r, h: t.randn(r, (h + 2 * kvh) * dim, generator=g, device="cuda")  # noqa: E731
+    first, one = rows(n, 0), rows(seqs, 4 * kvh)
+    b = nf4.KVBatch(i32(side, [n]), i32(side, table[:1]), row_start=i32(side, [0, n]), rows=n, max_rows=n, max_len=n)
+    nf4.nf4_kv_append(cache, 0, b, first, 2 * kvh * dim, first[:, kvh * dim:], 2 * kvh * dim, nf4.NF4_KV_F32)
+    return (nf4.KVBatch(i32(side, [n + 1] * seqs), i32(side, table), max_len=1 << 30),
+            nf4.KVGroups(i32(side, [n]), max_rows=seqs), one)
+
+
+def step(side, cache, b, g, x, ws, out, stream=None):
+    """Appends a token to each sequence, attends and reads the new rows back."""
+    nf4, (seqs, width) = side.nf4, x.shape
+    kvh, dim = cache.struct.kv_heads, cache.struct.head_dim
+    h, kv_at = 4 * kvh, 4 * kvh * dim
+    q, o, z, k, v = out
+    nf4.nf4_kv_append_rotated(cache, 0, b, nf4.Rotary(dim), x, width, h, None, x[:, kv_at:], width, None,
+                              x[:, kv_at + kvh * dim:], width, nf4.NF4_KV_F32, 0.0, q, stream=stream)
+    nf4.nf4_kv_attention_shared(cache, 0, b, g, q, h * dim, h, 0.1, 0, 0, o, z, ws, ws.numel(), stream=stream)
+    nf4.nf4_kv_read(cache, 0, b, k, kvh * dim, v, kvh * dim, nf4.NF4_KV_F32, stream=stream)
+
+
+def outputs(side, cache, seqs):
+    t, kvh, dim = side.torch, cache.struct.kv_heads, cache.struct.head_dim
+    full = lambda w, d: t.full((seqs, w), 7.0, dtype=d, device="cuda")  # noqa: E731
+    return (full(4 * kvh * dim, t.bfloat16), full(4 * kvh * dim, t.bfloat16), full(4 * kvh, t.float32),
+            full(kvh * dim, t.float32), full(kvh * dim, t.float32))
+
+
+def test_pages_past_32_bits(side):
+    """The last pages of a cache whose codes pass 2^32 bytes: what the first pages give."""
+    t, nf4 = side.torch, side.nf4
+    pages, page, kvh, dim, seqs, n = 17000, 256, 8, 128, 20, 512
+    cache = nf4.KVCache(1, pages, kvh, page, dim)
+    assert cache.k.numel() > 1 << 32
+    width = SAVED // ((seqs - 2) * kvh * 2 * dim) // page + 2
+    res = []
+    for at in (0, pages - 2 - seqs):
+        b, g, x = branches_of(side, cache, at + np.arange(2 + seqs), seqs, width, n, 3)
+        need = nf4.nf4_kv_attention_shared_workspace_bytes(cache, b, g, 4 * kvh)
+        assert need != nf4.nf4_kv_attention_workspace_bytes(cache, b, 4 * kvh), "not taken apart"
+        ws = t.full((need,), 0xFF, dtype=t.uint8, device="cuda")
+        res.append(outputs(side, cache, seqs))
+        step(side, cache, b, g, x, ws, res[-1])
+        t.cuda.synchronize()
+    for a, b in zip(*res):
+        assert t.equal(a, b) and not bool((a == 7).all(-1).any())
+
+
+def test_two_at_once(side):
+    """Two runs on two streams, each with its own cache, workspace and outputs."""
+    t, nf4 = side.torch, side.nf4
+    runs = []
+    for seed, (dim, kvh, seqs) in ((4, (128, 2, 40)), (5, (64, 4, 24))):
+        cache = nf4.KVCache(1, 200, kvh, 16, dim)
+        width = SAVED // ((seqs - 3) * kvh * 2 * dim) // 16 + 2
+        b, g, x = branches_of(side, cache, np.arange(200), seqs, width, 960, seed)
+        need = nf4.nf4_kv_attention_shared_workspace_bytes(cache, b, g, 4 * kvh)
+        assert need != nf4.nf4_kv_attention_workspace_bytes(cache, b, 4 * kvh), "not taken apart"
+        want = outputs(side, cache, seqs)
+        ws = t.empty(need, dtype=t.uint8, device="cuda")
+        step(side, cache, b, g, x, ws, want)
+        runs.append((cache, b, g, x, ws, want, outputs(side, cache, seqs), t.cuda.Stream()))
+    t.cuda.synchronize()
+    for _ in range(10):
+        for cache, b, g, x, ws, _, got, stream in runs:
+            step(side, cache, b, g, x, ws, got, stream)
+        t.cuda.synchronize()
+        for *_, want, got, _ in runs:
+            assert all(t.equal(a, b) for a, b in zip(want, got))
+            for a in got:
+                a.fill_(7.0)
