@@ -1242,7 +1242,22 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 
 // Shared first tokens: the first workgroups take the prefixes of all groups, the others
 // the suffixes of all sequences, in one launch: the former are bound by the vector
-// unit, the latter by memory.
+// unit, the latter by memory.  A group's rows of a kv head (sequences x rows x query heads
+// to each) are the columns of one product, in tiles of 64 rows or 16, so that shared keys
+// are read and widened once for all of them; a row's parts of the prefix and its
+// sequence's suffix, each (m, l, sum), meet in join_shared_kernel by
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum x_i 2^(m_i - m) / l.
+// Tiles of 64 round the weights to bf16 as the tile kernel does (two terms would double the
+// second product, which is bound by its instructions), those of 16 to two terms.
+//
+// 64 sequences of up to 2000 tokens past 4096 shared ones, 32 heads over 8 of 128 (145 MB):
+// 36.9 us in a trace, 3.9 TB/s; 512 of its 608 workgroups run at a time (registers), the rest
+// start where the prefixes' end, after some 15 us.  Short calls are bound by chains that
+// nothing hides: 8 sequences past 14449, 28 heads over 4 (16 MB), 13.7 us, of a prefix's
+// workgroup some 1.5 for arguments and groups, 2 to the first page ids, 2 to the first keys,
+// 0.6 for each step of its keys (widening, products and softmax of one wave per SIMD), 2.5 for
+// the halves' meeting and the store.  As two launches, prefixes then suffixes, the four
+// cases took 2 to 8 us more.
 struct SharedPlan {
   uint32_t prefix_grid;
   Divisor groups, prefix_tiles, prefix_splits;
@@ -1359,7 +1374,10 @@ __global__ __launch_bounds__(256) void join_kernel(KvCache c, KvBatch b, KvAtten
 
 // The same for rows whose keys are those of a shared prefix and of the sequence's own
 // suffix: a workgroup takes `256 / (D / 4) / turns` rows and heads of a sequence, which lie
-// side by side in every slot.
+// side by side in every slot.  Bound by its chain: arguments and groups 1 us, the parts, which
+// other dies have written, 2, the turns' meeting 1; 4.0 to 5.1 us in traces.  The first
+// parts read beside the groups, from where the rows most likely are, took longer
+// (beams over 14449 tokens 17.1 us against 16.8 as a whole), by the instructions it added.
 struct SharedJoin {
   Divisor splits;     // the suffix's plan
   int steps;
