@@ -1252,12 +1252,11 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 //
 // 64 sequences of up to 2000 tokens past 4096 shared ones, 32 heads over 8 of 128 (145 MB):
 // 36.9 us in a trace, 3.9 TB/s; 512 of its 608 workgroups run at a time (registers), the rest
-// start where the prefixes' end, after some 15 us.  Short calls are bound by chains that
-// nothing hides: 8 sequences past 14449, 28 heads over 4 (16 MB), 13.7 us, of a prefix's
-// workgroup some 1.5 for arguments and groups, 2 to the first page ids, 2 to the first keys,
-// 0.6 for each step of its keys (widening, products and softmax of one wave per SIMD), 2.5 for
-// the halves' meeting and the store.  As two launches, prefixes then suffixes, the four
-// cases took 2 to 8 us more.
+// start where short suffixes end, after some 15 us.  Short calls are bound by chains that
+// nothing hides: 8 sequences past 14449, 28 heads over 4 (16 MB), a prefix's workgroup takes
+// 9.6 us, 3.6 of them to its first step (arguments, groups, page ids and positions, trips to
+// memory one after the other), 1.1 for its first keys, 1 for each of four steps, which is
+// 3.9 TB/s by all of them, and 1.9 for the halves' meeting and the store.
 struct SharedPlan {
   uint32_t prefix_grid;
   Divisor groups, prefix_tiles, prefix_splits;
