@@ -1597,7 +1597,12 @@ Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
 // 14449, of 4 18.7, of 7 19.7), and more, up to 24, where that is more workgroups than
 // run at a time, the suffixes' among them (23 sequences of three rows over 10477, two
 // groups, of 16 34.9, of 12 41.5; 64 of up to 2000 tokens past 4096, which are as many as
-// run at a time by themselves, of 24 46.0, of 16 48.2, of 12 53.9).
+// run at a time by themselves, of 24 46.0, of 16 48.2, of 12 53.9, of 32 46.7 against 44.3).
+// Suffixes end early where they are short, and count by their length (19 sequences of five
+// rows, 28 heads over 4, whose suffixes are tiles of 64 rows, over 12000 and up to 100 tokens
+// 41.0, counted whole 44.7; over 6498 and up to 1331 41.9, counted whole 35.5).  Beside those, prefixes of 128 values take up to
+// 32 steps (48 of five rows over 12000, three groups, 28 heads over 4, 69.4, with 24 73.2), of
+// 64 values 24 (32 heads over 4, 50.0, with 32 55.0).
 // Tiles of 16 rows: 43 over 9451, 5 groups, 16 heads over 8 of 64, in parts of 24
 // steps 23.6, of 16 26.6.  A window's rows may stand anywhere: as many steps as it is long
 // are counted.
@@ -1620,9 +1625,10 @@ Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
   } else {
     per = std::min<int64_t>(std::max<int64_t>(p.items * steps * 5 / (4 * cus), 2), 12);
     const int64_t slots = (c.head_dim == 128 ? 2 : 3) * cus;
-    const int64_t taken = own.items * own.splits * std::min<int64_t>(own.split_steps * own.keys, 1024) / 1024;
+    const int64_t whole = own.few ? 1024 : 512;  // keys of a suffix that stays as long as prefixes
+    const int64_t taken = own.items * own.splits * std::min<int64_t>(own.split_steps * own.keys, whole) / whole;
     const int64_t room = std::max<int64_t>((slots - taken) / p.items, 1);
-    per = std::max<int64_t>(per, std::min<int64_t>((steps + room - 1) / room, 24));
+    per = std::max<int64_t>(per, std::min<int64_t>((steps + room - 1) / room, !own.few && c.head_dim == 128 ? 32 : 24));
   }
   per = std::max<int64_t>(per, (steps + kMaxSplits - 1) / kMaxSplits);
   p.splits = (steps + per - 1) / per;
