@@ -1603,8 +1603,11 @@ Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
 // 41.0, counted whole 44.7; over 6498 and up to 1331 41.9, counted whole 35.5).  Beside those, prefixes of 128 values take up to
 // 32 steps (48 of five rows over 12000, three groups, 28 heads over 4, 69.4, with 24 73.2), of
 // 64 values 24 (32 heads over 4, 50.0, with 32 55.0).
-// Tiles of 16 rows: 43 over 9451, 5 groups, 16 heads over 8 of 64, in parts of 24
-// steps 23.6, of 16 26.6.  A window's rows may stand anywhere: as many steps as it is long
+// Tiles of 16 rows: some 200 workgroups, of 16 to 40 steps of 32 keys (8 sequences over 20000,
+// 16 heads over 8, in parts of 24 17.7, of 16 19.7, of 40 18.9; 8 over 32000, 8 heads, of 40
+// 20.3, of 16 23.0, of 64 22.9; 16 over 3000, 16 heads over 8, of 16 13.9, of 24 15.4), and
+// more where that is three for every compute unit (32 over 9000, 8 groups, 32 heads over 8, of
+// 40 37.1, of 24 41.7).  A window's rows may stand anywhere: as many steps as it is long
 // are counted.
 Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int heads, int window,
                  const Plan &own) {
@@ -1621,7 +1624,8 @@ Plan prefix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
   if (window > 0) steps = std::min<int64_t>(steps, window / p.keys + 2);
   int64_t per;
   if (p.few) {
-    per = std::max<int64_t>(p.items * steps / (3 * cus), kMinSteps);
+    per = std::min<int64_t>(std::max<int64_t>(p.items * steps * 5 / (4 * cus), kMinSteps), 40);
+    per = std::max<int64_t>(per, p.items * steps / (3 * cus));
   } else {
     per = std::min<int64_t>(std::max<int64_t>(p.items * steps * 5 / (4 * cus), 2), 12);
     const int64_t slots = (c.head_dim == 128 ? 2 : 3) * cus;
