@@ -37,8 +37,9 @@ def near(got, want, mag, normed, bf):
     # values that do not turn keep their bits without a norm, and 4 roundings with one
     turns = mag > 0
     bound = np.where(turns, (8 if normed else 4) * U * mag, 4 * U * np.abs(want) if normed else 0.0)
-    bound = bound + (np.abs(want) + bound) * (2.0 ** -8 if bf else 0.0) + 2.0 ** -148
-    bad = fine & (np.abs(got - want) > bound)
+    with np.errstate(invalid="ignore"):  # infinities, which are not `fine`
+        bound = bound + (np.abs(want) + bound) * (2.0 ** -8 if bf else 0.0) + 2.0 ** -148
+        bad = fine & (np.abs(got - want) > bound)
     assert not bad.any(), f"{bad.sum()} off, first at {np.argwhere(bad)[0]}: " \
         f"{got[bad][0]} for {want[bad][0]}, bound {bound[bad][0]}"
 
