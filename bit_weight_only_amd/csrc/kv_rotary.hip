@@ -202,13 +202,61 @@ __device__ inline void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Where in a wave's row of LDS a lane finds the other values of its pairs, where these start
+// anywhere (an odd number of pairs, or one that pieces end inside of): a place is left
+// free after every eight values, so that lanes find theirs in different banks.  For eight values
+// (bf16) the places are byte offsets, two in a register: worked out for every row they are a
+// fifth of its instructions (the append of 5 times 701 rows, 32 heads over 8 of 64: 16.7 us,
+// kept 14.9).  For four (fp32) they are worked out there, since the kernel has no registers left
+// to keep them (14449 rows of 28 heads over 4 78.3 us, kept 90.5).
+template <class T, int VEC>
+struct Others {
+  static constexpr bool KEPT = VEC == 8;
+  uint32_t at[KEPT ? VEC / 2 : 1];
+  __device__ static int place(int value) { return value + value / 8; }
+  __device__ static int other(const KvRotary &rot, int v) {
+    const int half = rot.dims / 2;
+    return place(v >= rot.dims ? v : v < half ? v + half : v - half);
+  }
+  // Whether a lane's values have theirs at places of their own.
+  __device__ static bool apart(const KvRotary &rot) { return rot.dims / 2 % VEC != 0; }
+  __device__ Others(const KvRotary &rot, int piece) {
+    if (!KEPT || rot.pairs || !apart(rot)) return;
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2)
+      at[KEPT ? e / 2 : 0] = (uint32_t)(other(rot, piece * VEC + e) * sizeof(T)) |
+                             (uint32_t)(other(rot, piece * VEC + e + 1) * sizeof(T)) << 16;
+  }
+  // Through the row: x the lane's values, from value `first` on, y the others.
+  __device__ void exchange(const KvRotary &rot, T *row, int first, const T (&x)[VEC], T (&y)[VEC]) const {
+    // (the compiler is not to keep places from row to row: registers)
+    if (!KEPT) asm volatile("" : "+v"(first));
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) row[place(first) + e] = x[e];
+    wave_sync();
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      if constexpr (KEPT) {
+        uint32_t both = at[e / 2];
+        asm volatile("" : "+v"(both));
+        const uint8_t *bytes = reinterpret_cast<const uint8_t *>(row);
+        y[e] = *reinterpret_cast<const T *>(bytes + (both & 0xFFFFu));
+        y[e + 1] = *reinterpret_cast<const T *>(bytes + (both >> 16));
+      } else {
+        y[e] = row[other(rot, first + e)];
+        y[e + 1] = row[other(rot, first + e + 1)];
+      }
+    }
+  }
+};
+
 // Norms (weight w) and turns one token's values of one row: `v` are the lane's, from
 // value VEC * piece on; `r` the token's row of the table; `row` the row in LDS for this
 // lane's token.  All lanes of the wave come here together.
 template <class T, int D, int VEC, class Lds>
 __device__ inline void turn_row(const Lds &lds, T *row, const KvRotary &rot,
-                                const float (&w)[VEC], bool norm, double eps, int r, int piece,
-                                float (&v)[VEC]) {
+                                const Others<T, VEC> &others, const float (&w)[VEC], bool norm,
+                                double eps, int r, int piece, float (&v)[VEC]) {
   constexpr bool LOW = sizeof(T) == 8;
   T x[VEC];
 #pragma unroll
@@ -233,24 +281,12 @@ __device__ inline void turn_row(const Lds &lds, T *row, const KvRotary &rot,
 #pragma unroll
       for (int e = 0; e < VEC; ++e) other[e] = across<D / VEC>(x[e]);
     } else {
-      if (half % VEC == 0) {  // the other values of a lane's pairs are one piece
+      if (!others.apart(rot)) {  // the other values of a lane's pairs are one piece
         __builtin_memcpy(__builtin_assume_aligned(row + e0, 16), x, sizeof(x));
         wave_sync();
         load_n<16>(other, row + (e0 >= rot.dims ? e0 : e0 < half ? e0 + half : e0 - half));
       } else {
-        // they start anywhere: one at a time, a place left free after every eight values, so
-        // that lanes find theirs in different banks
-        auto place = [](int at) { return at + at / 8; };
-        int from = e0;
-        asm volatile("" : "+v"(from));  // places are worked out here, not kept from row to row
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) row[place(from) + e] = x[e];
-        wave_sync();
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int at = from + e;
-          other[e] = row[place(at >= rot.dims ? at : at < half ? at + half : at - half)];
-        }
+        others.exchange(rot, row, e0, x, other);  // one at a time
       }
       wave_sync();
     }
@@ -332,18 +368,19 @@ struct Heads : Block<F32, D> {
     if (weight) load_n<16>(w, weight + piece() * B::VEC);
   }
   template <class T, class Lds>
-  __device__ static void turn(Lds &lds, const KvRotary &rot, const float (&w)[B::VEC], bool norm,
-                              double eps, int i, int t, float (&val)[B::VEC]) {
+  __device__ static void turn(Lds &lds, const KvRotary &rot, const Others<T, B::VEC> &others,
+                              const float (&w)[B::VEC], bool norm, double eps, int i, int t,
+                              float (&val)[B::VEC]) {
     T *row = lds.rows[threadIdx.x >> 6][(threadIdx.x & 63) / B::CHUNKS];
-    turn_row<T, D, B::VEC>(lds, row, rot, w, norm, eps, 4 * quad(i) + t, piece(), val);
+    turn_row<T, D, B::VEC>(lds, row, rot, others, w, norm, eps, 4 * quad(i) + t, piece(), val);
     __builtin_amdgcn_sched_barrier(0);  // one at a time: registers
   }
   // All rows turned and stored, T what they are worked out in: row r's lie at dst + r *
   // stride bytes.
   template <class T, bool Y32, class Lds>
-  __device__ void turn_and_store(Lds &lds, const KvRotary &rot, const float (&w)[B::VEC], bool norm,
-                                 double eps, uint8_t *dst, uint32_t stride, int head, int lo,
-                                 int hi) const {
+  __device__ void turn_and_store(Lds &lds, const KvRotary &rot, const Others<T, B::VEC> &others,
+                                 const float (&w)[B::VEC], bool norm, double eps, uint8_t *dst,
+                                 uint32_t stride, int head, int lo, int hi) const {
     const uint32_t at = ((uint32_t)head * D + piece() * B::VEC) * (Y32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < B::PER; ++i)
@@ -354,7 +391,7 @@ struct Heads : Block<F32, D> {
         if (!__any(mine)) continue;
         float val[B::VEC];
         values(i, t, val);
-        turn<T>(lds, rot, w, norm, eps, i, t, val);
+        turn<T>(lds, rot, others, w, norm, eps, i, t, val);
         if (mine) store_values<Y32>(dst + (uint32_t)(r * stride + at), val);
       }
   }
@@ -395,13 +432,14 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(KvRotary rot, RotateAr
   auto head = [&](int first) { return first + H::sub() < end ? first + H::sub() : -1; };
   float w[H::VEC];
   H::weights(a.weight, w);
+  const Others<T, H::VEC> others(rot, H::piece());
   H now, next;
   now.load(src, (uint32_t)a.x_stride, head(first), 0, n);
   fill_table<T, D>(lds, rot, turns, 0, n, [&](int r) { return (int64_t)a.positions[row0 + r]; });
   __syncthreads();
   for (; first < end; first += STEP) {
     next.load(src, (uint32_t)a.x_stride, head(first + STEP), 0, n);
-    now.template turn_and_store<T, Y32>(lds, rot, w, a.weight != nullptr, a.eps, dst,
+    now.template turn_and_store<T, Y32>(lds, rot, others, w, a.weight != nullptr, a.eps, dst,
                                         (uint32_t)a.y_stride, head(first), 0, n);
     now = next;
   }
@@ -467,13 +505,14 @@ __device__ inline void append_queries(const AppendArgs &x, int64_t seq, uint32_t
   auto head = [&](int first) { return first + H::sub() < end ? first + H::sub() : -1; };
   float w[H::VEC];
   H::weights(a.q_weight, w);
+  const Others<float, H::VEC> others(x.rot, H::piece());
   H now, next;
   now.load(src, (uint32_t)a.q_stride, head(first), r.lo, r.hi);
   fill_table<float, D>(lds, x.rot, turns, r.lo, r.hi, [&](int i) { return (int64_t)(r.t0 + i); });
   __syncthreads();
   for (; first < end; first += WAVES * H::SUB) {
     next.load(src, (uint32_t)a.q_stride, head(first + WAVES * H::SUB), r.lo, r.hi);
-    now.template turn_and_store<float, false>(lds, x.rot, w, a.q_weight != nullptr, a.eps, dst,
+    now.template turn_and_store<float, false>(lds, x.rot, others, w, a.q_weight != nullptr, a.eps, dst,
                                               (uint32_t)(heads * D * 2), head(first), r.lo, r.hi);
     now = next;
   }
@@ -496,6 +535,7 @@ __device__ inline void append_block(const AppendArgs &x, int64_t seq, uint32_t b
   const int units = (c.kv_heads + SUB - 1) / SUB, end = min(2 * units, (slice + 1) * x.kv_per);
   int unit = slice * x.kv_per + wave;
   const bool turned = slice * x.kv_per < units;
+  const Others<double, H::VEC> others(x.rot, H::piece());
   H now;
   auto load = [&] {
     const int value = unit >= units, h = (unit - (value ? units : 0)) * SUB + H::sub();
@@ -525,7 +565,7 @@ __device__ inline void append_block(const AppendArgs &x, int64_t seq, uint32_t b
         const bool mine = row >= r.lo && row < r.kv_hi;
         now.values(i, t, val[i][t]);
         if (!__any(mine)) continue;
-        if (!value) H::template turn<double>(lds, x.rot, w, norm, a.eps, i, t, val[i][t]);
+        if (!value) H::template turn<double>(lds, x.rot, others, w, norm, a.eps, i, t, val[i][t]);
 #pragma unroll
         for (int e = 0; e < H::VEC; ++e) {
           const uint32_t mag = __float_as_uint(val[i][t][e]) & 0x7FFFFFFFu;
