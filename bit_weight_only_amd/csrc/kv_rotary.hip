@@ -588,7 +588,7 @@ __device__ inline void append_block(const AppendArgs &x, int64_t seq, uint32_t b
 // the old codes): 5.9 us in a trace for one token of 28 heads over 4, 7.2 for 64 of 32 over
 // 8, an empty launch 1.6.  Long prompts are memory bound: 14449 fp32 rows of 28 heads over 4 of
 // 128 (385 MB) 78.4 us = 4.9 TB/s.  In between the vector unit takes part: 5 chunks of up to
-// 701 rows, 32 heads over 8 of 64, normed, 50 values turned (40 MB) 16.6 us, of which some 6
+// 701 rows, 32 heads over 8 of 64, normed, 50 values turned (40 MB) 14.8 us, of which some 4
 // go if nothing turns.
 template <bool F32, int D>
 __global__ __launch_bounds__(kThreads) void append_rotated_kernel(AppendArgs) {
