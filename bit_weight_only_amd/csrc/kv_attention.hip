@@ -1108,7 +1108,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     union {
       bf16x8 v[4 / H];
       bf16x2 e[16 / H];
-    } p;
+    } p, rest;  // rest: the second term, in tiles of 64 rows
 #pragma unroll
     for (int k = 0; k < 4 / H; ++k) {
       const float mk = (float)__builtin_amdgcn_readlane(ve_l, 4 + k + 2 * half) - base;
@@ -1119,6 +1119,10 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
         const float y = exp2_fast(fmaf(s[k >> 1][8 * (k & 1) + i + 1], kc[k], mk));
         p.e[4 * k + i / 2][0] = (__bf16)x;
         p.e[4 * k + i / 2][1] = (__bf16)y;
+        if (H == 2) {
+          rest.e[4 * k + i / 2][0] = (__bf16)(x - (float)p.e[4 * k + i / 2][0]);
+          rest.e[4 * k + i / 2][1] = (__bf16)(y - (float)p.e[4 * k + i / 2][1]);
+        }
         l[0] = fmaf(x, inv, l[0]);
         l[1] = fmaf(y, inv, l[1]);
       }
@@ -1128,7 +1132,11 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
       uint32_t va[DT], vc[DT];
       values(vt, k + 2 * half, va, vc);
 #pragma unroll
-      for (int t = 0; t < DT; ++t) o[t] = mfma(widen(va[t], vc[t]), p.v[k], o[t]);
+      for (int t = 0; t < DT; ++t) {
+        const bf16x8 v = widen(va[t], vc[t]);
+        o[t] = mfma(v, p.v[k], o[t]);
+        if (H == 2) o[t] = mfma(v, rest.v[k], o[t]);
+      }
     }
   };
 
@@ -1251,8 +1259,11 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 // are read and widened once for all of them; a row's parts of the prefix and its
 // sequence's suffix, each (m, l, sum), meet in join_shared_kernel by
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum x_i 2^(m_i - m) / l.
-// Tiles of 64 round the weights to bf16 as the tile kernel does (two terms would double the
-// second product, which is bound by its instructions), those of 16 to two terms.
+// Weights go into the products as two bf16 terms, as those of single tokens do in
+// nf4_kv_attention, in whose place a call may stand: one term, which halves the second
+// product of tiles of 64, took 17.5 us of 18.2 (eight beams over 14449 tokens, 28 heads over 4),
+// 40.2 of 41.8 (64 sequences over 4096), 22.4 of 24.2 (24 of five rows over up to 3501), with the
+// results' error up from 0.0017 to 0.0022.
 //
 // 64 sequences of up to 2000 tokens past 4096 shared ones, 32 heads over 8 of 128 (145 MB):
 // 36.9 us in a trace, 3.9 TB/s; 512 of its 608 workgroups run at a time (registers), the rest

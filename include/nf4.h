@@ -620,8 +620,8 @@ size_t nf4_kv_attention_shared_workspace_bytes(const nf4_kv_cache *cache,
  * group's rows, through the table of its first sequence (or, where each sequence's own rows
  * are many, each through its own), and the tokens past them sequence by sequence;
  * the two meet through the workspace.  Calls that this would save little run as
- * nf4_kv_attention does.  Rows may stand anywhere, among the shared tokens too.  The weights of shared tokens are rounded to bf16 (groups of up to 32 rows
- * of a kv head: to two bf16 terms).  Bitwise reproducible run to run for a given
+ * nf4_kv_attention does.  Rows may stand anywhere, among the shared tokens too.  Where shared tokens are taken
+ * apart, all weights are rounded to two bf16 terms.  Bitwise reproducible run to run for a given
  * device.  Other arguments and errors as nf4_kv_attention; NF4_ERR_NULL for a missing
  * structure or prefix_len, NF4_ERR_SHAPE for its sizes. */
 nf4_status nf4_kv_attention_shared(const nf4_kv_cache *cache, int64_t layer,

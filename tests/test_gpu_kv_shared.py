@@ -359,3 +359,27 @@ def test_forked_sequences(side):
         # both round weights and results to bf16: twice two half steps of values of up to 6
         assert float((res[0][0] - res[1][0]).abs().max()) <= 4 * 2.0 ** -8 * 6
         assert float((res[0][1] - res[1][1]).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads,count", [(128, 7, 1, [1] * 8), (64, 14, 2, [2] * 6),
+                                                      (64, 4, 1, [12, 9, 12]), (128, 8, 2, [20, 1, 17])])
+def test_weights_of_many_rows_keep_two_terms(side, dim, heads, kv_heads, count):
+    """Groups and sequences of more than 32 rows of a kv head: as exact as few rows.  A result
+    is within half a step of bf16 of a sum whose weights are within 2^-16 of theirs (each of
+    the two roundings keeps 2^-8 of what it is given), its scores and sums as in `bounds`:
+    with weights of one bf16 term a fifth of the results and more are not."""
+    n = len(count)
+    c = Shared(side, 21, dim, 16, heads, kv_heads, [300 + 7 * s + count[s] for s in range(n)], count, [0, n], [300])
+    assert c.apart
+    c.c.ks[:], c.c.vs[:] = 2.0 ** -8, 2.0 ** -6
+    scale = float(np.float32(0.02))
+    out, z = c.run(scale=scale)
+    want, lse, mag, big = kv.attention(c.c, 0, c.table, c.start, c.kv_len,
+                                       c.q.reshape(-1, heads, dim).astype(np.float64), scale, 0, 0)
+    delta = 2.0 ** -24 * (2 * dim + 16) * big + 2.0 ** -21
+    sums = (max(c.kv_len) / 8 + 200) * 2.0 ** -24
+    off = mag * (2.0 ** -16 + 2 * delta[..., None] + 2 * sums) * 1.01
+    assert off.max() < 2.0 ** -12 * mag.max()  # so that one term shows
+    half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(out), 2.0 ** -100))) - 8)
+    bad = np.abs(out - want) > half + off
+    assert not bad.any(), f"{bad.sum()} of {bad.size} past the bound"
