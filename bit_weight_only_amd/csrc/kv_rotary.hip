@@ -8,8 +8,8 @@
 //
 // the norm before it is x (mean x^2 + eps)^-1/2 w over the whole head.  Frequencies
 // come as turns a token in 64-bit fixed point, so that p f modulo a full turn is a
-// 64-bit product, exact to 2^-35 of a turn at the longest position; its sine and
-// cosine are summed in 64 bits.
+// 64-bit product, off by the position times what rounding the turns left; its sine and
+// cosine are summed in 64 bits, to 2^-37.
 //
 // What leaves as bf16 is worked out in fp32.  Keys, which go on to be quantized, and
 // fp32 results are worked out in 64 bits and rounded once: a code then differs from
@@ -28,14 +28,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Cosine and sine of u 2^-32 turns, times gain.  With the nearest quarter turn taken
+// Cosine and sine of u 2^-64 turns, times gain.  With the nearest quarter turn taken
 // off, |x| <= pi / 4, and what the Taylor sums leave out is under x^13 / 13! = 7e-12.
+// All 64 bits go in: the upper 32 alone are up to 1.5e-9 rad off, which is more than an fp32
+// rounding of a result under a fortieth of its pair.
 struct Turn {
   double c, s;
 };
-__device__ inline Turn turned(uint32_t u, double gain) {
-  const uint32_t quarter = (u + 0x20000000u) >> 30;
-  const double x = (double)(int)(u - (quarter << 30)) * (6.283185307179586 / 4294967296.0);
+__device__ inline Turn turned(uint64_t u, double gain) {
+  const uint32_t quarter = ((uint32_t)(u >> 32) + 0x20000000u) >> 30;
+  const double x = (double)(int64_t)(u - ((uint64_t)quarter << 62)) * (6.283185307179586 * 0x1p-64);
   const double y = x * x;
   double s = fma(y, -1.0 / 39916800, 1.0 / 362880);
   s = fma(y, s, -1.0 / 5040);
@@ -77,7 +79,7 @@ __device__ inline void fill_table(Lds &lds, const KvRotary &rot, uint64_t turns,
   if (2 * p >= rot.dims) return;
   for (int r = threadIdx.x / PAIRS; r < hi; r += kThreads / PAIRS) {
     if (r < lo) continue;
-    const Turn t = turned((uint32_t)(((uint64_t)position(r) * turns) >> 32), rot.gain);
+    const Turn t = turned((uint64_t)position(r) * turns, rot.gain);
     const float2 cs = make_float2((float)t.c, (float)t.s);
     const float2 low = make_float2((float)(t.c - cs.x), (float)(t.s - cs.y));
     auto set = [&](int at, float sign) {

@@ -528,8 +528,8 @@ nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout l
  * that -p undoes p).  weight: device fp32[head_dim], 16-byte aligned, of the norm, or NULL
  * for none; eps: at least 2^-100, not looked at without a norm.  y may be x with
  * the same type and stride (NF4_ERR_SHAPE with others); else they must not overlap.
- * Sines and cosines are worked out in 64 bits, and so is all of an fp32 result, which
- * is rounded once; a bfloat16 result is worked out in fp32 from them (the norm's sum in
+ * Sines and cosines are worked out in 64 bits, to 2^-37, and so is all of an fp32 result,
+ * which is rounded once; a bfloat16 result is worked out in fp32 from them (the norm's sum in
  * 64 bits where a mean square passes 2^100).  head_dim: 64 or 128; rows <= 2^23.
  * Bitwise reproducible.
  * Errors: NF4_ERR_NULL, NF4_ERR_SHAPE, NF4_ERR_ALIGN. */

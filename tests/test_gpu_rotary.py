@@ -470,3 +470,45 @@ def test_large_rows_leave_their_neighbours_alone(side, dim):
                 assert bool(same[r, h]), (r, h)
     # scaled by a power of two, and eps far below both: the same up to the roundings
     assert float((out[0].float() - out[1].float()).abs().max()) <= float(out[0].float().abs().max()) * 2.0 ** -7
+
+
+def half_step(x):
+    """Half a step of fp32 at x."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -126))) - 24)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("layout", [plain.HALVES, plain.PAIRS])
+@pytest.mark.parametrize("dim,dims", [(128, 128), (128, 50), (64, 64)])
+def test_fp32_results_are_rounded_once(side, dim, dims, layout, f32):
+    """Half a step of the exact value and what 64 bits leave: the sine's sum stops before
+    x^13 / 13! of the angle x that a quarter turn leaves, each pair's turns a token are 2^-65 of a
+    turn off, sines and cosines are kept to 2^-48 and products are good to 2^-52 (2^-46 for
+    all of that), 80 bits of the oracle's angle are 2^-61 of its radians.  Slow pairs at small
+    positions, and pairs of which one value is 0, show the sine by itself."""
+    rng = np.random.default_rng(51)
+    f = plain.frequencies(dims, 1e6)
+    at = np.array([0, 1, -1, 2, 5, 17, -100, 1000, 14449, 2 ** 20 + 7, -2 ** 20 - 7])
+    rows = len(at)
+    x = values(rng, rows, 4, dim, f32).reshape(rows, 4, dim)
+    a, b = plain.pair_indexes(dims, layout)
+    x[:, 1, a], x[:, 1, b], x[:, 2, a], x[:, 2, b] = 0.0, 1.0, 1.0, 0.0
+    x = x.reshape(rows, 4 * dim)
+    got = rotate(side, side.nf4.Rotary(dims, layout, frequencies=f), x, f32, at, 4, dim, None, True)
+    got = got.reshape(rows, 4, dim).astype(np.float64)
+    want, mag = turned(x.reshape(rows, 4, dim).astype(np.float64), at, f, layout, 1.0, None)
+    angle = np.abs(at)[:, None] * f
+    left = np.abs(angle - np.rint(angle / (np.pi / 2)) * (np.pi / 2))
+    off = left ** 13 / 6227020800 + 2 * np.pi * 2.0 ** -65 * np.abs(at)[:, None] + angle * 2.0 ** -61
+    c, s = np.abs(np.cos(angle))[:, None], np.abs(np.sin(angle))[:, None]
+    p, q = (np.abs(x.reshape(rows, 4, dim)[..., i]) for i in (a, b))
+    bound = half_step(want)
+    bound[..., a] += off[:, None] * mag[..., a] + 2.0 ** -46 * (p * c + q * s)
+    bound[..., b] += off[:, None] * mag[..., b] + 2.0 ** -46 * (p * s + q * c)
+    bad = np.abs(got - want) > bound
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: " \
+        f"{got[bad][0]} for {want[bad][0]}"
+    # a turn back is the negative angle, to the bit
+    for i, j in ((1, 2), (9, 10)):
+        assert np.array_equal(got[i, 1, a], -got[j, 1, a]) and np.array_equal(got[i, 2, b], -got[j, 2, b])
+        assert np.array_equal(got[i, 1, b], got[j, 1, b])
