@@ -115,6 +115,21 @@ nf4_status check_rotary(const nf4_rotary *r, int64_t head_dim, nf4::KvRotary &ou
   return NF4_OK;
 }
 
+// 2^64 times the turns of f radians, |f| <= 2^20, modulo 2^64 and rounded to nearest: half a
+// unit and 2^-32 of one off.  With |f| = m 2^(e - 53) for a whole m under 2^53, and 1 / (2 pi) to
+// 128 bits, what is wanted is m times those bits, shifted right by 117 - e; the lowest 64 are left out.
+uint64_t turns_of(double f) {
+  constexpr uint64_t kHigh = 0x28BE60DB9391054A, kLow = 0x7F09D5F47D4D3770;
+  using Wide = unsigned __int128;
+  int e;
+  const uint64_t m = (uint64_t)ldexp(frexp(fabs(f), &e), 53);
+  const Wide high = (Wide)m * kHigh + (uint64_t)((Wide)m * kLow >> 64);  // under 2^118
+  const int shift = 53 - e;                                             // 32 or more
+  if (shift > 119) return 0;
+  const uint64_t t = (uint64_t)((high + ((Wide)1 << (shift - 1))) >> shift);
+  return f < 0.0 ? 0 - t : t;
+}
+
 // Windows and first tokens past any position are as good as the longest one.
 int held(int64_t v) { return (int)(v > nf4::kKvLongest ? nf4::kKvLongest : v); }
 static_assert(nf4::kKvLongest == kMaxLen + kMaxRows, "no row of the longest sequence is held");
@@ -259,17 +274,7 @@ nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout l
   rotary->dims = dims;
   rotary->layout = layout;
   rotary->gain = gain;
-  for (int64_t i = 0; i < 64; ++i) {
-    uint64_t turns = 0;
-    if (i < dims / 2) {
-      // the part of a turn past the last whole one, in 80 bits: 2^-65 of a turn off
-      long double t = (long double)frequency[i] / 6.283185307179586476925286766559L;
-      t -= floorl(t);
-      t = rintl(ldexpl(t, 64));
-      turns = t >= 0x1p64L ? 0 : (uint64_t)t;
-    }
-    rotary->turns[i] = turns;
-  }
+  for (int64_t i = 0; i < 64; ++i) rotary->turns[i] = i < dims / 2 ? turns_of(frequency[i]) : 0;
   return NF4_OK;
 }
 

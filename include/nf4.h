@@ -515,8 +515,8 @@ nf4_status nf4_rotary_frequencies(int64_t dims, double base, nf4_rotary_scaling 
                                   double *frequency);
 
 /* Fills the structure from frequencies (host, radians a token, at most 2^20 in
- * magnitude; negative ones turn back).  A turn is kept to 2^-65, so that
- * angles are right to 2^-35 of a turn at positions up to 2^30. */
+ * magnitude; negative ones turn back).  A pair's turns a token are kept to
+ * 2^-65 of a turn, so that angles are right to 2^-35 of a turn at positions up to 2^30. */
 nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout layout,
                            const double *frequency, double gain);
 

@@ -288,3 +288,17 @@ def test_parts_that_take_too_much_room_are_not_taken_apart():
         b = batch(seqs=rows, rows=rows, max_rows=1, max_len=20000, table_stride=400)
         need = shared(cache(), b, groups(groups=1, max_prefix=16000), 8, 0, 0)
         assert (need != plain(cache(), b, 8, 0, 0)) == apart and need <= 2 << 30
+
+
+def test_turns_of_large_frequencies():
+    """Half a unit of 2^-64 of a turn over the whole range, and what 128 bits of 1 / (2 pi) leave."""
+    rng = np.random.default_rng(0)
+    f = np.concatenate([rng.uniform(-1, 1, 40) * 2.0 ** rng.integers(-60, 21, 40),
+                        [2.0 ** 20, -2.0 ** 20, np.nextafter(2.0 ** 20, 0), 2.0 * math.pi, 3e5 * math.pi, 5e-324,
+                         -5e-324, 2.0 ** -61, 2.0 ** -63, -2.0 ** -62, 1e-19, 0.0, -0.0, 1.0]])
+    r = nf4._Rotary()
+    nf4.nf4_rotary_init(r, 2 * len(f), nf4.NF4_ROTARY_HALVES, f)
+    for x, got in zip(f, r.turns):
+        turn = Fraction(float(x)) / (2 * PI)
+        off = abs((turn - math.floor(turn)) * 2 ** 64 - got)
+        assert min(off, 2 ** 64 - off) <= 0.5 + 2.0 ** -31, (x, got)
