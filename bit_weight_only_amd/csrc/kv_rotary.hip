@@ -151,11 +151,12 @@ __device__ inline void norm_row(const float (&w)[VEC], double eps, float (&v)[VE
     for (int e = 0; e < VEC; ++e) x[e] = v[e];
     norm_row<D, VEC>(w, eps, x);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = large ? (float)x[e] : v[e] * (inv * w[e]);
+    for (int e = 0; e < VEC; ++e) v[e] = large ? (float)x[e] : v[e] * inv * w[e];
     return;
   }
+  // (the value first: inv w passes fp32 for rows of zeros under large weights)
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) v[e] *= inv * w[e];
+  for (int e = 0; e < VEC; ++e) v[e] = v[e] * inv * w[e];
 }
 
 // What one lane's value is to the lane that holds the other half of its row, CHUNKS / 2 lanes

@@ -512,3 +512,26 @@ def test_fp32_results_are_rounded_once(side, dim, dims, layout, f32):
     for i, j in ((1, 2), (9, 10)):
         assert np.array_equal(got[i, 1, a], -got[j, 1, a]) and np.array_equal(got[i, 2, b], -got[j, 2, b])
         assert np.array_equal(got[i, 1, b], got[j, 1, b])
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_of_small_rows_under_large_weights(side, f32):
+    """Rows of zeros stay zeros and tiny ones come out finite, whatever 1 / sqrt(eps) times a
+    weight is."""
+    t, nf4 = side.torch, side.nf4
+    rng = np.random.default_rng(61)
+    x = bf16(rng.normal(size=(3, 2 * 64)))
+    x[0] = 0.0
+    x[1] *= np.float32(2.0 ** -60)
+    eps, w = 2.0 ** -100, np.full(64, 2.0 ** 100, np.float32)
+    f = plain.frequencies(64, 1e4)
+    xd = side.to_dev(x) if f32 else side.to_dev(x).bfloat16()
+    for to in (t.bfloat16, t.float32):
+        y = t.empty(3, 128, dtype=to, device="cuda")
+        nf4.nf4_rotate(nf4.Rotary(64, frequencies=f), xd, 128, int(f32), i32(side, [0, 1, 2]), 3, 2, 64,
+                       side.to_dev(w), eps, y, 128, int(to is t.float32))
+        t.cuda.synchronize()
+        x64 = x.reshape(3, 2, 64).astype(np.float64)
+        z = x64 / np.sqrt((x64 * x64).mean(-1, keepdims=True) + eps) * 2.0 ** 100
+        want, mag = plain.rotate(z, [0, 1, 2], f, 0)
+        near(y.double().cpu().numpy().reshape(want.shape), want, mag, True, to is t.bfloat16)
