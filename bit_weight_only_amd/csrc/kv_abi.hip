@@ -103,11 +103,14 @@ nf4_status check_rows(const void *p, int64_t stride, int64_t width, nf4_kv_type 
 // The norms' eps: what is divided by stays a normal float.
 bool eps_ok(float eps) { return isfinite(eps) && eps >= 0x1p-100f; }
 
+// A gain that sines and cosines times it, which kernels hold as two fp32 terms, stay in range with.
+bool gain_ok(double gain) { return gain == 0.0 || (fabs(gain) >= 0x1p-100 && fabs(gain) <= 0x1p100); }
+
 nf4_status check_rotary(const nf4_rotary *r, int64_t head_dim, nf4::KvRotary &out) {
   if (!r) return NF4_ERR_NULL;
   if (r->dims < 0 || r->dims > head_dim || r->dims % 2 != 0) return NF4_ERR_SHAPE;
   if (r->layout != NF4_ROTARY_HALVES && r->layout != NF4_ROTARY_PAIRS) return NF4_ERR_SHAPE;
-  if (!isfinite(r->gain)) return NF4_ERR_SHAPE;
+  if (!gain_ok(r->gain)) return NF4_ERR_SHAPE;
   out.dims = (int)r->dims;
   out.pairs = r->layout == NF4_ROTARY_PAIRS;
   out.gain = r->gain;
@@ -267,7 +270,7 @@ nf4_status nf4_rotary_frequencies(int64_t dims, double base, nf4_rotary_scaling 
 nf4_status nf4_rotary_init(nf4_rotary *rotary, int64_t dims, nf4_rotary_layout layout,
                            const double *frequency, double gain) {
   if (!rotary || (!frequency && dims > 0)) return NF4_ERR_NULL;
-  if (dims < 0 || dims > 128 || dims % 2 != 0 || !isfinite(gain)) return NF4_ERR_SHAPE;
+  if (dims < 0 || dims > 128 || dims % 2 != 0 || !gain_ok(gain)) return NF4_ERR_SHAPE;
   if (layout != NF4_ROTARY_HALVES && layout != NF4_ROTARY_PAIRS) return NF4_ERR_SHAPE;
   for (int64_t i = 0; i < dims / 2; ++i)
     if (!(fabs(frequency[i]) <= 0x1p20)) return NF4_ERR_SHAPE;

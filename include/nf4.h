@@ -484,7 +484,7 @@ typedef enum nf4_rotary_layout {
 typedef struct nf4_rotary {
   int64_t dims;       /* even, 0 (nothing turns) .. head_dim */
   int64_t layout;     /* nf4_rotary_layout */
-  double gain;
+  double gain;        /* 0, or 2^-100 .. 2^100 in magnitude */
   uint64_t turns[64]; /* pair i turns by turns[i] / 2^64 of a full turn a token */
 } nf4_rotary;
 

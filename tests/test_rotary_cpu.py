@@ -302,3 +302,15 @@ def test_turns_of_large_frequencies():
         turn = Fraction(float(x)) / (2 * PI)
         off = abs((turn - math.floor(turn)) * 2 ** 64 - got)
         assert min(off, 2 ** 64 - off) <= 0.5 + 2.0 ** -31, (x, got)
+
+
+@pytest.mark.parametrize("gain,ok", [(0.0, True), (2.0 ** -100, True), (-2.0 ** 100, True), (1e300, False),
+                                     (-2.0 ** 101, False), (2.0 ** -101, False), (1e-45, False)])
+def test_gains_past_what_the_kernels_hold(gain, ok):
+    """Sines and cosines times the gain are two fp32 terms: 2^128 would make them infinite,
+    2^-140 leave them a few bits."""
+    r, f = nf4._Rotary(), (ctypes.c_double * 64)()
+    assert nf4.lib().nf4_rotary_init(ctypes.byref(r), 128, 0, f, gain) == (nf4.NF4_OK if ok else nf4.NF4_ERR_SHAPE)
+    # the structure's own; what is accepted is refused by its y, which is not aligned
+    status = nf4.lib().nf4_rotate(rotary(gain=gain), A, 1024, 0, A, 5, 8, 128, A, 1e-6, 2 * A + 2, 1024, 0, None)
+    assert status == (nf4.NF4_ERR_ALIGN if ok else nf4.NF4_ERR_SHAPE)
