@@ -415,6 +415,16 @@ def _operands(where: str, gpu: int, type: int, *tensors) -> None:
             raise NF4Error(NF4_ERR_SHAPE, f"{where}: a tensor of another type")
 
 
+def _workspace(where: str, gpu: int, workspace, ws_bytes: int) -> None:
+    """A workspace tensor (not None, nor an address) lies on that GPU and holds the bytes."""
+    if workspace is None or workspace.__class__ is int:
+        return
+    if workspace.get_device() != gpu:
+        raise NF4Error(NF4_ERR_SHAPE, f"{where}: tensors that are not on one GPU")
+    if workspace.numel() * workspace.element_size() < ws_bytes or not workspace.is_contiguous():
+        raise NF4Error(NF4_ERR_WORKSPACE, f"{where}: a workspace of fewer bytes than given")
+
+
 def _stream_on(where: str, gpu: int, stream) -> int | None:
     """The stream's handle.  The current one, and a Stream object, have to be of the
     tensors' GPU: a launch on another GPU's would take their addresses as its own."""
@@ -525,6 +535,7 @@ def nf4_kv_attention_shared(cache, layer: int, batch, groups, q, q_stride: int, 
     _on_gpu(where, cache.gpu, groups.gpu)
     _operands(where, cache.gpu, NF4_KV_BF16, q, out)
     _operands(where, cache.gpu, NF4_KV_F32, lse)
+    _workspace(where, cache.gpu, workspace, ws_bytes)
     _check(lib().nf4_kv_attention_shared(cache.arg, layer, batch.arg, groups.arg, _ptr(q), q_stride,
                                          heads, scale, window, sinks, _ptr(out), _ptr(lse),
                                          _ptr(workspace), ws_bytes,

@@ -314,3 +314,33 @@ def test_gains_past_what_the_kernels_hold(gain, ok):
     # the structure's own; what is accepted is refused by its y, which is not aligned
     status = nf4.lib().nf4_rotate(rotary(gain=gain), A, 1024, 0, A, 5, 8, 128, A, 1e-6, 2 * A + 2, 1024, 0, None)
     assert status == (nf4.NF4_ERR_ALIGN if ok else nf4.NF4_ERR_SHAPE)
+
+
+def test_workspaces_of_the_host_or_too_small_are_refused(monkeypatch):
+    """The kernels would take a host address as the GPU's, and write as many bytes as said."""
+    torch = pytest.importorskip("torch")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    c, b = nf4.KVCache(1, 4, 2, 16, 64, device="cpu"), nf4.KVBatch(i32(2), i32(2, 4))
+    g, out = nf4.KVGroups(i32(1)), torch.zeros(2, 128, dtype=torch.bfloat16)
+    ws = torch.zeros(64, dtype=torch.float32)
+
+    def call(workspace, ws_bytes):
+        nf4.nf4_kv_attention_shared(c, 0, b, g, out, 128, 2, 0.1, 0, 0, out, None, workspace, ws_bytes, stream=0)
+    reached = []
+    monkeypatch.setattr(nf4, "_operands", lambda *a: None)  # rows as if on the GPU
+    monkeypatch.setattr(nf4, "_on_gpu", lambda *a: None)
+    monkeypatch.setattr(nf4, "_check", lambda *a: reached.append(a))
+    monkeypatch.setattr(nf4, "lib", lambda: type("L", (), {"nf4_kv_attention_shared": lambda *a: 0,
+                                                           "nf4_status_string": lambda s: b"refused"}))
+    c.gpu = 0
+    with pytest.raises(nf4.NF4Error, match="not on one GPU"):
+        call(ws, 256)
+    c.gpu = -1  # where the host's tensors are
+    for bad, n in ((ws, 257), (ws[::2], 128)):
+        with pytest.raises(nf4.NF4Error) as e:
+            call(bad, n)
+        assert e.value.status == nf4.NF4_ERR_WORKSPACE
+    assert not reached
+    for fine, n in ((ws, 256), (ws, 16), (None, 0), (0x1000, 1 << 40)):
+        call(fine, n)
+    assert len(reached) == 4
