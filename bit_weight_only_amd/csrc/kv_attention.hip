@@ -258,36 +258,24 @@ struct TileOf {
     p_lo = 0;
     p_hi = -1;
   }
-  // The positions of its tokens: lane l has those of tokens l and 64 + l from its first on
-  // (a tile of no more than 64 rows has no others).
-  struct Guesses {
-    KvBatch::Guess low, high;
-  };
+  // The positions of its tokens, in two steps (KvBatch): lane l has that of token l from its
+  // first one on, -1 past the last.
   template <int WIDTH>
-  __device__ Guesses guess(const KvBatch &b, int first, int past) const {
-    const int last = (int)((min(r0 + WIDTH, rows) - 1) / group);
-    Guesses g;
-    g.high = g.low = b.guess(row0 + min(token(0), last), first, past, row0, all);
-    if (WIDTH > 64) g.high = b.guess(row0 + min(token(1), last), first, past, row0, all);
-    return g;
+  __device__ KvBatch::Guess guess(const KvBatch &b, int first, int past) const {
+    return b.guess(row0 + min(token(), last_token<WIDTH>()), first, past, row0, all);
   }
   template <int WIDTH>
-  __device__ void positions(const KvBatch &b, int first, int past, const Guesses &g,
-                            int (&at)[2]) {
-    const int last = (int)((min(r0 + WIDTH, rows) - 1) / group);
-    at[0] = token(0) <= last ? b.position(g.low, row0 + token(0), first, past) : -1;
-    at[1] = -1;
-    if (WIDTH > 64 && token(1) <= last) at[1] = b.position(g.high, row0 + token(1), first, past);
-    p_hi = -lanes_min(-max(at[0], at[1]));
-    p_lo = lanes_min(min(token(0) <= last ? at[0] : p_hi,
-                         WIDTH > 64 && token(1) <= last ? at[1] : p_hi));
+  __device__ int positions(const KvBatch &b, int first, int past, const KvBatch::Guess &g) {
+    static_assert(WIDTH <= 64, "a lane for every token");
+    const bool has = token() <= last_token<WIDTH>();
+    const int at = has ? b.position(g, row0 + token(), first, past) : -1;
+    p_hi = -lanes_min(-at);
+    p_lo = lanes_min(has ? at : p_hi);
+    return at;
   }
-  __device__ int token(int i) const { return (int)(r0 / group) + 64 * i + (int)(threadIdx.x & 63); }
-  // Position of the tile's token t (counted from its first) from what the lanes hold.
-  __device__ static int position(const int (&at)[2], int t) {
-    const int x = __shfl(at[0], t & 63), y = __shfl(at[1], t & 63);
-    return t < 64 ? x : y;
-  }
+  __device__ int token() const { return (int)(r0 / group) + (int)(threadIdx.x & 63); }
+  template <int WIDTH>
+  __device__ int last_token() const { return (int)((min(r0 + WIDTH, rows) - 1) / group); }
 };
 using Tile = TileOf<uint32_t>;
 
@@ -501,9 +489,9 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   if (S::kPrefix && place.shared == 0) return;
   Tile tl = place.tile();
   if (tl.empty()) return;
-  int at[2];
+  int at = -1;  // a prefix's: positions of the tile's tokens
   if (S::kPrefix && !place.ahead())
-    tl.template positions<16>(b, place.first, place.past, tl.template guess<16>(b, place.first, place.past), at);
+    at = tl.template positions<16>(b, place.first, place.past, tl.template guess<16>(b, place.first, place.past));
   const Steps<32> steps = place.steps(tl, tl.p_hi);
   const Range range = place.range(steps);
   if (range.none) return;
@@ -566,16 +554,17 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   };
 
   look(first);
-  typename Tile::Guesses guesses = {};
-  if (S::kPrefix && place.ahead()) guesses = tl.template guess<16>(b, place.first, place.past);
+  KvBatch::Guess guess = {};
+  if constexpr (S::kPrefix)
+    if (place.ahead()) guess = tl.template guess<16>(b, place.first, place.past);
 
   bf16x8 q[KS];
   const uint16_t *qp = a.q + (tl.row0 + tok) * a.q_stride + (int64_t)qh * D + g * 16;
 #pragma unroll
   for (int j = 0; j < KS; ++j)
     q[j] = *reinterpret_cast<const bf16x8 *>(qp + 64 * (j / 2) + 8 * (j % 2));
-  if (S::kPrefix && place.ahead()) tl.template positions<16>(b, place.first, place.past, guesses, at);
-  const int row_pos = S::kPrefix ? Tile::position(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
+  if (S::kPrefix && place.ahead()) at = tl.template positions<16>(b, place.first, place.past, guess);
+  const int row_pos = S::kPrefix ? __shfl(at, tok - (int)(tl.r0 / tl.group)) : tl.len - tl.n + tok;
   const int pos = mine ? row_pos : -1;
 
   const Visible<S> visible{a.window, a.sinks, place.shared};
@@ -902,9 +891,11 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   if (S::kPrefix && place.shared == 0) return;
   Tile tl = place.tile();
   if (tl.empty()) return;
-  int at[2];
-  if (S::kPrefix && !place.ahead())
-    tl.template positions<kTileRows / H>(b, place.first, place.past, tl.template guess<kTileRows / H>(b, place.first, place.past), at);
+  int at = -1;  // a prefix's: positions of the tile's tokens
+  if constexpr (S::kPrefix)
+    if (!place.ahead())
+      at = tl.template positions<kTileRows / H>(b, place.first, place.past,
+                                                tl.template guess<kTileRows / H>(b, place.first, place.past));
   // the wave's rows: with two teams, waves w and w + 4 share a SIMD and hold
   // different halves of the tile
   const int sub = H == 2 ? wave & 1 : team == 0 ? wave : wave ^ 2;
@@ -992,8 +983,9 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     to = to == lds0 + (kStages - 1) * L::kStage ? lds0 : to + L::kStage;
   };
 
-  typename Tile::Guesses guesses = {};
-  if (S::kPrefix && place.ahead()) guesses = tl.template guess<kTileRows / H>(b, place.first, place.past);
+  KvBatch::Guess guess = {};
+  if constexpr (S::kPrefix)
+    if (place.ahead()) guess = tl.template guess<kTileRows / H>(b, place.first, place.past);
 
   // the element of key piece 2m + h that step 2m + e of the first product takes
   // is value 32m + 16h + 8e
@@ -1146,8 +1138,8 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
   }
   if constexpr (S::kPrefix) {
     // (all of these loads are in flight together)
-    if (place.ahead()) tl.template positions<kTileRows / H>(b, place.first, place.past, guesses, at);
-    const int row_pos = Tile::position(at, tok - (int)(tl.r0 / tl.group));
+    if (place.ahead()) at = tl.template positions<kTileRows / H>(b, place.first, place.past, guess);
+    const int row_pos = __shfl(at, tok - (int)(tl.r0 / tl.group));
     pos = mine ? row_pos : -1;
     w_lo = lanes_min(mine ? pos : 0x7FFFFFFF);
     w_hi = -lanes_min(-pos);
