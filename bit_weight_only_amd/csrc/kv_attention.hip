@@ -301,6 +301,7 @@ struct Place {
   int first, past;  // sequences of the group
   KvBatch::Raw raw;
   int shared;
+  int first_len;  // tokens of the group's first sequence
   const int32_t *table;
 
   __device__ Place(const KvCache &c, const KvBatch &b, const KvAttention &a, const S &scope,
@@ -316,7 +317,21 @@ struct Place {
     if constexpr (!S::kPrefix) raw = b.raw(seq);
     if constexpr (S::kSuffix) shared = scope.g.shared_of(b, seq);
     // (a group without sequences has no rows: nothing of its table is read)
-    table = b.table + (int64_t)(first < b.seqs ? first : 0) * b.table_stride;
+    const int64_t s = first < b.seqs ? first : 0;
+    if constexpr (S::kPrefix) first_len = b.kv_len[s];
+    table = b.table + s * b.table_stride;
+  }
+  // Shared tokens are read from the first sequence's pages, unless it has not got them all, as
+  // one that was released or is behind the others: then `table` becomes another one's.  Asked
+  // once that first pages' ids are on their way, so that the common case waits for nothing.
+  __device__ bool elsewhere(const int32_t *&table) const {
+    if constexpr (!S::kPrefix) return false;
+    else {
+      if (first_len >= shared) return false;
+      const int s = scope.g.source(b, first, past, shared);
+      table = b.table + (int64_t)s * b.table_stride;
+      return s != first;
+    }
   }
   using Tile = TileOf<typename S::Number>;
   __device__ Tile tile() const {
@@ -554,6 +569,7 @@ __device__ inline void decode_part(const KvCache &c, int64_t layer, const KvBatc
   };
 
   look(first);
+  if (place.elsewhere(table)) look(first);
   KvBatch::Guess guess = {};
   if constexpr (S::kPrefix)
     if (place.ahead()) guess = tl.template guess<16>(b, place.first, place.past);
@@ -942,6 +958,7 @@ __device__ inline void tile_part(const KvCache &c, int64_t layer, const KvBatch 
     return page;
   };
   int page_l = -1, page_next = pages_of(0);
+  if (place.elsewhere(table)) page_next = pages_of(0);
   uint64_t hole_mask = 0;
   uint32_t holes = 0;  // four bits each for the steps that are in LDS or on their way
   const uint32_t page_bytes = (uint32_t)c.page_bytes();  // at most 2^25

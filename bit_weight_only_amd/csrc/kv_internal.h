@@ -127,6 +127,28 @@ struct KvGroups {
     const int most = max_shared < b.max_len ? max_shared : b.max_len;
     return n < 0 ? 0 : n > most ? most : n;
   }
+  // The sequence of first .. past - 1 whose pages the group's `shared` tokens are read from: the
+  // first one that has them all, or has the most of them.  The whole wave looks.
+  __device__ int source(const KvBatch &b, int first, int past, int shared) const {
+    int most = -1, at = first;
+    for (int s0 = first; s0 < past; s0 += 64) {
+      const int s = s0 + (int)(threadIdx.x & 63), len = s < past ? b.kv_len[s] : -1;
+      const uint64_t all = __ballot(len >= shared);
+      if (all) return s0 + __builtin_ctzll(all);
+      if (len > most) {
+        most = len;
+        at = s;
+      }
+    }
+    for (int o = 1; o < 64; o *= 2) {
+      const int len = __shfl_xor(most, o), s = __shfl_xor(at, o);
+      if (len > most || (len == most && s < at)) {
+        most = len;
+        at = s;
+      }
+    }
+    return __builtin_amdgcn_readfirstlane(at);
+  }
   // The same of the group that sequence s is in (0: in none), and that group's first
   // sequence.  The whole wave looks, a lane at every 64th place, so that up to 64 groups
   // take one trip to memory.

@@ -594,8 +594,9 @@ nf4_status nf4_kv_attention(const nf4_kv_cache *cache, int64_t layer, const nf4_
  * sequences first[g] .. first[g + 1] - 1 (device int32[groups + 1], ascending) all
  * have the same keys and values in their first prefix_len[g] tokens (device
  * int32[groups]; less than 1: none), in the same pages or in copies.  A sequence may
- * have fewer tokens than that, but the first one of a group not fewer of the shared
- * ones than any other: they are read from its pages.  Sequences of no group share
+ * have fewer tokens than that, or none any more (one that was released and stays in the
+ * batch): the shared ones are read from the pages of the group's first sequence that has
+ * them all, or of the first one that has the most of them.  Sequences of no group share
  * nothing.  first NULL: one group of all sequences (groups == 1).
  * max_rows bounds the rows of a group together, as the host knows it (0: the
  * batch's rows): rows of a group past it may miss what is shared.  max_prefix, 0 ..
@@ -617,7 +618,7 @@ size_t nf4_kv_attention_shared_workspace_bytes(const nf4_kv_cache *cache,
 
 /* nf4_kv_attention for a batch whose sequences share their first tokens: what it
  * computes, with the keys and values of a group's shared tokens read once for all of the
- * group's rows, through the table of its first sequence (or, where each sequence's own rows
+ * group's rows, through the table of one sequence (or, where each sequence's own rows
  * are many, each through its own), and the tokens past them sequence by sequence;
  * the two meet through the workspace.  Calls that this would save little run as
  * nf4_kv_attention does.  Rows may stand anywhere, among the shared tokens too.  Where shared tokens are taken

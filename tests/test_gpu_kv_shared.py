@@ -383,3 +383,58 @@ def test_weights_of_many_rows_keep_two_terms(side, dim, heads, kv_heads, count):
     half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(out), 2.0 ** -100))) - 8)
     bad = np.abs(out - want) > half + off
     assert not bad.any(), f"{bad.sum()} of {bad.size} past the bound"
+
+
+def shorter(c, s, n):
+    """Sequence s of a case has n tokens left, and pages for no more."""
+    c.kv_len[s] = n
+    c.table[s, -(-n // c.page):] = -1
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1 << 40, 3)])
+@pytest.mark.parametrize("dim,heads,kv_heads,count", [(128, 4, 2, 1), (64, 7, 1, 2), (64, 4, 1, 12)])
+@pytest.mark.parametrize("left", [[(0, 0)], [(0, 0), (1, 0), (2, 40)], [(0, 40)], [(0, 0), (4, 17), (5, 0)],
+                                  [(s, n) for s, n in enumerate((50, 0, 90, 90, 17, 90))]])
+def test_groups_whose_first_sequence_ended(side, left, dim, heads, kv_heads, count, window, sinks):
+    """Released sequences stay in the batch with no tokens, others fall behind: the rest see
+    what they share all the same, from the pages of one that has it, or most of it."""
+    c = Shared(side, 22, dim, 16, heads, kv_heads, [130, 140, 133, 150, 120, 125], [count] * 6, [0, 4, 6], [100, 101])
+    for s, n in left:
+        shorter(c, s, n)
+    c.run(window, sinks)
+
+
+@pytest.mark.parametrize("count", [1, 3])
+def test_many_sequences_ended(side, count):
+    """More of them than lanes before the first that is left; none that has all of it."""
+    for last in (90, 60):
+        c = Shared(side, 23, 64, 16, 2, 1, [90 + count] * 140, [count] * 140, [0, 140], [90])
+        for s in range(140):
+            shorter(c, s, 0 if s < 133 else 30 if s % 2 else last)
+        c.run()
+
+
+def test_first_sequence_released_between_replays(side):
+    """A captured step goes on after a fork's first branch is released."""
+    t, nf4 = side.torch, side.nf4
+    c = Shared(side, 24, 128, 16, 8, 2, [150, 140, 160, 155], [1] * 4, [0, 4], [128],
+               stride_more=SAVED // (2 * 2 * 2 * 128) // 16 + 2)
+    d = device_cache(side, c.c)
+    lens, table = i32(side, c.kv_len), i32(side, c.table)
+    b, g = nf4.KVBatch(lens, table), nf4.KVGroups(i32(side, [128]), i32(side, [0, 4]))
+    q = side.to_dev(c.q).bfloat16()
+    n = nf4.nf4_kv_attention_shared_workspace_bytes(d, b, g, 8)
+    assert n != nf4.nf4_kv_attention_workspace_bytes(d, b, 8), "not taken apart"
+    ws = t.full((n,), 0xFF, dtype=t.uint8, device="cuda")
+    out, z = t.zeros(4, 8 * 128, dtype=t.bfloat16, device="cuda"), t.zeros(4, 8, device="cuda")
+    graph = t.cuda.CUDAGraph()
+    t.cuda.synchronize()
+    with t.cuda.graph(graph):
+        nf4.nf4_kv_attention_shared(d, 0, b, g, q, 1024, 8, 0.09, 0, 0, out, z, ws, n)
+    for s in (None, 0, 1):
+        if s is not None:
+            shorter(c, s, 0)
+            lens[s], table[s] = 0, -1
+        graph.replay()
+        t.cuda.synchronize()
+        c.check(out.float().cpu().numpy().reshape(4, 8, 128), z.cpu().numpy(), 0, 0, 0.09)
