@@ -234,3 +234,29 @@ def test_two_at_once(side):
             assert all(t.equal(a, b) for a, b in zip(want, got))
             for a in got:
                 a.fill_(7.0)
+
+
+def test_two_at_once_each_after_its_fill(side):
+    """As test_two_at_once, with every run's stream behind the fills of what it writes: those are
+    the current stream's, which streams of torch do not wait for by themselves."""
+    t, nf4 = side.torch, side.nf4
+    runs = []
+    for seed, (dim, kvh, seqs) in ((4, (128, 2, 40)), (5, (64, 4, 24))):
+        cache = nf4.KVCache(1, 200, kvh, 16, dim)
+        width = SAVED // ((seqs - 3) * kvh * 2 * dim) // 16 + 2
+        b, g, x = branches_of(side, cache, np.arange(200), seqs, width, 960, seed)
+        need = nf4.nf4_kv_attention_shared_workspace_bytes(cache, b, g, 4 * kvh)
+        want = outputs(side, cache, seqs)
+        ws = t.empty(need, dtype=t.uint8, device="cuda")
+        step(side, cache, b, g, x, ws, want)
+        runs.append((cache, b, g, x, ws, want, outputs(side, cache, seqs), t.cuda.Stream()))
+    t.cuda.synchronize()
+    for _ in range(10):
+        for cache, b, g, x, ws, _, got, stream in runs:
+            for a in got:
+                a.fill_(7.0)
+            stream.wait_stream(t.cuda.current_stream())
+            step(side, cache, b, g, x, ws, got, stream)
+        t.cuda.synchronize()
+        for *_, want, got, _ in runs:
+            assert all(t.equal(a, b) for a, b in zip(want, got))
