@@ -119,8 +119,9 @@ nf4_status check_rotary(const nf4_rotary *r, int64_t head_dim, nf4::KvRotary &ou
 }
 
 // 2^64 times the turns of f radians, |f| <= 2^20, modulo 2^64 and rounded to nearest: half a
-// unit and 2^-32 of one off.  With |f| = m 2^(e - 53) for a whole m under 2^53, and 1 / (2 pi) to
-// 128 bits, what is wanted is m times those bits, shifted right by 117 - e; the lowest 64 are left out.
+// unit and 2^-32 of one off.  With |f| = m 2^(e - 53) for a whole m under 2^53, and
+// 1 / (2 pi) to 128 bits, what is wanted is m times those bits, shifted right by 117 - e;
+// the lowest 64 are left out.
 uint64_t turns_of(double f) {
   constexpr uint64_t kHigh = 0x28BE60DB9391054A, kLow = 0x7F09D5F47D4D3770;
   using Wide = unsigned __int128;

@@ -1275,12 +1275,14 @@ __global__ __launch_bounds__(64 * kTileWaves * G, 2) void tile_kernel(KvCache c,
 // results' error up from 0.0017 to 0.0022.
 //
 // 64 sequences of up to 2000 tokens past 4096 shared ones, 32 heads over 8 of 128 (145 MB):
-// 36.9 us in a trace, 3.9 TB/s; 512 of its 608 workgroups run at a time (registers), the rest
+// 39.8 us in a trace, 3.6 TB/s; 512 of its 608 workgroups run at a time (211 registers, and
+// 57.5 KB of LDS, of which a compute unit has 160), the rest
 // start where short suffixes end, after some 15 us.  Short calls are bound by chains that
-// nothing hides: 8 sequences past 14449, 28 heads over 4 (16 MB), a prefix's workgroup takes
-// 9.6 us, 3.6 of them to its first step (arguments, groups, page ids and positions, trips to
-// memory one after the other), 1.1 for its first keys, 1 for each of four steps, which is
-// 3.9 TB/s by all of them, and 1.9 for the halves' meeting and the store.
+// nothing hides: 8 sequences past 14449, 28 heads over 4 (16 MB, 14.1 us in a trace), a
+// prefix's workgroup takes, by clocks read while weights had one term, 9.6 us, 3.6 of them to
+// its first step (arguments, groups, page ids and positions, trips to memory one after the
+// other), 1.1 for its first keys, 1 for each of four steps, which is 3.9 TB/s by all of them, and
+// 1.9 for the halves' meeting and the store.
 struct SharedPlan {
   uint32_t prefix_grid;
   Divisor groups, prefix_tiles, prefix_splits;
@@ -1620,9 +1622,12 @@ Plan suffix_plan(const KvCache &c, const KvBatch &b, const KvGroups &g, int head
 // run at a time by themselves, of 24 46.0, of 16 48.2, of 12 53.9, of 32 46.7 against 44.3).
 // Suffixes end early where they are short, and count by their length (19 sequences of five
 // rows, 28 heads over 4, whose suffixes are tiles of 64 rows, over 12000 and up to 100 tokens
-// 41.0, counted whole 44.7; over 6498 and up to 1331 41.9, counted whole 35.5).  Beside those, prefixes of 128 values take up to
-// 32 steps (48 of five rows over 12000, three groups, 28 heads over 4, 69.4, with 24 73.2), of
-// 64 values 24 (32 heads over 4, 50.0, with 32 55.0).
+// 41.0, counted whole 44.7; over 6498 and up to 1331 41.9, counted whole 35.5).  Beside
+// those, prefixes of 128 values take up to 32 steps (48 of five rows over 12000, three
+// groups, 28 heads over 4, 69.4, with 24 73.2), of 64 values 24 (32 heads over 4, 50.0,
+// with 32 55.0).  All of these with weights of one bf16 term in tiles of 64 rows; two take 2 to
+// 8 % longer.  Every group counts as large as the largest: where they differ, some of the
+// workgroups have nothing to do, and the others' parts are that much longer.
 // Tiles of 16 rows: some 200 workgroups, of 16 to 40 steps of 32 keys (8 sequences over 20000,
 // 16 heads over 8, in parts of 24 17.7, of 16 19.7, of 40 18.9; 8 over 32000, 8 heads, of 40
 // 20.3, of 16 23.0, of 64 22.9; 16 over 3000, 16 heads over 8, of 16 13.9, of 24 15.4), and

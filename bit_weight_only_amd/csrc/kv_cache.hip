@@ -90,9 +90,9 @@ struct ReadRows {
 // The reverse of append_kernel, by the same division of the work: a wave per
 // (sequence, block that its rows touch, head, keys or values).  Rows that have no
 // place get zeros.  Memory bound: 6 sequences of up to 14449 tokens, 8 heads of 128, to bf16
-// (291 MB): 53.9 us in a trace = 5.4 TB/s; a chunk of 113 tokens, 4 heads, to fp32 3.8 us,
-// of which 1.6 an empty launch and the rest three trips to memory one after the
-// other (place and length, page id, codes).
+// (291 MB), other ones in every call: 62.6 us = 4.6 TB/s; a chunk of 113 tokens, 4 heads, to
+// fp32 3.8 us in a trace, of which 1.6 an empty launch and the rest three trips to memory one
+// after the other (place and length, page id, codes).
 template <bool F32, int D>
 __global__ __launch_bounds__(256) void read_kernel(KvCache c, int64_t layer, KvBatch b, ReadRows y,
                                                    int64_t blocks_per_seq) {

@@ -414,8 +414,11 @@ struct RotateArgs {
 // values on their way while these are worked on.  The 16 rows' sines and cosines are
 // worked out once for all of the workgroup's heads, some 40 instructions of 64 bits each: by
 // every head for itself they would take longer than the rows' way through memory.
-// Memory bound: 14449 rows of 32 heads of 128, bf16 to bf16, normed (237 MB): 39.9 us in a
-// trace = 5.9 TB/s.  One row of 28 heads: 3.7 us, 1.6 of them an empty launch.
+// Memory bound, other rows in every call: 14449 rows of 32 heads of 128, normed, bf16 to bf16
+// (237 MB) 45.4 us = 5.2 TB/s, the rate of a large copy; bf16 to fp32 and back (355 MB)
+// 76 us = 4.7; fp32 to fp32 (473 MB) 103 us = 4.6, 0.9 of that rate: where fp32 leaves, 52 KB of
+// LDS keep it to three workgroups per compute unit.  One row of 28 heads: 3.7 us in a trace, 1.6
+// of them an empty launch.
 template <bool F32, bool Y32, int D>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(KvRotary rot, RotateArgs a,
                                                           uint32_t slices) {
@@ -588,11 +591,15 @@ __device__ inline void append_block(const AppendArgs &x, int64_t seq, uint32_t b
 // q_slices workgroups that turn queries and kv_slices that turn keys and write keys and
 // values into their page.  One launch, so that a decoded token waits for one chain of trips
 // to memory (place and length, then rows beside the page id, then the old scale beside
-// the old codes): 5.9 us in a trace for one token of 28 heads over 4, 7.2 for 64 of 32 over
+// the old codes): 5.8 us in a trace for one token of 28 heads over 4, 7.1 for 64 of 32 over
 // 8, an empty launch 1.6.  Long prompts are memory bound: 14449 fp32 rows of 28 heads over 4 of
-// 128 (385 MB) 78.4 us = 4.9 TB/s.  In between the vector unit takes part: 5 chunks of up to
-// 701 rows, 32 heads over 8 of 64, normed, 50 values turned (40 MB) 14.8 us, of which some 4
-// go if nothing turns.
+// 128 (385 MB) 78.3 us back to back = 4.9 TB/s (83.4 alone in a trace).  In between the vector
+// unit takes part, and LDS, where lanes read the sines' table 64 bytes apart in halves of
+// bf16 (32 in pairs): 5 chunks of up to 701 rows, 32 heads over 8 of 64, normed, 50 values
+// turned (40 MB) 14.8 us back to back, of which some 4 go if nothing turns; conflicts of
+// LDS banks are 6500 cycles of a compute unit, up to 2.7 us.
+// Every sequence has as many workgroups as the longest chunk: 63 single tokens beside a chunk
+// of 1024 rows, 28 fp32 heads over 4, 33.6 us in a graph, beside one of 113 14.7.
 template <bool F32, int D>
 __global__ __launch_bounds__(kThreads) void append_rotated_kernel(AppendArgs) {
   __shared__ union {
