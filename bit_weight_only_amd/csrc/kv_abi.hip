@@ -103,7 +103,7 @@ nf4_status check_rows(const void *p, int64_t stride, int64_t width, nf4_kv_type 
 // The norms' eps: what is divided by stays a normal float.
 bool eps_ok(float eps) { return isfinite(eps) && eps >= 0x1p-100f; }
 
-// A gain that sines and cosines times it, which kernels hold as two fp32 terms, stay in range with.
+// Gains whose products with sines and cosines, held as two fp32 terms, stay in fp32's range.
 bool gain_ok(double gain) { return gain == 0.0 || (fabs(gain) >= 0x1p-100 && fabs(gain) <= 0x1p100); }
 
 nf4_status check_rotary(const nf4_rotary *r, int64_t head_dim, nf4::KvRotary &out) {
